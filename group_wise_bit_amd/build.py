@@ -26,9 +26,13 @@ PEAKS_PATH = os.path.join(PKG_DIR, "libqlin_peaks.so")
 PEAKS_SOURCE = os.path.join(CSRC, "peaks.hip")
 API_SOURCE = os.path.join(CSRC, "qlin_api.hip")
 INST_SOURCE = os.path.join(CSRC, "inst.hip")
+# row-wise products (include/qlin_rows.h): entry points, and one object per width
+ROWS_API_SOURCE = os.path.join(CSRC, "rows", "rows_api.hip")
+ROWS_INST_SOURCE = os.path.join(CSRC, "rows", "rows_inst.hip")
 HEADERS = [os.path.join(CSRC, f) for f in ("device_common.h", "codes.h", "kernels.h", "plan.h",
-                                           "launch_impl.h")] + [
-    os.path.join(ROOT, "include", "qlin.h")]
+                                           "launch_impl.h", "checks.h", "rows/rows.h", "rows/group.h",
+                                           "rows/route.h", "rows/rows_plan.h")] + [
+    os.path.join(ROOT, "include", f) for f in ("qlin.h", "qlin_rows.h")]
 
 GEMV_BITS = (2, 3, 4, 5, 6, 7, 8, 16)   # part 0: GEMV and row gather (16: fp16 control)
 GEMM_BITS = (2, 3, 4, 5, 6, 7, 8)       # part 1: GEMM
@@ -66,6 +70,9 @@ def _units():
     for b in QUANT_BITS:
         units.append((f"quant_b{b}", INST_SOURCE,
                       [f"-DQLIN_INST_BITS={b}", "-DQLIN_INST_PART=2", *QUANT_FLAGS]))
+    units.append(("rows_api", ROWS_API_SOURCE, []))
+    for b in GEMM_BITS:
+        units.append((f"rows_b{b}", ROWS_INST_SOURCE, [f"-DQLIN_INST_BITS={b}"]))
     return units
 
 

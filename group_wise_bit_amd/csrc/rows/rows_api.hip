@@ -1,0 +1,325 @@
+// Entry points of qlin_rows.h: host checks, workspace layout, launches.
+#include <hip/hip_runtime.h>
+
+#include "../../../include/qlin_rows.h"
+#include "../checks.h"
+#include "group.h"
+#include "route.h"
+#include "rows_plan.h"
+
+using namespace qlin;
+
+namespace {
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+constexpr int64_t kMaxPairs = 1 << 26;
+
+int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
+
+// The workspace of one call, cut into 256-byte aligned parts behind the
+// counters that the other entry points keep at its start.
+struct Arena {
+  char* base;
+  int64_t at = kCounterBytes;
+  template <typename T>
+  T* take(int64_t count) {
+    T* p = reinterpret_cast<T*>(base + at);
+    at += align256(count * (int64_t)sizeof(T));
+    return p;
+  }
+};
+
+// Row tiles of `height` rows that `count` rows over `buckets` buckets can need.
+int64_t tile_bound(int64_t count, int buckets, int height) {
+  return count / height + (count < buckets ? count : buckets);
+}
+
+RowPlan take_plan(Arena& ar, int64_t count, int buckets, int height) {
+  RowPlan p;
+  p.offs = ar.take<int32_t>(buckets + 2);
+  p.order = ar.take<int32_t>(count);
+  p.tiles = ar.take<int32_t>(2 * tile_bound(count, buckets, height));
+  p.ntiles = ar.take<int32_t>(1);
+  return p;
+}
+
+int64_t code_words(const qlin_weight* w) { return packed_bytes(w->n, w->k, w->bits) / 4; }
+
+void set_weight(RowsArgs& a, int i, const qlin_weight* w) {
+  a.codes[i] = static_cast<const uint32_t*>(w->data);
+  a.scale[i] = w->scale;
+  a.zero[i] = w->zero;
+  a.code_step = code_words(w);
+  a.meta_step = meta_entries(w->n, w->k, w->group);
+  a.n = w->n;
+  a.kb = w->k / kBlock;
+  a.G = w->group == w->k ? 1 : a.kb;
+}
+
+void run_rows(const RowsArgs& a, int bits, int mode, RowsCfg c, hipStream_t st) {
+  switch (bits) {
+    case 2: launch_rows<2>(a, mode, c, st); break;
+    case 3: launch_rows<3>(a, mode, c, st); break;
+    case 4: launch_rows<4>(a, mode, c, st); break;
+    case 5: launch_rows<5>(a, mode, c, st); break;
+    case 6: launch_rows<6>(a, mode, c, st); break;
+    case 7: launch_rows<7>(a, mode, c, st); break;
+    default: launch_rows<8>(a, mode, c, st); break;
+  }
+}
+
+bool stack_overlaps(const qlin_weight* w, int64_t experts, Range r) {
+  const int64_t me = meta_entries(w->n, w->k, w->group) * experts;
+  return overlaps(r, range_of(w->data, packed_bytes(w->n, w->k, w->bits) * experts)) ||
+         overlaps(r, range_of(w->scale, me * 2)) || overlaps(r, range_of(w->zero, me));
+}
+
+// ---------------------------------------------------------------- experts --
+struct MoePlan {
+  int64_t pairs;
+  RowsCfg cfg;
+  RowPlan rows;
+  uint16_t* h;
+  float* d;
+  int64_t bytes;
+};
+
+MoePlan moe_plan(int inner, int model, int experts, int m, int top_k, void* ws) {
+  MoePlan p;
+  p.pairs = (int64_t)m * top_k;
+  p.cfg.height = 32;
+  p.cfg.tiles = (int)tile_bound(p.pairs, experts, p.cfg.height);
+  Arena ar{static_cast<char*>(ws)};
+  p.rows = take_plan(ar, p.pairs, experts, p.cfg.height);
+  p.h = ar.take<uint16_t>(p.pairs * inner);
+  p.d = ar.take<float>(p.pairs * model);
+  p.bytes = ar.at;
+  return p;
+}
+
+qlin_status check_moe(const qlin_weight* gate, const qlin_weight* up, const qlin_weight* down,
+                      int32_t experts, int32_t m, int32_t top_k) {
+  const qlin_weight* w[3] = {gate, up, down};
+  for (const qlin_weight* x : w) {
+    const qlin_status st = check_weight(x, false, false);
+    if (st != QLIN_OK) return st;
+  }
+  if (up->n != gate->n || up->k != gate->k || down->n != gate->k || down->k != gate->n)
+    return QLIN_ERR_SHAPE;
+  if (up->bits != gate->bits || up->group != gate->group) return QLIN_ERR_FORMAT;
+  if (experts < 1 || experts > kMaxExperts || top_k < 1 || top_k > kMaxTopK || m < 0 ||
+      m > kMaxM || (int64_t)m * top_k > kMaxPairs)
+    return QLIN_ERR_SHAPE;
+  return QLIN_OK;
+}
+
+// --------------------------------------------------------------- adapters --
+struct LoraPlan {
+  RowsCfg cfg;
+  uint16_t* t;
+  float* tscale;
+  int rp;
+  int64_t bytes;
+};
+
+LoraPlan lora_plan(const qlin_adapters* ad, int m, void* ws) {
+  LoraPlan p;
+  p.cfg.height = 32;
+  p.cfg.tiles = (m + 31) / 32;
+  p.rp = (ad->rank + 15) / 16 * 16;
+  Arena ar{static_cast<char*>(ws)};
+  p.t = ar.take<uint16_t>((int64_t)m * 2 * p.rp);
+  p.tscale = ar.take<float>(m);
+  p.bytes = ar.at;
+  return p;
+}
+
+qlin_status check_lora(const qlin_weight* w, const qlin_adapters* ad, int32_t m) {
+  const qlin_status st = check_weight(w, false, false);
+  if (st != QLIN_OK) return st;
+  if (ad == nullptr) return QLIN_ERR_NULL;
+  if (ad->slots < 1 || ad->slots > kMaxExperts || ad->rank < 8 || ad->rank > 128 ||
+      ad->rank % 8 != 0 || m < 0 || m > kMaxM)
+    return QLIN_ERR_SHAPE;
+  return QLIN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+qlin_status qlin_route(const qlin_router* r, const float* logits, int32_t m, int64_t ld,
+                       int32_t* ids, float* weights, hipStream_t stream) {
+  if (r == nullptr) return QLIN_ERR_NULL;
+  if (r->experts < 1 || r->experts > kMaxExperts || r->top_k < 1 || r->top_k > kMaxTopK ||
+      r->top_k > r->experts || r->groups < 1 || r->groups > 64 || r->experts % r->groups != 0 ||
+      r->top_groups < 1 || r->top_groups > r->groups || r->group_top < 1 || r->group_top > 2 ||
+      r->top_groups * (r->experts / r->groups) < r->top_k)
+    return QLIN_ERR_SHAPE;
+  if ((r->score != QLIN_SCORE_SOFTMAX && r->score != QLIN_SCORE_SIGMOID) ||
+      (r->renormalize != 0 && r->renormalize != 1))
+    return QLIN_ERR_FORMAT;
+  if (m < 0 || m > kMaxM || ld < r->experts) return QLIN_ERR_SHAPE;
+  if (m == 0) return QLIN_OK;
+  if (logits == nullptr || ids == nullptr || weights == nullptr) return QLIN_ERR_NULL;
+  if (!aligned4(logits) || !aligned4(ids) || !aligned4(weights) || !aligned4(r->bias))
+    return QLIN_ERR_ALIGN;
+  const Range in[2] = {range_of(logits, ((int64_t)(m - 1) * ld + r->experts) * 4),
+                       range_of(r->bias, r->bias != nullptr ? (int64_t)r->experts * 4 : 0)};
+  const Range out[2] = {range_of(ids, (int64_t)m * r->top_k * 4),
+                        range_of(weights, (int64_t)m * r->top_k * 4)};
+  for (const Range& o : out)
+    for (const Range& i : in)
+      if (overlaps(o, i)) return QLIN_ERR_ALIAS;
+  if (overlaps(out[0], out[1])) return QLIN_ERR_ALIAS;
+  const qlin_status st = check_device();
+  if (st != QLIN_OK) return st;
+  RouteArgs a{logits, r->bias, ld, ids, weights, m, r->experts, r->top_k, r->groups,
+              r->top_groups, r->group_top, r->scale, r->score == QLIN_SCORE_SIGMOID,
+              r->renormalize != 0};
+  const dim3 grid((m + kRouteWaves - 1) / kRouteWaves), block(kRouteWaves * 64);
+  if (r->experts <= 64) hipLaunchKernelGGL((k_route<1>), grid, block, 0, stream, a);
+  else if (r->experts <= 128) hipLaunchKernelGGL((k_route<2>), grid, block, 0, stream, a);
+  else if (r->experts <= 256) hipLaunchKernelGGL((k_route<4>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((k_route<8>), grid, block, 0, stream, a);
+  return hip_status(hipGetLastError());
+}
+
+int64_t qlin_moe_mlp_workspace_bytes(const qlin_weight* gate, const qlin_weight* down,
+                                     int32_t experts, int32_t m, int32_t top_k) {
+  if (check_moe(gate, gate, down, experts, m, top_k) != QLIN_OK || m == 0) return 0;
+  return moe_plan(gate->n, gate->k, experts, m, top_k, nullptr).bytes;
+}
+
+qlin_status qlin_moe_mlp(const qlin_weight* gate, const qlin_weight* up, const qlin_weight* down,
+                         int32_t experts, const uint16_t* X, int32_t m, int64_t ld_x,
+                         const int32_t* ids, const float* weights, int32_t top_k, float* Y,
+                         uint16_t* Y16, int64_t ld_y, void* workspace, int64_t workspace_bytes,
+                         hipStream_t stream) {
+  qlin_status st = check_moe(gate, up, down, experts, m, top_k);
+  if (st != QLIN_OK) return st;
+  if (ld_x < gate->k || ld_y < down->n) return QLIN_ERR_SHAPE;
+  if (ld_x % 8 != 0) return QLIN_ERR_ALIGN;
+  if (m == 0) return QLIN_OK;
+  if (X == nullptr || ids == nullptr || weights == nullptr || (Y == nullptr && Y16 == nullptr))
+    return QLIN_ERR_NULL;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(Y16) || !aligned4(ids) || !aligned4(weights) ||
+      !aligned16(workspace))
+    return QLIN_ERR_ALIGN;
+  const int inner = gate->n, model = gate->k;
+  const MoePlan p = moe_plan(inner, model, experts, m, top_k, workspace);
+  if (!rows_fits(inner, p.cfg) || !rows_fits(model, p.cfg)) return QLIN_ERR_SHAPE;
+  if (workspace == nullptr || workspace_bytes < p.bytes) return QLIN_ERR_WORKSPACE;
+  const int64_t span = (int64_t)(m - 1) * ld_y + model;
+  const Range out[3] = {range_of(workspace, workspace_bytes),
+                        range_of(Y, Y != nullptr ? span * 4 : 0),
+                        range_of(Y16, Y16 != nullptr ? span * 2 : 0)};
+  const Range in[3] = {range_of(X, ((int64_t)(m - 1) * ld_x + model) * 2),
+                       range_of(ids, p.pairs * 4), range_of(weights, p.pairs * 4)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& r : in)
+      if (overlaps(out[i], r)) return QLIN_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i], out[j])) return QLIN_ERR_ALIAS;
+    if (stack_overlaps(gate, experts, out[i]) || stack_overlaps(up, experts, out[i]) ||
+        stack_overlaps(down, experts, out[i]))
+      return QLIN_ERR_ALIAS;
+  }
+  st = check_device();
+  if (st != QLIN_OK) return st;
+  hipLaunchKernelGGL(k_rows_plan, dim3(1), dim3(kPlanWaves * 64), 0, stream, ids, (int)p.pairs,
+                     experts, p.cfg.height, p.rows);
+  RowsArgs a{};
+  set_weight(a, 0, gate);
+  set_weight(a, 1, up);
+  a.X = X;
+  a.ldx = ld_x;
+  a.m = m;
+  a.top_k = top_k;
+  a.plan = p.rows;
+  a.y16 = p.h;
+  a.ldy = inner;
+  run_rows(a, gate->bits, kSwiglu, p.cfg, stream);
+  RowsArgs b{};
+  set_weight(b, 0, down);
+  b.X = p.h;
+  b.ldx = inner;
+  b.m = m;
+  b.top_k = top_k;
+  b.plan = p.rows;
+  b.weights = weights;
+  b.y = p.d;
+  b.ldy = model;
+  run_rows(b, down->bits, kDown, p.cfg, stream);
+  const int64_t groups = ((int64_t)m * (model / 4) + 255) / 256;
+  hipLaunchKernelGGL(k_rows_combine, dim3((unsigned)(groups < 65536 ? groups : 65536)), dim3(256), 0, stream,
+                     p.d, ids, m, top_k, experts, model, Y, Y16, ld_y);
+  return hip_status(hipGetLastError());
+}
+
+int64_t qlin_gemm_lora_workspace_bytes(const qlin_weight* w, const qlin_adapters* ad, int32_t m) {
+  if (check_lora(w, ad, m) != QLIN_OK || m == 0) return 0;
+  return lora_plan(ad, m, nullptr).bytes;
+}
+
+qlin_status qlin_gemm_lora(const qlin_weight* w, const qlin_adapters* ad, const uint16_t* X,
+                           int32_t m, int64_t ld_x, const int32_t* ids, float* Y, uint16_t* Y16,
+                           int64_t ld_y, void* workspace, int64_t workspace_bytes,
+                           hipStream_t stream) {
+  qlin_status st = check_lora(w, ad, m);
+  if (st != QLIN_OK) return st;
+  if (ld_x < w->k || ld_y < w->n) return QLIN_ERR_SHAPE;
+  if (ld_x % 8 != 0) return QLIN_ERR_ALIGN;
+  if (m == 0) return QLIN_OK;
+  if (X == nullptr || ids == nullptr || ad->a == nullptr || ad->b == nullptr ||
+      (Y == nullptr && Y16 == nullptr))
+    return QLIN_ERR_NULL;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(Y16) || !aligned16(ad->a) ||
+      !aligned16(ad->b) || !aligned4(ad->scale) || !aligned4(ids) || !aligned16(workspace))
+    return QLIN_ERR_ALIGN;
+  const LoraPlan p = lora_plan(ad, m, workspace);
+  if (!rows_fits(w->n, p.cfg)) return QLIN_ERR_SHAPE;
+  if (workspace == nullptr || workspace_bytes < p.bytes) return QLIN_ERR_WORKSPACE;
+  const int64_t span = (int64_t)(m - 1) * ld_y + w->n;
+  const int64_t sr = (int64_t)ad->slots * ad->rank;
+  const Range out[3] = {range_of(workspace, workspace_bytes),
+                        range_of(Y, Y != nullptr ? span * 4 : 0),
+                        range_of(Y16, Y16 != nullptr ? span * 2 : 0)};
+  const Range in[5] = {range_of(X, ((int64_t)(m - 1) * ld_x + w->k) * 2),
+                       range_of(ids, (int64_t)m * 4), range_of(ad->a, sr * w->k * 2),
+                       range_of(ad->b, sr * w->n * 2),
+                       range_of(ad->scale, ad->scale != nullptr ? (int64_t)ad->slots * 4 : 0)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& r : in)
+      if (overlaps(out[i], r)) return QLIN_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i], out[j])) return QLIN_ERR_ALIAS;
+    if (output_overlaps_weight(w, out[i])) return QLIN_ERR_ALIAS;
+  }
+  st = check_device();
+  if (st != QLIN_OK) return st;
+  const ShrinkArgs s{X, ld_x, m, w->k, ad->slots, ad->rank, p.rp, ids, ad->a, ad->scale,
+                     p.t, p.tscale};
+  hipLaunchKernelGGL(k_lora_shrink_row, dim3(m), dim3(256), 0, stream, s);
+  RowsArgs a{};
+  set_weight(a, 0, w);
+  a.X = X;
+  a.ldx = ld_x;
+  a.m = m;
+  a.top_k = 1;
+  a.y = Y;
+  a.y16 = Y16;
+  a.ldy = ld_y;
+  a.ids = ids;
+  a.t = p.t;
+  a.tscale = p.tscale;
+  a.b = ad->b;
+  a.slots = ad->slots;
+  a.rank = ad->rank;
+  a.rp = p.rp;
+  run_rows(a, w->bits, kLora, p.cfg, stream);
+  return hip_status(hipGetLastError());
+}
+
+}  // extern "C"

@@ -38,6 +38,11 @@ EXPORTS = (
 # include/qlin_tune.h (launch-shape sweeps and tests only)
 TUNE_EXPORTS = ("qlin_set_launch_override",)
 TUNE_FAMILIES = {"gemv": 0, "gemm": 1}
+# include/qlin_rows.h (products whose weights differ from row to row)
+ROWS_EXPORTS = (
+    "qlin_route", "qlin_moe_mlp_workspace_bytes", "qlin_moe_mlp",
+    "qlin_gemm_lora_workspace_bytes", "qlin_gemm_lora",
+)
 
 
 class QlinError(RuntimeError):
@@ -64,6 +69,21 @@ class QlinQuantJobC(ctypes.Structure):
         ("w16", ctypes.c_void_p), ("ld_w", ctypes.c_int64), ("n", ctypes.c_int32),
         ("k", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
         ("zero", ctypes.c_void_p),
+    ]
+
+
+class QlinRouterC(ctypes.Structure):
+    _fields_ = [
+        ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+        ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("bias", ctypes.c_void_p),
+    ]
+
+
+class QlinAdaptersC(ctypes.Structure):
+    _fields_ = [
+        ("slots", ctypes.c_int32), ("rank", ctypes.c_int32), ("a", ctypes.c_void_p),
+        ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
     ]
 
 
@@ -124,6 +144,18 @@ def _lib() -> ctypes.CDLL:
         lib.qlin_gemv_noalloc.restype = ctypes.c_int
         lib.qlin_set_launch_override.argtypes = [i32, ctypes.POINTER(i32)]
         lib.qlin_set_launch_override.restype = ctypes.c_int
+        rp, ap = ctypes.POINTER(QlinRouterC), ctypes.POINTER(QlinAdaptersC)
+        lib.qlin_route.argtypes = [rp, vp, i32, i64, vp, vp, vp]
+        lib.qlin_route.restype = ctypes.c_int
+        lib.qlin_moe_mlp_workspace_bytes.argtypes = [wp, wp, i32, i32, i32]
+        lib.qlin_moe_mlp_workspace_bytes.restype = i64
+        lib.qlin_moe_mlp.argtypes = [wp, wp, wp, i32, vp, i32, i64, vp, vp, i32, vp, vp, i64, vp,
+                                     i64, vp]
+        lib.qlin_moe_mlp.restype = ctypes.c_int
+        lib.qlin_gemm_lora_workspace_bytes.argtypes = [wp, ap, i32]
+        lib.qlin_gemm_lora_workspace_bytes.restype = i64
+        lib.qlin_gemm_lora.argtypes = [wp, ap, vp, i32, i64, vp, vp, vp, i64, vp, i64, vp]
+        lib.qlin_gemm_lora.restype = ctypes.c_int
         _LIB = lib
     return _LIB
 
@@ -488,3 +520,271 @@ def gemm_swiglu(gate: QWeight, up: QWeight, X: torch.Tensor,
                                  _ptr(H), _ptr(H16), ld, _ptr(ws), wsb, _stream())
     _check(st, "qlin_gemm_swiglu")
     return H, H16
+
+
+# ---------------------------------------- products whose weights differ by row
+# (include/qlin_rows.h).  Every tensor of a call is on one device, and the
+# kernels run on that device's current stream, whichever device is current.
+
+def _same_device(dev: torch.device, named) -> None:
+    for name, t in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the inputs on {dev}")
+
+
+class _on_device:
+    """The tensors' device made current for a call (a no-op where it is)."""
+
+    def __init__(self, dev: torch.device):
+        if dev.type != "cuda":
+            raise ValueError(f"the tensors must be on a GPU, not on {dev}")
+        self.guard = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _rows_workspace(ws, need: int, dev: torch.device) -> Optional[torch.Tensor]:
+    """The workspace of a row-wise call: the caller's, or the device and
+    stream's own.  Under stream capture a buffer of the graph's own memory:
+    one that a later, larger call may replace must not be recorded."""
+    if not isinstance(ws, str):
+        if ws is not None and ws.device != dev:
+            raise ValueError(f"ws is on {ws.device}, the inputs on {dev}")
+        if ws is not None and not ws.is_contiguous():
+            raise ValueError("ws must be contiguous")
+        return ws
+    if need <= 0:
+        return None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace(need, dev)
+
+
+def _need_rows_x(X: torch.Tensor, k: int) -> None:
+    if not isinstance(X, torch.Tensor) or X.dtype != torch.float16 or X.dim() != 2 or \
+            X.shape[1] != k or (X.shape[0] > 0 and X.stride(1) != 1):
+        raise TypeError(f"X must be a float16 [m, {k}] tensor with contiguous rows")
+
+
+def _row_pitch(t: torch.Tensor) -> int:
+    """Elements from one row to the next (one row has no next: its own length)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _need_flat(t: torch.Tensor, dtype: torch.dtype, shape: Tuple[int, ...], name: str) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape or \
+            not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+
+
+def _row_outputs(m: int, n: int, dev, Y, Y16, want_y: bool, want_y16: bool):
+    """fp32 and fp16 [m, n] outputs of a row-wise product and their common row stride."""
+    if Y is None and want_y:
+        Y = torch.empty(m, n, dtype=torch.float32, device=dev)
+    if Y16 is None and want_y16:
+        Y16 = torch.empty(m, n, dtype=torch.float16, device=dev)
+    outs = []
+    for t, dtype, name in ((Y, torch.float32, "Y"), (Y16, torch.float16, "Y16")):
+        if t is not None:
+            _need_out(t, dtype, dev, m, n, name) if m else None
+            outs.append(t)
+    if not outs:
+        raise ValueError("one of Y and Y16 must be wanted")
+    ld = _row_pitch(outs[0])
+    if m > 1 and any(t.stride(0) != ld for t in outs):
+        raise ValueError("Y and Y16 must share one row stride")
+    if m <= 1:
+        ld = n
+    return Y, Y16, ld
+
+
+@dataclass
+class Router:
+    """How route() turns logits into experts (qlin_router in qlin_rows.h)."""
+    experts: int
+    top_k: int
+    score: str = "softmax"                # or "sigmoid"
+    bias: Optional[torch.Tensor] = None   # fp32 [experts]: added for the choice only
+    groups: int = 1
+    top_groups: Optional[int] = None      # None: all groups
+    group_top: int = 1
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def c_struct(self) -> QlinRouterC:
+        if self.score not in ("softmax", "sigmoid"):
+            raise ValueError("score must be 'softmax' or 'sigmoid'")
+        if self.bias is not None:
+            _need_flat(self.bias, torch.float32, (self.experts,), "bias")
+        return QlinRouterC(self.experts, self.top_k, int(self.score == "sigmoid"), self.groups,
+                           self.groups if self.top_groups is None else self.top_groups,
+                           self.group_top, int(bool(self.renormalize)), self.scale,
+                           _ptr(self.bias))
+
+
+def route(router: Router, logits: torch.Tensor, ids: Optional[torch.Tensor] = None,
+          weights: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """qlin_route: (ids int32, weights fp32), both [m, top_k], of fp32 logits [m, experts]."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype != torch.float32 or \
+            logits.dim() != 2 or logits.shape[1] != router.experts or \
+            (logits.shape[0] > 0 and logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise TypeError(f"logits must be a float32 [m, {router.experts}] tensor with contiguous rows")
+    m, dev = logits.shape[0], logits.device
+    c = router.c_struct()
+    if router.top_k < 1:
+        raise ValueError("top_k must be at least 1")
+    if ids is None:
+        ids = torch.empty(m, router.top_k, dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty(m, router.top_k, dtype=torch.float32, device=dev)
+    _need_flat(ids, torch.int32, (m, router.top_k), "ids")
+    _need_flat(weights, torch.float32, (m, router.top_k), "weights")
+    _same_device(dev, (("bias", router.bias), ("ids", ids), ("weights", weights)))
+    with _on_device(dev):
+        st = _lib().qlin_route(ctypes.byref(c), logits.data_ptr(), m, _row_pitch(logits),
+                               ids.data_ptr(), weights.data_ptr(), _stream())
+    _check(st, "qlin_route")
+    return ids, weights
+
+
+@dataclass
+class QExperts:
+    """A stack of packed weights of one shape, expert after expert (the layout
+    qlin_moe_mlp takes): each tensor holds `count` times one QWeight's."""
+    count: int
+    n: int
+    k: int
+    bits: int
+    group: int
+    data: torch.Tensor
+    scale: torch.Tensor
+    zero: torch.Tensor
+
+    def c_struct(self) -> QlinWeightC:
+        words = self.count * (packed_bytes(self.n, self.k, self.bits) // 4)
+        entries = self.count * meta_entries(self.n, self.k, self.group)
+        for t, dtype, size, name in ((self.data, torch.int32, words, "data"),
+                                     (self.scale, torch.float16, entries, "scale"),
+                                     (self.zero, torch.uint8, entries, "zero")):
+            if t.dtype != dtype or not t.is_contiguous() or t.numel() < size or \
+                    t.device != self.data.device:
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {size} "
+                                 "elements on the codes' device")
+        return QlinWeightC(self.n, self.k, self.bits, self.group, FMT_PACKED, 0,
+                           self.data.data_ptr(), 0, self.scale.data_ptr(), self.zero.data_ptr())
+
+    def expert(self, e: int) -> QWeight:
+        """Expert e as a QWeight over the same memory."""
+        if not 0 <= e < self.count:
+            raise IndexError(f"expert {e} of {self.count}")
+        w, s = packed_bytes(self.n, self.k, self.bits) // 4, meta_entries(self.n, self.k, self.group)
+        return QWeight(self.n, self.k, self.bits, self.group, FMT_PACKED,
+                       self.data.reshape(-1)[e * w:(e + 1) * w],
+                       self.scale.reshape(-1)[e * s:(e + 1) * s],
+                       self.zero.reshape(-1)[e * s:(e + 1) * s])
+
+
+def quantize_experts(w16: torch.Tensor, bits: int, group) -> QExperts:
+    """qlin_quantize_batch of fp16 masters [count, n, k] into one stack."""
+    if w16.dim() != 3 or w16.shape[0] < 1:
+        raise TypeError("w16 must be a float16 [count, n, k] tensor")
+    count, n, k = w16.shape
+    g = k if group in ("k", "K") else int(group)
+    words, entries = packed_bytes(n, k, bits) // 4, meta_entries(n, k, g)
+    if not words or not entries:
+        raise ValueError(f"no packed layout for n = {n}, k = {k}, bits = {bits}, group = {group}")
+    dev = w16.device
+    q = QExperts(count, n, k, bits, g, torch.empty(count * words, dtype=torch.int32, device=dev),
+                 torch.empty(count * entries, dtype=torch.float16, device=dev),
+                 torch.empty(count * entries, dtype=torch.uint8, device=dev))
+    with _on_device(dev):
+        quantize_batch([w16[e] for e in range(count)], bits, "K" if g != 64 else 64,
+                       outs=[q.expert(e) for e in range(count)])
+    return q
+
+
+def moe_mlp(gate: QExperts, up: QExperts, down: QExperts, X: torch.Tensor, ids: torch.Tensor,
+            weights: torch.Tensor, Y: Optional[torch.Tensor] = None,
+            Y16: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = "auto",
+            want_y: bool = True, want_y16: bool = True
+            ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """qlin_moe_mlp: Y[i] = sum_j weights[i, j] * down_e(silu(gate_e x_i) * up_e x_i), e =
+    ids[i, j]; fp32 and / or fp16 [m, n].  ids and weights [m, top_k] as route() gives them."""
+    _need_rows_x(X, gate.k)
+    m, dev = X.shape[0], X.device
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise TypeError("ids must be a contiguous torch.int32 [m, top_k] tensor")
+    top_k = ids.shape[1]
+    _need_flat(ids, torch.int32, (m, top_k), "ids")
+    _need_flat(weights, torch.float32, (m, top_k), "weights")
+    if not gate.count == up.count == down.count:
+        raise ValueError("gate, up and down must hold the same number of experts")
+    _same_device(dev, (("gate", gate.data), ("up", up.data), ("down", down.data), ("ids", ids),
+                       ("weights", weights)))
+    Y, Y16, ld = _row_outputs(m, down.n, dev, Y, Y16, want_y, want_y16)
+    g, u, d = gate.c_struct(), up.c_struct(), down.c_struct()
+    lib = _lib()
+    with _on_device(dev):
+        if isinstance(ws, str):
+            need = lib.qlin_moe_mlp_workspace_bytes(ctypes.byref(g), ctypes.byref(d), gate.count,
+                                                    m, top_k)
+        else:
+            need = 0
+        ws = _rows_workspace(ws, need, dev)
+        st = lib.qlin_moe_mlp(ctypes.byref(g), ctypes.byref(u), ctypes.byref(d), gate.count,
+                              X.data_ptr(), m, _row_pitch(X), ids.data_ptr(), weights.data_ptr(),
+                              top_k, _ptr(Y), _ptr(Y16), ld, _ptr(ws),
+                              0 if ws is None else ws.numel() * ws.element_size(), _stream())
+    _check(st, "qlin_moe_mlp")
+    return Y, Y16
+
+
+@dataclass
+class Adapters:
+    """A pool of low-rank adapters of one projection: a fp16 [slots, rank, k],
+    b fp16 [slots, n, rank], scale fp32 [slots] or None (all 1)."""
+    a: torch.Tensor
+    b: torch.Tensor
+    scale: Optional[torch.Tensor] = None
+
+    def c_struct(self, w: "QWeight") -> QlinAdaptersC:
+        if self.a.dim() != 3:
+            raise TypeError("a must be a contiguous torch.float16 [slots, rank, k] tensor")
+        slots, rank = self.a.shape[0], self.a.shape[1]
+        _need_flat(self.a, torch.float16, (slots, rank, w.k), "a")
+        _need_flat(self.b, torch.float16, (slots, w.n, rank), "b")
+        if self.scale is not None:
+            _need_flat(self.scale, torch.float32, (slots,), "scale")
+        return QlinAdaptersC(slots, rank, self.a.data_ptr(), self.b.data_ptr(), _ptr(self.scale))
+
+
+def gemm_lora(w: QWeight, X: torch.Tensor, adapters: Adapters, ids: torch.Tensor,
+              Y: Optional[torch.Tensor] = None, Y16: Optional[torch.Tensor] = None,
+              ws: Optional[torch.Tensor] = "auto", want_y: bool = True, want_y16: bool = True
+              ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """qlin_gemm_lora: Y[i] = W x_i + scale[a] * B_a (A_a x_i), a = ids[i] (W x_i alone where
+    ids[i] is no slot); fp32 and / or fp16 [m, n]."""
+    _need_rows_x(X, w.k)
+    m, dev = X.shape[0], X.device
+    _need_flat(ids, torch.int32, (m,), "ids")
+    ad = adapters.c_struct(w)
+    _same_device(dev, (("w", w.data), ("a", adapters.a), ("b", adapters.b),
+                       ("scale", adapters.scale), ("ids", ids)))
+    Y, Y16, ld = _row_outputs(m, w.n, dev, Y, Y16, want_y, want_y16)
+    c = w.c_struct()
+    lib = _lib()
+    with _on_device(dev):
+        need = (lib.qlin_gemm_lora_workspace_bytes(ctypes.byref(c), ctypes.byref(ad), m)
+                if isinstance(ws, str) else 0)
+        ws = _rows_workspace(ws, need, dev)
+        st = lib.qlin_gemm_lora(ctypes.byref(c), ctypes.byref(ad), X.data_ptr(), m, _row_pitch(X),
+                                ids.data_ptr(), _ptr(Y), _ptr(Y16), ld, _ptr(ws),
+                                0 if ws is None else ws.numel() * ws.element_size(), _stream())
+    _check(st, "qlin_gemm_lora")
+    return Y, Y16
