@@ -11,21 +11,13 @@ namespace qlin {
 // indexes of the ids, bucket after bucket, in order within a bucket; ids
 // outside [0, buckets) share a last bucket.  Also the table of row tiles: up
 // to `rows` positions of one bucket each.  One work-group: wave w takes the
-// w-th 16th of the ids, counts it (lanes with equal ids find each other by
-// ballots over the id's bits, their first lane adds to the wave's own
-// counters), the counters are turned into starts, and a second pass writes
-// the positions.  No atomics: the order is the ids' own.
+// w-th 16th of the ids and counts it in counters of its own, the counters are
+// turned into starts, and a second pass writes the positions, 64 ids at a
+// time: each lane sets its bit in its bucket's mask, and the bits below its own
+// are the equal ids before it.  The atomics (LDS, one wave's) count and OR, so
+// the order is the ids' own.  (Masks by ballots over the id's bits took 60 of
+// 90 instructions per 64 ids: 16384 ids over 32 buckets 29 us.)
 constexpr int kPlanWaves = 16;
-
-// Lanes of the wave (in `live`) whose id equals this lane's; nbits covers the ids.
-__device__ __forceinline__ uint64_t same_id(int id, uint64_t live, int nbits) {
-  uint64_t m = live;
-  for (int b = 0; b < nbits; ++b) {
-    const uint64_t one = __builtin_amdgcn_ballot_w64((id >> b) & 1);
-    m &= ((id >> b) & 1) ? one : ~one;
-  }
-  return m;
-}
 
 // Sum of v over the lanes below this one.
 __device__ __forceinline__ int lanes_before(int v) {
@@ -60,23 +52,35 @@ __device__ __forceinline__ void counters_written() {
 __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
     const int32_t* __restrict__ ids, int count, int buckets, int rows, RowPlan plan) {
   __shared__ int hist[kPlanWaves][kMaxExperts + 1];
+  __shared__ unsigned long long mask[kPlanWaves][kMaxExperts + 1];
   __shared__ int part[kPlanWaves][2];
+  __shared__ int2 first[kMaxExperts + 1];    // each bucket's first tile and position
   const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
-  for (int i = tid; i < kPlanWaves * (kMaxExperts + 1); i += kPlanWaves * 64) (&hist[0][0])[i] = 0;
+  for (int w = 0; w < kPlanWaves; ++w)
+    for (int i = tid; i <= buckets; i += kPlanWaves * 64) {
+      hist[w][i] = 0;
+      mask[w][i] = 0;
+    }
   __syncthreads();
-  const int nbits = 32 - __builtin_clz(buckets);
   const int share = ((count + kPlanWaves * 64 - 1) / (kPlanWaves * 64)) * 64;
   const int i0 = min(count, wave * share), i1 = min(count, i0 + share);
-  auto bucket_of = [&](int i) __attribute__((always_inline)) {
-    const int id = i < i1 ? ids[i] : 0;
-    return (uint32_t)id < (uint32_t)buckets ? id : buckets;
+  // the buckets of 8 x 64 ids, loaded together
+  constexpr int U = 8;
+  int id8[U];
+  auto load_ids = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = b + 64 * u + lane;
+      const int id = i < i1 ? ids[i] : 0;
+      id8[u] = (uint32_t)id < (uint32_t)buckets ? id : buckets;
+    }
   };
-  for (int b = i0; b < i1; b += 64) {
-    const int id = bucket_of(b + lane);
-    const uint64_t live = __builtin_amdgcn_ballot_w64(b + lane < i1);
-    const uint64_t m = same_id(id, live, nbits);
-    if (b + lane < i1 && (m & ((1ull << lane) - 1)) == 0) hist[wave][id] += __builtin_popcountll(m);
-    counters_written();
+  for (int b0 = i0; b0 < i1; b0 += 64 * U) {
+    load_ids(b0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b0 + 64 * u + lane < i1) atomicAdd(&hist[wave][id8[u]], 1);
+    }
   }
   __syncthreads();
   // thread t: bucket t's count, starts of its waves, its start and its tiles'
@@ -99,25 +103,44 @@ __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
       plan.offs[buckets + 1] = end;
       *plan.ntiles = tend;
     }
-    for (int i = 0; i < mine; ++i) {
-      plan.tiles[2 * (tend - mine + i)] = tid;
-      plan.tiles[2 * (tend - mine + i) + 1] = start + i * rows;
-    }
+    first[tid] = make_int2(tend - mine, start);
   }
   __syncthreads();
-  for (int b = i0; b < i1; b += 64) {
-    const int id = bucket_of(b + lane);
-    const uint64_t live = __builtin_amdgcn_ballot_w64(b + lane < i1);
-    const uint64_t m = same_id(id, live, nbits);
-    const int before = __builtin_popcountll(m & ((1ull << lane) - 1));
-    int at = 0;
-    if (b + lane < i1) {
-      at = hist[wave][id] + before;
-      plan.order[at] = b + lane;
+  // tile i belongs to the last bucket that starts at or before it
+  const int ntiles = first[buckets].x;
+  for (int i = tid; i < ntiles; i += kPlanWaves * 64) {
+    int lo = 0, hi = buckets;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (first[mid].x <= i) lo = mid;
+      else hi = mid;
     }
-    counters_written();
-    if (b + lane < i1 && before == 0) hist[wave][id] = at + __builtin_popcountll(m);
-    counters_written();
+    plan.tiles[2 * i] = lo;
+    plan.tiles[2 * i + 1] = first[lo].y + (i - first[lo].x) * rows;
+  }
+  for (int b0 = i0; b0 < i1; b0 += 64 * U) {
+    load_ids(b0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + 64 * u, id = id8[u];
+      if (b >= i1) break;
+      const bool in = b + lane < i1;
+      if (in) atomicOr(&mask[wave][id], 1ull << lane);
+      counters_written();
+      const uint64_t m = mask[wave][id];
+      const int before = __builtin_popcountll(m & ((1ull << lane) - 1));
+      int at = 0;
+      if (in) {
+        at = hist[wave][id] + before;
+        plan.order[at] = b + lane;
+      }
+      counters_written();
+      if (in && before == 0) {
+        hist[wave][id] = at + __builtin_popcountll(m);
+        mask[wave][id] = 0;
+      }
+      counters_written();
+    }
   }
 }
 
@@ -145,23 +168,6 @@ __global__ __launch_bounds__(256) void k_rows_combine(
 }
 
 // ------------------------------------------------------ A x of the adapters --
-// t = scale * A x of one row, kept as a power of two 2^e and the fp16 halves
-// of t 2^-e (high, then what is left of it), |t 2^-e| < 2^15: 22 bits of the
-// row's largest entry, for any finite t.
-__device__ __forceinline__ float half_scale(float largest) {
-  if (!(largest > 0.f) || largest > 3.402823466e38f) return 1.f;
-  const int e = ((__builtin_bit_cast(uint32_t, largest) >> 23) & 255) - 127;   // floor(log2)
-  const int s = max(-126, min(127, e - 14));
-  return __builtin_bit_cast(float, (uint32_t)(s + 127) << 23);
-}
-__device__ __forceinline__ void store_halves(uint16_t* hi, uint16_t* lo, float t) {
-  const f16 a = (f16)t;
-  const float rest = t - (float)a;
-  const f16 b = (f16)(__builtin_isfinite(rest) ? rest : 0.f);
-  *hi = __builtin_bit_cast(uint16_t, a);
-  *lo = __builtin_bit_cast(uint16_t, b);
-}
-
 struct ShrinkArgs {
   const uint16_t* X;
   int64_t ldx;
@@ -169,48 +175,110 @@ struct ShrinkArgs {
   const int32_t* ids;
   const uint16_t* a;      // [slots][rank][k]
   const float* scale;     // [slots] or null
-  uint16_t* t;            // [m][2][rp]
-  float* tscale;          // [m]
+  float* t;               // [splits][m][rp]
+  RowPlan plan;           // (tile form) rows by adapter, 16 at a time
+  int splits, steps;      // (tile form) K splits; 128-column steps per split
 };
 
-// One work-group per row: its waves take the rank rows w, w + 4, ...
-__global__ __launch_bounds__(256) void k_lora_shrink_row(const ShrinkArgs s) {
-  __shared__ float red[128];
-  const int lane = lane_id(), wave = wave_id();
+__device__ __forceinline__ float dot8(uint4 x, uint4 y, float s) {
+  s = __builtin_amdgcn_fdot2(as_h2(x.x), as_h2(y.x), s, false);
+  s = __builtin_amdgcn_fdot2(as_h2(x.y), as_h2(y.y), s, false);
+  s = __builtin_amdgcn_fdot2(as_h2(x.z), as_h2(y.z), s, false);
+  return __builtin_amdgcn_fdot2(as_h2(x.w), as_h2(y.w), s, false);
+}
+
+// Few rows, each with an adapter of its own: one wave per (row, rank row), with
+// the loads of 4096 columns in flight together.  grid = (m, ceil(rp / 8)).
+__global__ __launch_bounds__(512) void k_lora_shrink_row(const ShrinkArgs s) {
+  const int lane = lane_id();
   const int64_t row = blockIdx.x;
+  const int r = blockIdx.y * 8 + wave_id();
   const int slot = s.ids[row];
-  if ((uint32_t)slot >= (uint32_t)s.slots) return;
-  const uint16_t* x = s.X + row * s.ldx;
-  for (int r = wave; r < s.rank; r += 4) {
+  if ((uint32_t)slot >= (uint32_t)s.slots || r >= s.rp) return;
+  float sum = 0.f;
+  if (r < s.rank) {
+    const uint16_t* x = s.X + row * s.ldx;
     const uint16_t* ar = s.a + ((int64_t)slot * s.rank + r) * s.k;
-    float sum = 0.f;
-    for (int k = 8 * lane; k < s.k; k += 512) {
-      const uint4 av = *reinterpret_cast<const uint4*>(ar + k);
-      const uint4 xv = *reinterpret_cast<const uint4*>(x + k);
-      sum = __builtin_amdgcn_fdot2(as_h2(av.x), as_h2(xv.x), sum, false);
-      sum = __builtin_amdgcn_fdot2(as_h2(av.y), as_h2(xv.y), sum, false);
-      sum = __builtin_amdgcn_fdot2(as_h2(av.z), as_h2(xv.z), sum, false);
-      sum = __builtin_amdgcn_fdot2(as_h2(av.w), as_h2(xv.w), sum, false);
+    constexpr int U = 8;
+    float part[2] = {0.f, 0.f};
+    for (int k0 = 8 * lane; k0 < s.k; k0 += 512 * U) {
+      uint4 av[U], xv[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = k0 + 512 * u < s.k;
+        const int k = in ? k0 + 512 * u : k0;
+        av[u] = *reinterpret_cast<const uint4*>(ar + k);
+        xv[u] = *reinterpret_cast<const uint4*>(x + k);
+        if (!in) av[u] = xv[u] = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) part[u & 1] = dot8(av[u], xv[u], part[u & 1]);
     }
-    sum = row_sum16(sum);
+    sum = row_sum16(part[0] + part[1]);
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
-    if (lane == 0) red[r] = sum;
+    if (s.scale != nullptr) sum *= s.scale[slot];
   }
-  __syncthreads();
-  if (wave != 0) return;
-  const float f = s.scale != nullptr ? s.scale[slot] : 1.f;
-  const float t0 = lane < s.rank ? f * red[lane] : 0.f;
-  const float t1 = lane + 64 < s.rank ? f * red[lane + 64] : 0.f;
-  float top = fmaxf(__builtin_fabsf(t0), __builtin_fabsf(t1));
+  if (lane == 0) s.t[row * s.rp + r] = sum;
+}
+
+// Many rows, ordered by adapter: one work-group per 16 rows of one adapter and
+// K split.  v_mfma_f32_16x16x32_f16: lane (c, q) supplies row c of X and rank
+// row 16 i + c of A at K positions 8q .. +7 of each 32; the 8 waves take
+// 128-column steps in turn and add their sums in LDS in wave order.
+template <int NR>
+__global__ __launch_bounds__(512) void k_lora_shrink_tile(const ShrinkArgs s) {
+  __shared__ f32x4 red[8][NR][64];
+  const int y = blockIdx.x, sp = blockIdx.y;
+  if (y >= *s.plan.ntiles) return;
+  const int slot = s.plan.tiles[2 * y], p0 = s.plan.tiles[2 * y + 1];
+  const int rows = min(16, s.plan.offs[slot + 1] - p0);
+  const int lane = lane_id(), wave = wave_id();
+  const int c = lane & 15, q = lane >> 4;
+  const uint16_t* x = s.X + (int64_t)s.plan.order[p0 + (c < rows ? c : 0)] * s.ldx + 8 * q;
+  const uint16_t* ar[NR];
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-  const float p = half_scale(top);
-  uint16_t* out = s.t + row * 2 * s.rp;
-  const float inv = 1.f / p;
-  if (lane < s.rp) store_halves(out + lane, out + s.rp + lane, t0 * inv);
-  if (lane + 64 < s.rp) store_halves(out + lane + 64, out + s.rp + lane + 64, t1 * inv);
-  if (lane == 0) s.tscale[row] = p;
+  for (int i = 0; i < NR; ++i)
+    ar[i] = s.a + ((int64_t)slot * s.rank + min(16 * i + c, s.rank - 1)) * s.k + 8 * q;
+  f32x4 acc[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  const int end = min(s.k, (sp + 1) * s.steps * 128);
+  for (int k = (sp * s.steps + wave) * 128; k < end; k += 8 * 128) {
+    f16x8 xv[4], av[NR][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int kk = min(k + 32 * e, s.k - 32);          // (k is a multiple of 64)
+      xv[e] = *reinterpret_cast<const f16x8*>(x + kk);
+#pragma unroll
+      for (int i = 0; i < NR; ++i) av[i][e] = *reinterpret_cast<const f16x8*>(ar[i] + kk);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (k + 32 * e >= end) break;
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[e], av[i][e], acc[i], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NR; ++i) red[wave][i][lane] = acc[i];
+  __syncthreads();
+  const float f = s.scale != nullptr ? s.scale[slot] : 1.f;
+  for (int e = threadIdx.x; e < NR * 64; e += 512) {
+    const int i = e >> 6, l = e & 63, r = 16 * i + (l & 15);
+    f32x4 sum = red[0][i][l];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) sum += red[w][i][l];
+    if (r >= s.rp) continue;
+    // D[4 (l / 16) + v][l % 16]
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int row = 4 * (l >> 4) + v;
+      if (row < rows)
+        s.t[((int64_t)sp * s.m + s.plan.order[p0 + row]) * s.rp + r] = r < s.rank ? f * sum[v] : 0.f;
+    }
+  }
 }
 
 }  // namespace qlin

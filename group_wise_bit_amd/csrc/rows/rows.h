@@ -77,7 +77,7 @@ struct RowsArgs {
   const uint8_t* zero[2];
   int64_t code_step, meta_step;   // words / entries from one expert to the next
   int n, kb, G;
-  int cols;                       // work-group columns: blockIdx.x = row tile * cols + column
+  int cols;                       // work-group columns of a row tile
   const uint16_t* X;
   int64_t ldx;
   int m, top_k;
@@ -88,30 +88,40 @@ struct RowsArgs {
   int64_t ldy;
   // kLora
   const int32_t* ids;
-  const uint16_t* t;              // [m][2][rp]: the high and low halves of A x
-  const float* tscale;            // [m]: their power of two
+  const float* t;                 // [splits][m][rp]: scale * A x, partial sums over K
   const uint16_t* b;              // [slots][n][rank]
-  int slots, rank, rp;            // rp: rank rounded up to 16
+  int slots, rank, rp, tsplits;   // rp: rank rounded up to 16, t is 0 from rank on
 };
 
-// A work-group's rows: positions p0 .. p0 + rows - 1 of expert e.
-struct RowTile { int e, p0, rows; };
+// A work-group's rows: positions p0 .. p0 + rows - 1 of expert e, and its column.
+struct RowTile { int e, p0, rows, col; };
+
+// Work-groups go to the 8 XCDs (each with its own L2) round-robin by their id:
+// of `total` positions, numbered row tile by row tile, every XCD gets one
+// contiguous range, so that the rows of a tile, and the weights of an expert,
+// are fetched into one L2.
+__device__ __forceinline__ int xcd_position(int total) {
+  const int f = blockIdx.x, per = total / kXcds, rem = total % kXcds;
+  const int xcd = f % kXcds, local = f / kXcds;
+  return xcd < rem ? xcd * (per + 1) + local : rem * (per + 1) + (xcd - rem) * per + local;
+}
 
 template <int MODE>
-__device__ __forceinline__ RowTile row_tile(const RowsArgs& a, int y, int height) {
+__device__ __forceinline__ RowTile row_tile(const RowsArgs& a, int height) {
   RowTile r;
+  r.e = r.p0 = r.rows = r.col = 0;
+  const int tiles = MODE == kLora ? (a.m + height - 1) / height : *a.plan.ntiles;
+  const int total = tiles * a.cols;
+  if ((int)blockIdx.x >= total) return r;
+  const int f = xcd_position(total), y = f / a.cols;
+  r.col = f % a.cols;
   if constexpr (MODE == kLora) {
-    r.e = 0;
     r.p0 = y * height;
     r.rows = min(height, a.m - r.p0);
   } else {
-    r.rows = 0;
-    r.e = r.p0 = 0;
-    if (y < *a.plan.ntiles) {
-      r.e = a.plan.tiles[2 * y];
-      r.p0 = a.plan.tiles[2 * y + 1];
-      r.rows = min(height, a.plan.offs[r.e + 1] - r.p0);
-    }
+    r.e = a.plan.tiles[2 * y];
+    r.p0 = a.plan.tiles[2 * y + 1];
+    r.rows = min(height, a.plan.offs[r.e + 1] - r.p0);
   }
   return r;
 }
@@ -124,45 +134,95 @@ __device__ __forceinline__ int64_t x_row(const RowsArgs& a, int p) {
   else return a.plan.order != nullptr ? a.plan.order[p] : p;
 }
 
-// Adds the adapters of 32 rows to a 32 x 32 block of sums (MFMA layout: lane
-// (c, h), register r: row 8 (r / 4) + 4h + r % 4, column col of the lane).
-// row: this lane's row c of X, or -1.  Each adapter that stands among the rows
-// is multiplied once for all 32 rows and added to its own alone; `part` of
-// `parts` callers takes every parts-th of them.
-__device__ __forceinline__ void add_adapters(const RowsArgs& a, int64_t row, int col, int part,
-                                             int parts, f32x16& acc) {
-  const int lane = lane_id(), h = lane >> 5;
+// The power of two 2^e that brings a row of A x into fp16's range with room for
+// 22 bits in two halves: |t 2^-e| < 2^15 for the row's largest |t| (1 for a
+// row of zeros or one that is not finite).
+__device__ __forceinline__ float half_scale(float largest) {
+  if (!(largest > 0.f) || largest > 3.402823466e38f) return 1.f;
+  const int e = (int)(__builtin_bit_cast(uint32_t, largest) >> 23) - 127;   // floor(log2)
+  return __builtin_bit_cast(float, (uint32_t)(max(-126, e - 14) + 127) << 23);
+}
+
+// 8 entries of one row of A x from the partial sums, in split order.
+__device__ __forceinline__ void load_t8(const RowsArgs& a, const float* p, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  for (int s = 0; s < a.tsplits; ++s) {
+    const f32x4 x = reinterpret_cast<const f32x4*>(p)[0], y = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] += x[i];
+      v[4 + i] += y[i];
+    }
+    p += (int64_t)a.m * a.rp;
+  }
+}
+
+// Adds the adapters of 32 rows to CB blocks of 32 x 32 sums (MFMA layout: lane
+// (c, h), register r: row 8 (r / 4) + 4h + r % 4, column c).  row: the lane's
+// row c in X, or -1; col[cb]: its column of block cb.  Each adapter that stands
+// among the rows is multiplied once for all of them and added to its own rows
+// alone; `part` of `parts` callers takes every parts-th adapter.  A x (fp32)
+// becomes 2^e (high + low fp16 half), both halves exact products with B.
+template <int CB>
+__device__ __forceinline__ void add_adapters(const RowsArgs& a, int64_t row, const int (&col)[CB],
+                                             int part, int parts, f32x16 (&acc)[CB]) {
+  const int h = lane_id() >> 5;
   const int id = row >= 0 ? a.ids[row] : -1;
   const bool has = (uint32_t)id < (uint32_t)a.slots;
-  const float ts = has ? a.tscale[row] : 0.f;
   uint32_t left = (uint32_t)__builtin_amdgcn_ballot_w64(has);
+  if (left == 0) return;
+  // the rows' powers of two (a lane holds half of its row's entries)
+  const float* tp = a.t + (has ? row : 0) * a.rp + 8 * h;
+  float top = 0.f;
+  for (int q = 0; q < a.rp; q += 16) {
+    float v[8];
+    load_t8(a, tp + q, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(v[i]));
+  }
+  const float ts = half_scale(__builtin_fmaxf(top, __shfl_xor(top, 32)));
+  const float inv = 1.f / ts;              // a power of two: exact
   for (int i = 0; left != 0; ++i) {
-    const int first = __builtin_ctz(left);
-    const int slot = __builtin_amdgcn_readlane(id, first);
+    const int slot = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
     const uint32_t mine = (uint32_t)__builtin_amdgcn_ballot_w64(has && id == slot);
     left &= ~mine;
     if (i % parts != part) continue;
-    f32x16 hi, lo;
+    f32x16 hi[CB], lo[CB];
+    const uint16_t* bp[CB];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) hi[r] = lo[r] = 0.f;
-    const uint16_t* tp = a.t + (has ? row : 0) * 2 * a.rp + 8 * h;
-    const uint16_t* bp = a.b + ((int64_t)slot * a.n + min(col, a.n - 1)) * a.rank;
+    for (int cb = 0; cb < CB; ++cb) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) hi[cb][r] = lo[cb][r] = 0.f;
+      bp[cb] = a.b + ((int64_t)slot * a.n + min(col[cb], a.n - 1)) * a.rank + 8 * h;
+    }
     for (int q = 0; q < a.rp; q += 16) {
-      // (past the rank: the halves of A x are 0, the factor too)
-      uint4 bv = make_uint4(0, 0, 0, 0);
-      if (q + 8 * h < a.rank) bv = *reinterpret_cast<const uint4*>(bp + q + 8 * h);
-      const f16x8 bf = u4_to_f16x8(bv);
-      hi = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-          u4_to_f16x8(*reinterpret_cast<const uint4*>(tp + q)), bf, hi, 0, 0, 0);
-      lo = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-          u4_to_f16x8(*reinterpret_cast<const uint4*>(tp + a.rp + q)), bf, lo, 0, 0, 0);
+      float v[8];
+      load_t8(a, tp + q, v);
+      f16x8 th, tl;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = v[e] * inv;
+        th[e] = (f16)x;
+        tl[e] = (f16)(x - (float)th[e]);
+      }
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) {
+        // (past the rank A x is 0, the factor too)
+        const f16x8 bf = u4_to_f16x8(q + 8 * h < a.rank ? *reinterpret_cast<const uint4*>(bp[cb] + q)
+                                                        : make_uint4(0, 0, 0, 0));
+        hi[cb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(th, bf, hi[cb], 0, 0, 0);
+        lo[cb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(tl, bf, lo[cb], 0, 0, 0);
+      }
     }
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int rr = 8 * (r >> 2) + 4 * h + (r & 3);
       const float f = __shfl(ts, rr);
       // (a select, not a product with 0: another row's infinity stays its own)
-      acc[r] += (mine >> rr) & 1 ? f * (hi[r] + lo[r]) : 0.f;
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+        acc[cb][r] += (mine >> rr) & 1 ? f * (hi[cb][r] + lo[cb][r]) : 0.f;
     }
   }
 }
@@ -182,9 +242,9 @@ __global__ __launch_bounds__(WAVES * 64) void k_rows_ksplit(const RowsArgs a) {
   constexpr int PT = 1024 / NT;              // outputs per thread
   static_assert(16 % WAVES == 0, "reduction split");
   __shared__ float red[WAVES][1024];
-  const int gy = blockIdx.x / a.cols, gx = blockIdx.x % a.cols;
-  const RowTile rt = row_tile<MODE>(a, gy, 32);
+  const RowTile rt = row_tile<MODE>(a, 32);
   if (rt.rows <= 0) return;
+  const int gx = rt.col;
   const int lane = lane_id(), wave = wave_id();
   const int c = lane & 31, h = lane >> 5;
   const int t = gx >> 1, cb = gx & 1;
@@ -247,8 +307,10 @@ __global__ __launch_bounds__(WAVES * 64) void k_rows_ksplit(const RowsArgs a) {
     }
   }
   const int col = t * kTile + 32 * cb + c;
-  if constexpr (MODE == kLora)
-    add_adapters(a, c < rt.rows ? xr : -1, col, wave, WAVES, acc[0]);
+  if constexpr (MODE == kLora) {
+    const int cols[1] = {col};
+    add_adapters<1>(a, c < rt.rows ? xr : -1, cols, wave, WAVES, acc);
+  }
   // thread (wave, lane) finishes registers wave, wave + WAVES, ...
   float v[NM][PT];
 #pragma unroll
@@ -282,6 +344,191 @@ __global__ __launch_bounds__(WAVES * 64) void k_rows_ksplit(const RowsArgs a) {
       if (a.y16 != nullptr) a.y16[o] = __builtin_bit_cast(uint16_t, (f16)v[0][p]);
     }
   }
+}
+
+// Keeps the compiler from moving the computation of v past this point.
+__device__ __forceinline__ void here(f16x8& v) { asm volatile("" : "+v"(v)); }
+
+// -------------------------------------------------- many rows per expert --
+// Work-group: 32 RB rows of one expert x 128 columns (two 64-row weight tiles;
+// kSwiglu: tile t of gate and of up), 4 waves of 32 RB rows x 32 columns
+// (kSwiglu: 16 columns of gate in lanes c < 16, the same 16 of up in the
+// others).  A wave decodes its columns' block once, straight into MFMA B
+// registers -- integers q - z, exact, no scale rounded into them -- and
+// multiplies it by all RB blocks of X, read from LDS (16-byte chunks permuted
+// within their row by xswz, so that operand reads fall on distinct banks).  The four MFMAs of a block start from 0 and the group's scale takes
+// their sum to the fp32 accumulators, 16 fma per lane beside the next four
+// MFMAs.  Two X buffers: while block j is multiplied, block j + 1's rows are
+// on their way to registers and then to the other buffer; codes run two blocks
+// ahead.  One barrier per block.
+template <int BITS, int MODE, int RB, int D>
+__global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
+  constexpr int WPB = 2 * BITS;
+  constexpr int HW = BITS;
+  constexpr int BM = 32 * RB;
+  __shared__ f16x8 xs[2][BM * 8];
+  const RowTile rt = row_tile<MODE>(a, BM);
+  if (rt.rows <= 0) return;
+  const int gx = rt.col;
+  const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
+  const int c = lane & 31, h = lane >> 5;
+  const uint32_t magic = vreg_const(kMagic);
+  // the lane's weight row: row drow of tile dt of matrix di (a tile past the
+  // matrix re-reads its last one, never stored)
+  const int tiles = (a.n + kTile - 1) / kTile;
+  const int tile = MODE == kSwiglu ? gx : 2 * gx + (wave >> 1);
+  const int drow = MODE == kSwiglu ? 16 * wave + (c & 15) : 32 * (wave & 1) + c;
+  const int di = MODE == kSwiglu ? c >> 4 : 0;
+  const int dt = min(tile, tiles - 1);
+  const uint32_t* wsrc = (di ? a.codes[1] : a.codes[0]) + rt.e * a.code_step +
+                         ((int64_t)dt * a.kb * kTile + drow) * WPB;
+  const int64_t mt = rt.e * a.meta_step + (int64_t)dt * a.G * kTile + drow;
+  const uint16_t* ssrc = (di ? a.scale[1] : a.scale[0]) + mt;
+  const uint8_t* zsrc = (di ? a.zero[1] : a.zero[0]) + mt;
+  const int t8 = tid >> 3, xk = tid & 7;
+  const uint16_t* xsrc[RB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    const int r = t8 + 32 * i;
+    xsrc[i] = a.X + x_row<MODE>(a, rt.p0 + (r < rt.rows ? r : 0)) * a.ldx + 8 * xk;
+  }
+  const int xw = 8 * t8 + xswz(t8, xk);      // (rows 32 apart: the same place in their row)
+
+  uint32_t wl[D][HW];
+  uint16_t sr[D];
+  int zc[D];
+  f16x8 xg[D][RB];
+  auto request_x = [&](auto S, int j) __attribute__((always_inline)) {
+    constexpr int u = decltype(S)::value;
+    const int jj = min(j, a.kb - 1);
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+      xg[u][i] = *reinterpret_cast<const f16x8*>(xsrc[i] + (int64_t)jj * kBlock);
+  };
+  auto request_w = [&](auto S, int j) __attribute__((always_inline)) {
+    constexpr int u = decltype(S)::value;
+    const int jj = min(j, a.kb - 1);
+    load_half<BITS>(wsrc + (int64_t)jj * kTile * WPB, h, wl[u]);
+    const int64_t g = (a.G == 1) ? 0 : jj;
+    sr[u] = ssrc[g * kTile];
+    zc[u] = zsrc[g * kTile];
+  };
+  auto store_x = [&](auto S, int b) __attribute__((always_inline)) {
+    constexpr int u = decltype(S)::value;
+#pragma unroll
+    for (int i = 0; i < RB; ++i) xs[b][xw + 256 * i] = xg[u][i];
+  };
+  f32x16 acc[RB];
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[rb][r] = 0.f;
+  f16x8 bv[2][4];
+  float scl[2];
+  f32x16 blk[2];               // sums of one block and 32 rows, not yet scaled
+#pragma unroll
+  for (int r = 0; r < 16; ++r) blk[0][r] = blk[1][r] = 0.f;
+  scl[1] = 0.f;
+  static_for<0, D>([&](auto S) __attribute__((always_inline)) {
+    request_w(S, decltype(S)::value);
+    request_x(S, decltype(S)::value);
+  });
+  const std::integral_constant<int, 0> S0;
+  {
+    const DeqT<BITS> d = make_deq_b<BITS>(1.f, zc[0]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) bv[0][q] = int_half<BITS>(wl[0], q, d, magic);
+    scl[0] = h2f(sr[0]);
+    store_x(S0, 0);
+    request_w(S0, D);
+  }
+  lds_barrier();
+  // block j (slot U of D): from X buffer and operand registers j % 2; block
+  // j + 1's codes and rows wait in slot U + 1, slot U's rows are free
+  auto step = [&](auto U, int j) __attribute__((always_inline)) {
+    constexpr int u = decltype(U)::value, b = u & 1;
+    const std::integral_constant<int, (u + 1) % D> N;
+    constexpr int n = (u + 1) % D;
+    f16x8 av[2][4];
+    auto read_a = [&](int rb) __attribute__((always_inline)) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        av[rb & 1][q] = xs[b][8 * (32 * rb + c) + xswz(c, 4 * h + q)];
+    };
+    auto scale_block = [&](int rb, float s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[rb][r] = __builtin_fmaf(s, blk[rb & 1][r], acc[rb][r]);
+    };
+    read_a(0);
+    request_x(U, j + D);
+    const DeqT<BITS> d = make_deq_b<BITS>(1.f, zc[n]);
+    // the previous block's last rows, while this block's first operands arrive
+    scale_block(RB - 1, scl[1 - b]);
+    scl[1 - b] = h2f(sr[n]);
+    asm volatile("" : "+v"(scl[1 - b]));
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      if (rb + 1 < RB) read_a(rb + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      const f32x16 none = {};
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        blk[rb & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            av[rb & 1][q], bv[b][q], q == 0 ? none : blk[rb & 1], 0, 0, 0);
+#pragma unroll
+      for (int q = rb * 4 / RB; q < (rb + 1) * 4 / RB; ++q) {
+        bv[1 - b][q] = int_half<BITS>(wl[n], q, d, magic);
+        here(bv[1 - b][q]);
+      }
+      if (rb > 0) scale_block(rb - 1, scl[b]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    store_x(N, 1 - b);
+    request_w(N, j + 1 + D);
+    lds_barrier();
+  };
+  int j0 = 0;
+  for (; j0 + D <= a.kb; j0 += D)
+    static_for<0, D>([&](auto U) __attribute__((always_inline)) {
+      step(U, j0 + decltype(U)::value);
+    });
+  static_for<0, D - 1>([&](auto U) __attribute__((always_inline)) {
+    if (j0 + decltype(U)::value < a.kb) step(U, j0 + decltype(U)::value);
+  });
+  {
+    const float s = a.kb & 1 ? scl[0] : scl[1];
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      acc[RB - 1][r] = __builtin_fmaf(s, blk[(RB - 1) & 1][r], acc[RB - 1][r]);
+  }
+
+  const int col = tile * kTile + drow;
+  if constexpr (MODE == kLora) {
+    const int cols[1] = {col};
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+      add_adapters<1>(a, 32 * rb + c < rt.rows ? x_row<MODE>(a, rt.p0 + 32 * rb + c) : -1, cols, 0,
+                      1, reinterpret_cast<f32x16(&)[1]>(acc[rb]));
+  }
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int row = 32 * rb + 8 * (r >> 2) + 4 * h + (r & 3);
+      if constexpr (MODE == kSwiglu) {
+        const float u = __shfl_xor(acc[rb][r], 16);
+        if (row >= rt.rows || c >= 16) continue;
+        const float hv = silu(acc[rb][r]) * u;
+        a.y16[(int64_t)(rt.p0 + row) * a.ldy + col] = __builtin_bit_cast(uint16_t, (f16)hv);
+      } else {
+        if (row >= rt.rows || col >= a.n) continue;
+        const int64_t out = MODE == kDown ? a.plan.order[rt.p0 + row] : x_row<MODE>(a, rt.p0 + row);
+        const float v = MODE == kDown ? a.weights[out] * acc[rb][r] : acc[rb][r];
+        if (MODE == kDown || a.y != nullptr) a.y[out * a.ldy + col] = v;
+        if (MODE == kLora && a.y16 != nullptr)
+          a.y16[out * a.ldy + col] = __builtin_bit_cast(uint16_t, (f16)v);
+      }
+    }
 }
 
 }  // namespace qlin

@@ -88,7 +88,7 @@ struct MoePlan {
 MoePlan moe_plan(int inner, int model, int experts, int m, int top_k, void* ws) {
   MoePlan p;
   p.pairs = (int64_t)m * top_k;
-  p.cfg.height = 32;
+  p.cfg.height = p.pairs >= 16 * (int64_t)experts ? 64 : 32;
   p.cfg.tiles = (int)tile_bound(p.pairs, experts, p.cfg.height);
   Arena ar{static_cast<char*>(ws)};
   p.rows = take_plan(ar, p.pairs, experts, p.cfg.height);
@@ -115,22 +115,41 @@ qlin_status check_moe(const qlin_weight* gate, const qlin_weight* up, const qlin
 }
 
 // --------------------------------------------------------------- adapters --
+// From this many rows on they are ordered by adapter: A x is then formed on the
+// matrix cores, 16 rows of one adapter at a time, and a tile of the product
+// holds few adapters.  Below, each row reads its own adapter.
+constexpr int kSortRows = 128;
+
 struct LoraPlan {
   RowsCfg cfg;
-  uint16_t* t;
-  float* tscale;
+  bool sorted;         // rows are ordered by adapter first
+  RowPlan rows;
+  int tiles;           // (sorted) 16-row tiles of one adapter, at most
+  int splits, steps;   // K splits of A x, 128-column steps of each
+  float* t;
   int rp;
   int64_t bytes;
 };
 
-LoraPlan lora_plan(const qlin_adapters* ad, int m, void* ws) {
-  LoraPlan p;
-  p.cfg.height = 32;
-  p.cfg.tiles = (m + 31) / 32;
+LoraPlan lora_plan(const qlin_weight* w, const qlin_adapters* ad, int m, void* ws) {
+  LoraPlan p{};
+  p.cfg.height = m >= 1024 ? 64 : 32;
+  p.cfg.tiles = (m + p.cfg.height - 1) / p.cfg.height;
   p.rp = (ad->rank + 15) / 16 * 16;
+  p.sorted = m >= kSortRows;
+  p.splits = 1;
+  const int steps = (w->k + 127) / 128;
+  p.steps = steps;
   Arena ar{static_cast<char*>(ws)};
-  p.t = ar.take<uint16_t>((int64_t)m * 2 * p.rp);
-  p.tscale = ar.take<float>(m);
+  if (p.sorted) {
+    p.tiles = (int)tile_bound(m, ad->slots, 16);
+    // enough work-groups for the chip, a step for every wave of each
+    while (p.splits < 8 && p.tiles * p.splits < 256 && steps >= 16 * p.splits) p.splits *= 2;
+    p.steps = (steps + p.splits - 1) / p.splits;
+    p.splits = (steps + p.steps - 1) / p.steps;
+    p.rows = take_plan(ar, m, ad->slots, 16);
+  }
+  p.t = ar.take<float>((int64_t)p.splits * m * p.rp);
   p.bytes = ar.at;
   return p;
 }
@@ -209,7 +228,7 @@ qlin_status qlin_moe_mlp(const qlin_weight* gate, const qlin_weight* up, const q
     return QLIN_ERR_ALIGN;
   const int inner = gate->n, model = gate->k;
   const MoePlan p = moe_plan(inner, model, experts, m, top_k, workspace);
-  if (!rows_fits(inner, p.cfg) || !rows_fits(model, p.cfg)) return QLIN_ERR_SHAPE;
+  if (!rows_fits(inner, kSwiglu, p.cfg) || !rows_fits(model, kDown, p.cfg)) return QLIN_ERR_SHAPE;
   if (workspace == nullptr || workspace_bytes < p.bytes) return QLIN_ERR_WORKSPACE;
   const int64_t span = (int64_t)(m - 1) * ld_y + model;
   const Range out[3] = {range_of(workspace, workspace_bytes),
@@ -260,7 +279,7 @@ qlin_status qlin_moe_mlp(const qlin_weight* gate, const qlin_weight* up, const q
 
 int64_t qlin_gemm_lora_workspace_bytes(const qlin_weight* w, const qlin_adapters* ad, int32_t m) {
   if (check_lora(w, ad, m) != QLIN_OK || m == 0) return 0;
-  return lora_plan(ad, m, nullptr).bytes;
+  return lora_plan(w, ad, m, nullptr).bytes;
 }
 
 qlin_status qlin_gemm_lora(const qlin_weight* w, const qlin_adapters* ad, const uint16_t* X,
@@ -278,8 +297,8 @@ qlin_status qlin_gemm_lora(const qlin_weight* w, const qlin_adapters* ad, const 
   if (!aligned16(X) || !aligned16(Y) || !aligned16(Y16) || !aligned16(ad->a) ||
       !aligned16(ad->b) || !aligned4(ad->scale) || !aligned4(ids) || !aligned16(workspace))
     return QLIN_ERR_ALIGN;
-  const LoraPlan p = lora_plan(ad, m, workspace);
-  if (!rows_fits(w->n, p.cfg)) return QLIN_ERR_SHAPE;
+  const LoraPlan p = lora_plan(w, ad, m, workspace);
+  if (!rows_fits(w->n, kLora, p.cfg)) return QLIN_ERR_SHAPE;
   if (workspace == nullptr || workspace_bytes < p.bytes) return QLIN_ERR_WORKSPACE;
   const int64_t span = (int64_t)(m - 1) * ld_y + w->n;
   const int64_t sr = (int64_t)ad->slots * ad->rank;
@@ -299,9 +318,32 @@ qlin_status qlin_gemm_lora(const qlin_weight* w, const qlin_adapters* ad, const 
   }
   st = check_device();
   if (st != QLIN_OK) return st;
-  const ShrinkArgs s{X, ld_x, m, w->k, ad->slots, ad->rank, p.rp, ids, ad->a, ad->scale,
-                     p.t, p.tscale};
-  hipLaunchKernelGGL(k_lora_shrink_row, dim3(m), dim3(256), 0, stream, s);
+  ShrinkArgs s{};
+  s.X = X;
+  s.ldx = ld_x;
+  s.m = m;
+  s.k = w->k;
+  s.slots = ad->slots;
+  s.rank = ad->rank;
+  s.rp = p.rp;
+  s.ids = ids;
+  s.a = ad->a;
+  s.scale = ad->scale;
+  s.t = p.t;
+  if (p.sorted) {
+    s.plan = p.rows;
+    s.splits = p.splits;
+    s.steps = p.steps;
+    hipLaunchKernelGGL(k_rows_plan, dim3(1), dim3(kPlanWaves * 64), 0, stream, ids, m, ad->slots, 16,
+                       p.rows);
+    const dim3 grid(p.tiles, p.splits), block(512);
+    if (p.rp <= 16) hipLaunchKernelGGL((k_lora_shrink_tile<1>), grid, block, 0, stream, s);
+    else if (p.rp <= 32) hipLaunchKernelGGL((k_lora_shrink_tile<2>), grid, block, 0, stream, s);
+    else if (p.rp <= 64) hipLaunchKernelGGL((k_lora_shrink_tile<4>), grid, block, 0, stream, s);
+    else hipLaunchKernelGGL((k_lora_shrink_tile<8>), grid, block, 0, stream, s);
+  } else {
+    hipLaunchKernelGGL(k_lora_shrink_row, dim3(m, p.rp / 8), dim3(512), 0, stream, s);
+  }
   RowsArgs a{};
   set_weight(a, 0, w);
   a.X = X;
@@ -313,7 +355,8 @@ qlin_status qlin_gemm_lora(const qlin_weight* w, const qlin_adapters* ad, const 
   a.ldy = ld_y;
   a.ids = ids;
   a.t = p.t;
-  a.tscale = p.tscale;
+  a.tsplits = p.splits;
+  if (p.sorted) a.plan = p.rows;
   a.b = ad->b;
   a.slots = ad->slots;
   a.rank = ad->rank;

@@ -6,20 +6,25 @@ namespace qlin {
 
 constexpr int kB = QLIN_INST_BITS;
 
+
+template <int B, int MODE>
+void launch_mode(const RowsArgs& a, RowsCfg c, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)a.cols * c.tiles));
+  if (c.height == 32) {
+    constexpr int W = 8, U = MODE == kSwiglu ? 1 : 2;
+    hipLaunchKernelGGL((k_rows_ksplit<B, MODE, W, U>), grid, dim3(W * 64), 0, st, a);
+  } else {
+    hipLaunchKernelGGL((k_rows_tiled<B, MODE, 2, 4>), grid, dim3(256), 0, st, a);
+  }
+}
+
 template <int B>
 void launch_rows(const RowsArgs& args, int mode, RowsCfg c, hipStream_t st) {
   RowsArgs a = args;
-  a.cols = rows_cols(a.n);
-  const dim3 grid((unsigned)((int64_t)a.cols * c.tiles));
-  constexpr int W = 8;
-  const dim3 block(W * 64);
-  if (mode == kSwiglu) {
-    hipLaunchKernelGGL((k_rows_ksplit<B, kSwiglu, W, 1>), grid, block, 0, st, a);
-  } else if (mode == kDown) {
-    hipLaunchKernelGGL((k_rows_ksplit<B, kDown, W, 2>), grid, block, 0, st, a);
-  } else {
-    hipLaunchKernelGGL((k_rows_ksplit<B, kLora, W, 2>), grid, block, 0, st, a);
-  }
+  a.cols = rows_cols(a.n, mode, c);
+  if (mode == kSwiglu) launch_mode<B, kSwiglu>(a, c, st);
+  else if (mode == kDown) launch_mode<B, kDown>(a, c, st);
+  else launch_mode<B, kLora>(a, c, st);
 }
 
 template void launch_rows<kB>(const RowsArgs&, int, RowsCfg, hipStream_t);
