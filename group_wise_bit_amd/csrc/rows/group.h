@@ -98,11 +98,7 @@ __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
   const int start = end - total;
   if (tid <= buckets) {
     for (int w = 0; w < kPlanWaves; ++w) hist[w][tid] += start;
-    plan.offs[tid] = start;
-    if (tid == buckets) {
-      plan.offs[buckets + 1] = end;
-      *plan.ntiles = tend;
-    }
+    if (tid == buckets) *plan.ntiles = tend;
     first[tid] = make_int2(tend - mine, start);
   }
   __syncthreads();
@@ -115,8 +111,8 @@ __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
       if (first[mid].x <= i) lo = mid;
       else hi = mid;
     }
-    plan.tiles[2 * i] = lo;
-    plan.tiles[2 * i + 1] = first[lo].y + (i - first[lo].x) * rows;
+    const int p0 = first[lo].y + (i - first[lo].x) * rows;
+    plan.tiles[i] = make_int4(lo, p0, min(rows, first[lo + 1].y - p0), 0);
   }
   for (int b0 = i0; b0 < i1; b0 += 64 * U) {
     load_ids(b0);
@@ -231,8 +227,8 @@ __global__ __launch_bounds__(512) void k_lora_shrink_tile(const ShrinkArgs s) {
   __shared__ f32x4 red[8][NR][64];
   const int y = blockIdx.x, sp = blockIdx.y;
   if (y >= *s.plan.ntiles) return;
-  const int slot = s.plan.tiles[2 * y], p0 = s.plan.tiles[2 * y + 1];
-  const int rows = min(16, s.plan.offs[slot + 1] - p0);
+  const int4 tile = s.plan.tiles[y];
+  const int slot = tile.x, p0 = tile.y, rows = tile.z;
   const int lane = lane_id(), wave = wave_id();
   const int c = lane & 15, q = lane >> 4;
   const uint16_t* x = s.X + (int64_t)s.plan.order[p0 + (c < rows ? c : 0)] * s.ldx + 8 * q;

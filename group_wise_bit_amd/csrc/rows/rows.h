@@ -12,9 +12,8 @@ constexpr int kMaxTopK = 32;
 
 // Rows ordered by expert (k_rows_plan).
 struct RowPlan {
-  int32_t* offs;      // [buckets + 2]: first position of each bucket, then the count
   int32_t* order;     // [count]: position -> index
-  int32_t* tiles;     // [2 * ntiles]: bucket, first position
+  int4* tiles;        // [ntiles]: bucket, first position, rows
   int32_t* ntiles;    // [1]
 };
 
@@ -69,7 +68,8 @@ __device__ __forceinline__ f16x8 int_half(const uint32_t* wl, int s, const DeqT<
 //   kSwiglu  two matrices (gate, up): fp16 silu(g) * u, one row per position
 //   kDown    fp32 weights[index] * sum, one row per index (pair of token and slot)
 //   kLora    sum + the row's adapter, fp32 and / or fp16
-enum RowsMode { kSwiglu = 0, kDown = 1, kLora = 2 };
+//   kToken   one token: its slots' sums times their weights, fp32 and / or fp16
+enum RowsMode { kSwiglu = 0, kDown = 1, kLora = 2, kToken = 3 };
 
 struct RowsArgs {
   const uint32_t* codes[2];
@@ -82,12 +82,12 @@ struct RowsArgs {
   int64_t ldx;
   int m, top_k;
   RowPlan plan;                   // order null: positions are rows themselves
-  const float* weights;           // kDown
+  int experts;                    // one row: ids outside [0, experts) are no expert
+  const float* weights;           // kDown, kToken
   uint16_t* y16;                  // kSwiglu: h; kLora: Y16 or null
   float* y;                       // kDown: partial rows; kLora: Y or null
   int64_t ldy;
-  // kLora
-  const int32_t* ids;
+  const int32_t* ids;             // kLora, and one row
   const float* t;                 // [splits][m][rp]: scale * A x, partial sums over K
   const uint16_t* b;              // [slots][n][rank]
   int slots, rank, rp, tsplits;   // rp: rank rounded up to 16, t is 0 from rank on
@@ -119,9 +119,10 @@ __device__ __forceinline__ RowTile row_tile(const RowsArgs& a, int height) {
     r.p0 = y * height;
     r.rows = min(height, a.m - r.p0);
   } else {
-    r.e = a.plan.tiles[2 * y];
-    r.p0 = a.plan.tiles[2 * y + 1];
-    r.rows = min(height, a.plan.offs[r.e + 1] - r.p0);
+    const int4 v = a.plan.tiles[y];
+    r.e = v.x;
+    r.p0 = v.y;
+    r.rows = v.z;
   }
   return r;
 }
@@ -143,10 +144,12 @@ __device__ __forceinline__ float half_scale(float largest) {
   return __builtin_bit_cast(float, (uint32_t)(max(-126, e - 14) + 127) << 23);
 }
 
-// 8 entries of one row of A x from the partial sums, in split order.
-__device__ __forceinline__ void load_t8(const RowsArgs& a, const float* p, float (&v)[8]) {
+// 8 entries of one row of A x from the partial sums, in split order; 0 from rp on.
+__device__ __forceinline__ void load_t8(const RowsArgs& a, int64_t row, int r, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  if (r >= a.rp) return;
+  const float* p = a.t + row * a.rp + r;
   for (int s = 0; s < a.tsplits; ++s) {
     const f32x4 x = reinterpret_cast<const f32x4*>(p)[0], y = reinterpret_cast<const f32x4*>(p)[1];
 #pragma unroll
@@ -158,166 +161,236 @@ __device__ __forceinline__ void load_t8(const RowsArgs& a, const float* p, float
   }
 }
 
-// Adds the adapters of 32 rows to CB blocks of 32 x 32 sums (MFMA layout: lane
-// (c, h), register r: row 8 (r / 4) + 4h + r % 4, column c).  row: the lane's
-// row c in X, or -1; col[cb]: its column of block cb.  Each adapter that stands
-// among the rows is multiplied once for all of them and added to its own rows
-// alone; `part` of `parts` callers takes every parts-th adapter.  A x (fp32)
-// becomes 2^e (high + low fp16 half), both halves exact products with B.
+// The adapters of 32 rows, added to CB blocks of 32 x 32 sums (MFMA layout:
+// lane (c, h), register r: row 8 (r / 4) + 4h + r % 4, column c).  Each adapter
+// that stands among the rows is multiplied once for all of them and added to
+// its own rows alone; `part` of `parts` callers takes every parts-th adapter.
+// A x (fp32) becomes 2^e (high + low fp16 half), both halves exact products
+// with B, 64 ranks at a time.  begin() requests A x and the first adapter's B,
+// so that a caller can do so before its own loop; add() finishes.
 template <int CB>
-__device__ __forceinline__ void add_adapters(const RowsArgs& a, int64_t row, const int (&col)[CB],
-                                             int part, int parts, f32x16 (&acc)[CB]) {
-  const int h = lane_id() >> 5;
-  const int id = row >= 0 ? a.ids[row] : -1;
-  const bool has = (uint32_t)id < (uint32_t)a.slots;
-  uint32_t left = (uint32_t)__builtin_amdgcn_ballot_w64(has);
-  if (left == 0) return;
-  // the rows' powers of two (a lane holds half of its row's entries)
-  const float* tp = a.t + (has ? row : 0) * a.rp + 8 * h;
-  float top = 0.f;
-  for (int q = 0; q < a.rp; q += 16) {
-    float v[8];
-    load_t8(a, tp + q, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(v[i]));
+struct RowAdapters {
+  int64_t row;            // the lane's row c in X that has an adapter, or -1
+  int id, skip, parts, slot;
+  uint32_t all, left, mine;
+  int64_t b0[CB];         // the lane's columns of B
+  float t[4][8];
+  f16x8 bf[CB][4];
+
+  // This caller's next adapter of those left: its slot and rows (0: none).
+  __device__ __forceinline__ void next() {
+    mine = 0;
+    while (left != 0) {
+      const int s = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+      const uint32_t m = (uint32_t)__builtin_amdgcn_ballot_w64(row >= 0 && id == s);
+      left &= ~m;
+      if (skip-- == 0) {
+        skip = parts - 1;
+        mine = m;
+        slot = s;
+        return;
+      }
+    }
   }
-  const float ts = half_scale(__builtin_fmaxf(top, __shfl_xor(top, 32)));
-  const float inv = 1.f / ts;              // a power of two: exact
-  for (int i = 0; left != 0; ++i) {
-    const int slot = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-    const uint32_t mine = (uint32_t)__builtin_amdgcn_ballot_w64(has && id == slot);
-    left &= ~mine;
-    if (i % parts != part) continue;
-    f32x16 hi[CB], lo[CB];
-    const uint16_t* bp[CB];
+  __device__ __forceinline__ void load_t(const RowsArgs& a, int r0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) load_t8(a, row >= 0 ? row : 0, r0 + 16 * q + 8 * (lane_id() >> 5), t[q]);
+  }
+  // B of the adapter, 64 ranks from r0 on (0 past the rank, where A x is 0 too)
+  __device__ __forceinline__ void load_b(const RowsArgs& a, int r0) {
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
+      const uint16_t* bp = a.b + ((int64_t)slot * a.n + b0[cb]) * a.rank;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) hi[cb][r] = lo[cb][r] = 0.f;
-      bp[cb] = a.b + ((int64_t)slot * a.n + min(col[cb], a.n - 1)) * a.rank + 8 * h;
-    }
-    for (int q = 0; q < a.rp; q += 16) {
-      float v[8];
-      load_t8(a, tp + q, v);
-      f16x8 th, tl;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = v[e] * inv;
-        th[e] = (f16)x;
-        tl[e] = (f16)(x - (float)th[e]);
+      for (int q = 0; q < 4; ++q) {
+        const int r = r0 + 16 * q + 8 * (lane_id() >> 5);
+        bf[cb][q] = u4_to_f16x8(r < a.rank ? *reinterpret_cast<const uint4*>(bp + r)
+                                           : make_uint4(0, 0, 0, 0));
       }
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-        // (past the rank A x is 0, the factor too)
-        const f16x8 bf = u4_to_f16x8(q + 8 * h < a.rank ? *reinterpret_cast<const uint4*>(bp[cb] + q)
-                                                        : make_uint4(0, 0, 0, 0));
-        hi[cb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(th, bf, hi[cb], 0, 0, 0);
-        lo[cb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(tl, bf, lo[cb], 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int rr = 8 * (r >> 2) + 4 * h + (r & 3);
-      const float f = __shfl(ts, rr);
-      // (a select, not a product with 0: another row's infinity stays its own)
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb)
-        acc[cb][r] += (mine >> rr) & 1 ? f * (hi[cb][r] + lo[cb][r]) : 0.f;
     }
   }
-}
+  // xrow: the lane's row c of X, or -1; col[cb]: its column of block cb
+  __device__ __forceinline__ void begin(const RowsArgs& a, int64_t xrow, const int (&col)[CB],
+                                        int part, int of) {
+    id = xrow >= 0 ? a.ids[xrow] : -1;
+    const bool has = (uint32_t)id < (uint32_t)a.slots;
+    row = has ? xrow : -1;
+    parts = of;
+    skip = part;
+    all = left = (uint32_t)__builtin_amdgcn_ballot_w64(has);
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) b0[cb] = min(col[cb], a.n - 1);
+    next();
+    if (mine == 0) return;
+    load_t(a, 0);
+    load_b(a, 0);
+  }
+  __device__ __forceinline__ void add(const RowsArgs& a, f32x16 (&acc)[CB]) {
+    if (mine == 0) return;
+    const int h = lane_id() >> 5;
+    // the rows' powers of two (a lane holds half of its row's entries)
+    float top = 0.f;
+    for (int r0 = 0; r0 < a.rp; r0 += 64) {
+      if (r0 > 0) load_t(a, r0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = __builtin_fmaxf(top, __builtin_fabsf(t[q][e]));
+    }
+    const float ts = half_scale(__builtin_fmaxf(top, __shfl_xor(top, 32)));
+    const float inv = 1.f / ts;            // a power of two: exact
+    float f[16];                           // of the lane's 16 rows
+#pragma unroll
+    for (int r = 0; r < 16; ++r) f[r] = __shfl(ts, 8 * (r >> 2) + 4 * h + (r & 3));
+    const int part = skip;
+    for (int r0 = 0; r0 < a.rp; r0 += 64) {
+      if (a.rp > 64) load_t(a, r0);
+      f16x8 th[4], tl[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = t[q][e] * inv;
+          th[q][e] = (f16)x;
+          tl[q][e] = (f16)(x - (float)th[q][e]);
+        }
+      const int nq = min(4, (a.rp - r0) / 16);
+      const int first = slot;
+      const uint32_t first_rows = mine, first_left = left;
+      while (true) {
+        const uint32_t rows = mine >> (4 * h);   // bit 8 (r / 4) + r % 4: register r's row
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+          f32x16 d = {};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q < nq) {
+              d = __builtin_amdgcn_mfma_f32_32x32x16_f16(th[q], bf[cb][q], d, 0, 0, 0);
+              d = __builtin_amdgcn_mfma_f32_32x32x16_f16(tl[q], bf[cb][q], d, 0, 0, 0);
+            }
+          if (cb + 1 == CB) {
+            // the next adapter's B on its way while this one is added
+            next();
+            if (mine != 0) load_b(a, r0);
+          }
+          // (a select, not a product with 0: another row's infinity stays its own)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float with = __builtin_fmaf(f[r], d[r], acc[cb][r]);
+            acc[cb][r] = (rows >> (8 * (r >> 2) + (r & 3))) & 1 ? with : acc[cb][r];
+          }
+        }
+        if (mine == 0) break;
+      }
+      if (r0 + 64 < a.rp) {
+        // the next 64 ranks: from the first adapter again
+        slot = first;
+        mine = first_rows;
+        left = first_left;
+        skip = part;
+        load_b(a, r0 + 64);
+      }
+    }
+  }
+};
 
 // --------------------------------------------------- few rows per expert --
-// Work-group: up to 32 rows of one expert x 32 columns (half a 64-row weight
-// tile; kSwiglu: of gate and of up).  Its waves take the K-blocks w, w +
-// WAVES, ..., U at a time with every load in flight before the first decode,
-// and add their sums in LDS in wave order.  Bound by the weights' bytes.
+// Work-group: up to 32 rows of one expert x 32 CB columns (half or all of a
+// 64-row weight tile; kSwiglu: of gate and of up).  Its waves take the K-blocks
+// w, w + WAVES, ..., U at a time with every load in flight before the first
+// decode, and add their sums in LDS in wave order.  Bound by the weights' bytes.
 // Lane (c, h) supplies X row c / weight row c and K positions 32h + 8s .. +7.
-template <int BITS, int MODE, int WAVES, int U>
+template <int BITS, int MODE, int WAVES, int CB, int U>
 __global__ __launch_bounds__(WAVES * 64) void k_rows_ksplit(const RowsArgs a) {
   constexpr int WPB = 2 * BITS;
   constexpr int HW = BITS;                   // words of a half block
   constexpr int NM = MODE == kSwiglu ? 2 : 1;
-  constexpr int NT = WAVES * 64;
-  constexpr int PT = 1024 / NT;              // outputs per thread
-  static_assert(16 % WAVES == 0, "reduction split");
-  __shared__ float red[WAVES][1024];
-  const RowTile rt = row_tile<MODE>(a, 32);
-  if (rt.rows <= 0) return;
-  const int gx = rt.col;
+  constexpr int PT = CB * 16 / WAVES;        // outputs per thread
+  static_assert(CB * 16 % WAVES == 0, "reduction split");
+  __shared__ float red[WAVES][CB * 1024];
+  const int y = blockIdx.x / a.cols, gx = blockIdx.x % a.cols;
   const int lane = lane_id(), wave = wave_id();
   const int c = lane & 31, h = lane >> 5;
-  const int t = gx >> 1, cb = gx & 1;
-  const uint32_t magic = vreg_const(kMagic);
-  // rows past the tile read its first row (never stored)
-  const int64_t xr = x_row<MODE>(a, rt.p0 + (c < rt.rows ? c : 0));
-  const uint16_t* xrow = a.X + xr * a.ldx + 32 * h;
-  const uint32_t* wsrc[NM];
-  const uint16_t* ssrc[NM];
-  const uint8_t* zsrc[NM];
-#pragma unroll
-  for (int i = 0; i < NM; ++i) {
-    wsrc[i] = a.codes[i] + rt.e * a.code_step + ((int64_t)t * a.kb * kTile + 32 * cb + c) * WPB;
-    const int64_t mt = rt.e * a.meta_step + (int64_t)t * a.G * kTile + 32 * cb + c;
-    ssrc[i] = a.scale[i] + mt;
-    zsrc[i] = a.zero[i] + mt;
+  const int t = CB == 2 ? gx : gx >> 1, cb0 = CB == 2 ? 0 : gx & 1;
+  int e = 0, p0 = 32 * y, rows = min(32, a.m - p0);
+  if constexpr (MODE != kLora) {
+    const int4 v = a.plan.tiles[y];          // (in flight with the number of tiles)
+    if (y >= *a.plan.ntiles) return;
+    e = v.x;
+    p0 = v.y;
+    rows = v.z;
   }
-  f32x16 acc[NM];
+  const uint32_t magic = vreg_const(kMagic);
+  const int64_t woff = ((int64_t)t * a.kb * kTile + 32 * cb0 + c) * WPB;
+  const int64_t moff = (int64_t)t * a.G * kTile + 32 * cb0 + c;
+  // rows past the tile read its first row (never stored)
+  const int64_t xr = x_row<MODE>(a, p0 + (c < rows ? c : 0));
+  const uint16_t* xrow = a.X + xr * a.ldx + 32 * h;
+  f32x16 acc[NM][CB];
 #pragma unroll
   for (int i = 0; i < NM; ++i)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[i][r] = 0.f;
+    for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][cb][r] = 0.f;
+  RowAdapters<CB> adapters;
+  int col[CB];
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb) col[cb] = t * kTile + 32 * (cb0 + cb) + c;
+  if constexpr (MODE == kLora) adapters.begin(a, c < rows ? xr : -1, col, wave, WAVES);
   for (int jb = wave; jb < a.kb; jb += WAVES * U) {
     f16x8 xa[U][4];
-    uint32_t wl[U][NM][HW];
-    uint16_t sr[U][NM];
-    int zc[U][NM];
+    uint32_t wl[U][NM][CB][HW];
+    uint16_t sr[U][NM][CB];
+    int zc[U][NM][CB];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = min(jb + WAVES * u, a.kb - 1);     // past the range: re-read, not used
+      const int64_t g = (a.G == 1) ? 0 : j;
+#pragma unroll
+      for (int i = 0; i < NM; ++i)
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+          const int64_t mi = e * a.meta_step + moff + g * kTile + 32 * cb;
+          sr[u][i][cb] = a.scale[i][mi];
+          zc[u][i][cb] = a.zero[i][mi];
+          load_half<BITS>(a.codes[i] + e * a.code_step + woff + ((int64_t)j * kTile + 32 * cb) * WPB,
+                          h, wl[u][i][cb]);
+        }
       const f16x8* xp = reinterpret_cast<const f16x8*>(xrow + (int64_t)j * kBlock);
 #pragma unroll
       for (int s = 0; s < 4; ++s) xa[u][s] = xp[s];
-      const int64_t g = (a.G == 1) ? 0 : j;
-#pragma unroll
-      for (int i = 0; i < NM; ++i) {
-        load_half<BITS>(wsrc[i] + (int64_t)j * kTile * WPB, h, wl[u][i]);
-        sr[u][i] = ssrc[i][g * kTile];
-        zc[u][i] = zsrc[i][g * kTile];
-      }
     }
     loads_issued();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (jb + WAVES * u >= a.kb) break;
 #pragma unroll
-      for (int i = 0; i < NM; ++i) {
-        const DeqT<BITS> d = make_deq_b<BITS>(1.f, zc[u][i]);
-        f32x16 blk;
+      for (int i = 0; i < NM; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) blk[r] = 0.f;
+        for (int cb = 0; cb < CB; ++cb) {
+          const DeqT<BITS> d = make_deq_b<BITS>(1.f, zc[u][i][cb]);
+          f32x16 blk = {};
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-          blk = __builtin_amdgcn_mfma_f32_32x32x16_f16(xa[u][s], int_half<BITS>(wl[u][i], s, d, magic),
-                                                       blk, 0, 0, 0);
-        const float sc = h2f(sr[u][i]);
+          for (int s = 0; s < 4; ++s)
+            blk = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                xa[u][s], int_half<BITS>(wl[u][i][cb], s, d, magic), blk, 0, 0, 0);
+          const float sc = h2f(sr[u][i][cb]);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][r] = __builtin_fmaf(sc, blk[r], acc[i][r]);
-      }
+          for (int r = 0; r < 16; ++r) acc[i][cb][r] = __builtin_fmaf(sc, blk[r], acc[i][cb][r]);
+        }
     }
   }
-  const int col = t * kTile + 32 * cb + c;
-  if constexpr (MODE == kLora) {
-    const int cols[1] = {col};
-    add_adapters<1>(a, c < rt.rows ? xr : -1, cols, wave, WAVES, acc);
-  }
-  // thread (wave, lane) finishes registers wave, wave + WAVES, ...
+  if constexpr (MODE == kLora) adapters.add(a, acc[0]);
+  // thread (wave, lane) finishes registers wave, wave + WAVES, ... of the CB x 16
   float v[NM][PT];
 #pragma unroll
   for (int i = 0; i < NM; ++i) {
     if (i > 0) __syncthreads();
 #pragma unroll
-    for (int r = 0; r < 16; ++r) red[wave][64 * r + lane] = acc[i][r];
+    for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) red[wave][1024 * cb + 64 * r + lane] = acc[i][cb][r];
     __syncthreads();
 #pragma unroll
     for (int p = 0; p < PT; ++p) {
@@ -329,20 +402,125 @@ __global__ __launch_bounds__(WAVES * 64) void k_rows_ksplit(const RowsArgs a) {
   }
 #pragma unroll
   for (int p = 0; p < PT; ++p) {
-    const int r = wave + WAVES * p;
+    const int r = (wave + WAVES * p) & 15;
+    const int cl = t * kTile + 32 * (cb0 + ((wave + WAVES * p) >> 4)) + c;
     const int row = 8 * (r >> 2) + 4 * h + (r & 3);
-    if (row >= rt.rows || col >= a.n) continue;
+    if (row >= rows || cl >= a.n) continue;
     if constexpr (MODE == kSwiglu) {
       const float hv = silu(v[0][p]) * v[1][p];
-      a.y16[(int64_t)(rt.p0 + row) * a.ldy + col] = __builtin_bit_cast(uint16_t, (f16)hv);
+      a.y16[(int64_t)(p0 + row) * a.ldy + cl] = __builtin_bit_cast(uint16_t, (f16)hv);
     } else if constexpr (MODE == kDown) {
-      const int64_t pair = a.plan.order[rt.p0 + row];
-      a.y[pair * a.ldy + col] = a.weights[pair] * v[0][p];
+      const int64_t pair = a.plan.order[p0 + row];
+      a.y[pair * a.ldy + cl] = a.weights[pair] * v[0][p];
     } else {
-      const int64_t o = x_row<MODE>(a, rt.p0 + row) * a.ldy + col;
+      const int64_t o = x_row<MODE>(a, p0 + row) * a.ldy + cl;
       if (a.y != nullptr) a.y[o] = v[0][p];
       if (a.y16 != nullptr) a.y16[o] = __builtin_bit_cast(uint16_t, (f16)v[0][p]);
     }
+  }
+}
+
+// ---------------------------------------------------------------- one row --
+// Work-group: 8 outputs of one (token, slot) pair (kSwiglu, from gate and up)
+// or of one token (kToken: the K-blocks of all its slots, each with its own row
+// of h, its own weights and its weight beside the group's scale).  Lane 8r + g:
+// weight row r, eighth g of every block, decoded and multiplied by vector dot
+// products: with one row of X the matrix cores would be idle in 31 of 32 rows,
+// and 8 outputs per work-group spread even a small product over all CUs (the
+// 2048 outputs of a token's down projections: 14.3 us as 64 work-groups of 32
+// columns).
+template <int BITS, int MODE, int WAVES, int U>
+__global__ __launch_bounds__(WAVES * 64) void k_rows_gemv(const RowsArgs a) {
+  constexpr int WPB = 2 * BITS;
+  constexpr int NG = 8;
+  constexpr int NM = MODE == kSwiglu ? 2 : 1;
+  constexpr int SW = SliceWords<BITS, NG>::n;
+  __shared__ float red[NM][WAVES][8];
+  const uint32_t magic = vreg_const(kMagic);
+  const int lane = lane_id(), wave = wave_id();
+  const int r = lane / NG, g = lane % NG;
+  const int y = blockIdx.x / a.cols, gx = blockIdx.x % a.cols;
+  const int t = gx >> 3, R = 8 * (gx & 7) + r;
+  int e = 0;
+  if constexpr (MODE == kSwiglu) {
+    e = a.ids[y];
+    if ((uint32_t)e >= (uint32_t)a.experts) return;
+  }
+  const int64_t xr = MODE == kToken ? (int64_t)y * a.top_k : y / a.top_k;
+  const uint16_t* x = a.X + xr * a.ldx + 8 * g;
+  const int64_t woff = ((int64_t)t * a.kb * kTile + R) * WPB;
+  const int64_t moff = (int64_t)t * a.G * kTile + R;
+  float acc[NM];
+#pragma unroll
+  for (int i = 0; i < NM; ++i) acc[i] = 0.f;
+  const int items = MODE == kToken ? a.top_k * a.kb : a.kb;
+  for (int it = wave; it < items; it += WAVES * U) {
+    uint32_t wd[U][NM][SW];
+    uint16_t sr[U][NM];
+    int zc[U][NM];
+    uint4 xv[U];
+    float fw[U];
+    bool use[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // past the range: the last item again, not used
+      const int n = min(it + WAVES * u, items - 1);
+      int j = n, ex = e;
+      const uint16_t* xp = x;
+      use[u] = it + WAVES * u < items;
+      fw[u] = 1.f;
+      if constexpr (MODE == kToken) {
+        const int slot = n / a.kb;
+        j = n % a.kb;
+        ex = a.ids[(int64_t)y * a.top_k + slot];
+        const bool there = (uint32_t)ex < (uint32_t)a.experts;
+        use[u] = use[u] && there;
+        ex = there ? ex : 0;
+        fw[u] = a.weights[(int64_t)y * a.top_k + slot];
+        xp += slot * a.ldx;
+      }
+      const int64_t mi = (a.G == 1 ? 0 : j) * (int64_t)kTile + moff;
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+        load_slice_words<BITS, NG>(a.codes[i] + ex * a.code_step + woff + (int64_t)j * kTile * WPB, g,
+                                   wd[u][i]);
+        sr[u][i] = a.scale[i][ex * a.meta_step + mi];
+        zc[u][i] = a.zero[i][ex * a.meta_step + mi];
+      }
+      xv[u] = *reinterpret_cast<const uint4*>(xp + (int64_t)j * kBlock);
+    }
+    loads_issued();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!use[u]) continue;
+      const f16x2 xs[4] = {as_h2(xv[u].x), as_h2(xv[u].y), as_h2(xv[u].z), as_h2(xv[u].w)};
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+        const float s = MODE == kToken ? fw[u] * h2f(sr[u][i]) : h2f(sr[u][i]);
+        acc[i] = __builtin_fmaf(s, slice_dot<BITS, NG>(wd[u][i], xs, zc[u][i], g, magic), acc[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NM; ++i) {
+    acc[i] = slice_sum<NG>(acc[i]);
+    if (g == 0) red[i][wave][r] = acc[i];
+  }
+  lds_barrier();
+  if (wave != 0 || lane >= 8) return;
+  float tot[NM];
+#pragma unroll
+  for (int i = 0; i < NM; ++i) {
+    tot[i] = red[i][0][lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) tot[i] += red[i][w][lane];
+  }
+  const int64_t o = (int64_t)y * a.ldy + t * kTile + 8 * (gx & 7) + lane;   // (n % 64 == 0)
+  if constexpr (MODE == kSwiglu) {
+    a.y16[o] = __builtin_bit_cast(uint16_t, (f16)(silu(tot[0]) * tot[1]));
+  } else {
+    if (a.y != nullptr) a.y[o] = tot[0];
+    if (a.y16 != nullptr) a.y16[o] = __builtin_bit_cast(uint16_t, (f16)tot[0]);
   }
 }
 
@@ -506,9 +684,11 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
   if constexpr (MODE == kLora) {
     const int cols[1] = {col};
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
-      add_adapters<1>(a, 32 * rb + c < rt.rows ? x_row<MODE>(a, rt.p0 + 32 * rb + c) : -1, cols, 0,
-                      1, reinterpret_cast<f32x16(&)[1]>(acc[rb]));
+    for (int rb = 0; rb < RB; ++rb) {
+      RowAdapters<1> adapters;
+      adapters.begin(a, 32 * rb + c < rt.rows ? x_row<MODE>(a, rt.p0 + 32 * rb + c) : -1, cols, 0, 1);
+      adapters.add(a, reinterpret_cast<f32x16(&)[1]>(acc[rb]));
+    }
   }
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb)

@@ -37,9 +37,8 @@ int64_t tile_bound(int64_t count, int buckets, int height) {
 
 RowPlan take_plan(Arena& ar, int64_t count, int buckets, int height) {
   RowPlan p;
-  p.offs = ar.take<int32_t>(buckets + 2);
   p.order = ar.take<int32_t>(count);
-  p.tiles = ar.take<int32_t>(2 * tile_bound(count, buckets, height));
+  p.tiles = ar.take<int4>(tile_bound(count, buckets, height));
   p.ntiles = ar.take<int32_t>(1);
   return p;
 }
@@ -76,9 +75,15 @@ bool stack_overlaps(const qlin_weight* w, int64_t experts, Range r) {
 }
 
 // ---------------------------------------------------------------- experts --
+// Up to this many (token, slot) pairs each pair reads its expert's weights by
+// itself: no plan, and a token's slots are added by the work-group that
+// multiplies them.
+constexpr int kDirectPairs = 32;
+
 struct MoePlan {
   int64_t pairs;
-  RowsCfg cfg;
+  bool direct;
+  RowsCfg up, down;    // forms of the two products
   RowPlan rows;
   uint16_t* h;
   float* d;
@@ -86,14 +91,29 @@ struct MoePlan {
 };
 
 MoePlan moe_plan(int inner, int model, int experts, int m, int top_k, void* ws) {
-  MoePlan p;
+  MoePlan p{};
   p.pairs = (int64_t)m * top_k;
-  p.cfg.height = p.pairs >= 16 * (int64_t)experts ? 64 : 32;
-  p.cfg.tiles = (int)tile_bound(p.pairs, experts, p.cfg.height);
+  p.direct = p.pairs <= kDirectPairs;
+  const int height = p.direct ? 1 : p.pairs >= 16 * (int64_t)experts ? 64 : 32;
+  p.up.height = p.down.height = height;
+  const int ki = inner / kBlock, km = model / kBlock;
+  if (p.direct) {
+    p.up.tiles = (int)p.pairs;
+    p.down.tiles = m;
+    p.up.waves = km > 32 ? 16 : 8;
+    p.down.waves = top_k * ki > 32 ? 16 : 8;
+  } else {
+    p.up.tiles = p.down.tiles = (int)tile_bound(p.pairs, experts, height);
+    const int64_t used = p.pairs < experts ? p.pairs : experts;   // at most
+    ksplit_form(p.up, km, tiles_of(inner) * used);
+    ksplit_form(p.down, ki, tiles_of(model) * used);
+  }
   Arena ar{static_cast<char*>(ws)};
-  p.rows = take_plan(ar, p.pairs, experts, p.cfg.height);
   p.h = ar.take<uint16_t>(p.pairs * inner);
-  p.d = ar.take<float>(p.pairs * model);
+  if (!p.direct) {
+    p.rows = take_plan(ar, p.pairs, experts, height);
+    p.d = ar.take<float>(p.pairs * model);
+  }
   p.bytes = ar.at;
   return p;
 }
@@ -135,6 +155,7 @@ LoraPlan lora_plan(const qlin_weight* w, const qlin_adapters* ad, int m, void* w
   LoraPlan p{};
   p.cfg.height = m >= 1024 ? 64 : 32;
   p.cfg.tiles = (m + p.cfg.height - 1) / p.cfg.height;
+  ksplit_form(p.cfg, w->k / kBlock, tiles_of(w->n) * p.cfg.tiles);
   p.rp = (ad->rank + 15) / 16 * 16;
   p.sorted = m >= kSortRows;
   p.splits = 1;
@@ -228,7 +249,7 @@ qlin_status qlin_moe_mlp(const qlin_weight* gate, const qlin_weight* up, const q
     return QLIN_ERR_ALIGN;
   const int inner = gate->n, model = gate->k;
   const MoePlan p = moe_plan(inner, model, experts, m, top_k, workspace);
-  if (!rows_fits(inner, kSwiglu, p.cfg) || !rows_fits(model, kDown, p.cfg)) return QLIN_ERR_SHAPE;
+  if (!rows_fits(inner, kSwiglu, p.up) || !rows_fits(model, kDown, p.down)) return QLIN_ERR_SHAPE;
   if (workspace == nullptr || workspace_bytes < p.bytes) return QLIN_ERR_WORKSPACE;
   const int64_t span = (int64_t)(m - 1) * ld_y + model;
   const Range out[3] = {range_of(workspace, workspace_bytes),
@@ -247,8 +268,9 @@ qlin_status qlin_moe_mlp(const qlin_weight* gate, const qlin_weight* up, const q
   }
   st = check_device();
   if (st != QLIN_OK) return st;
-  hipLaunchKernelGGL(k_rows_plan, dim3(1), dim3(kPlanWaves * 64), 0, stream, ids, (int)p.pairs,
-                     experts, p.cfg.height, p.rows);
+  if (!p.direct)
+    hipLaunchKernelGGL(k_rows_plan, dim3(1), dim3(kPlanWaves * 64), 0, stream, ids, (int)p.pairs,
+                       experts, p.up.height, p.rows);
   RowsArgs a{};
   set_weight(a, 0, gate);
   set_weight(a, 1, up);
@@ -257,9 +279,11 @@ qlin_status qlin_moe_mlp(const qlin_weight* gate, const qlin_weight* up, const q
   a.m = m;
   a.top_k = top_k;
   a.plan = p.rows;
+  a.experts = experts;
+  a.ids = ids;
   a.y16 = p.h;
   a.ldy = inner;
-  run_rows(a, gate->bits, kSwiglu, p.cfg, stream);
+  run_rows(a, gate->bits, kSwiglu, p.up, stream);
   RowsArgs b{};
   set_weight(b, 0, down);
   b.X = p.h;
@@ -267,13 +291,22 @@ qlin_status qlin_moe_mlp(const qlin_weight* gate, const qlin_weight* up, const q
   b.m = m;
   b.top_k = top_k;
   b.plan = p.rows;
+  b.experts = experts;
+  b.ids = ids;
   b.weights = weights;
+  if (p.direct) {
+    b.y = Y;
+    b.y16 = Y16;
+    b.ldy = ld_y;
+    run_rows(b, down->bits, kToken, p.down, stream);
+    return hip_status(hipGetLastError());
+  }
   b.y = p.d;
   b.ldy = model;
-  run_rows(b, down->bits, kDown, p.cfg, stream);
+  run_rows(b, down->bits, kDown, p.down, stream);
   const int64_t groups = ((int64_t)m * (model / 4) + 255) / 256;
-  hipLaunchKernelGGL(k_rows_combine, dim3((unsigned)(groups < 65536 ? groups : 65536)), dim3(256), 0, stream,
-                     p.d, ids, m, top_k, experts, model, Y, Y16, ld_y);
+  hipLaunchKernelGGL(k_rows_combine, dim3((unsigned)(groups < 65536 ? groups : 65536)), dim3(256),
+                     0, stream, p.d, ids, m, top_k, experts, model, Y, Y16, ld_y);
   return hip_status(hipGetLastError());
 }
 

@@ -9,12 +9,21 @@ constexpr int kB = QLIN_INST_BITS;
 
 template <int B, int MODE>
 void launch_mode(const RowsArgs& a, RowsCfg c, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.cols * c.tiles));
-  if (c.height == 32) {
-    constexpr int W = 8, U = MODE == kSwiglu ? 1 : 2;
-    hipLaunchKernelGGL((k_rows_ksplit<B, MODE, W, U>), grid, dim3(W * 64), 0, st, a);
-  } else {
-    hipLaunchKernelGGL((k_rows_tiled<B, MODE, 2, 4>), grid, dim3(256), 0, st, a);
+  const dim3 grid((unsigned)((int64_t)a.cols * c.tiles)), block(c.height == 64 ? 256 : 64 * c.waves);
+  if constexpr (MODE == kSwiglu || MODE == kToken) {
+    if (c.height == 1) {
+      if (c.waves == 16) hipLaunchKernelGGL((k_rows_gemv<B, MODE, 16, 4>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((k_rows_gemv<B, MODE, 8, 4>), grid, block, 0, st, a);
+      return;
+    }
+  }
+  if constexpr (MODE != kToken) {
+    constexpr int U = MODE == kSwiglu && B > 4 ? 1 : 2;   // by the registers of a block
+    if (c.height == 64) hipLaunchKernelGGL((k_rows_tiled<B, MODE, 2, 4>), grid, block, 0, st, a);
+    else if (c.half) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 8, 1, 2>), grid, block, 0, st, a);
+    else if (c.waves == 8) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 8, 2, U>), grid, block, 0, st, a);
+    else if (c.waves == 4) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 4, 2, U>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 2, 2, U>), grid, block, 0, st, a);
   }
 }
 
@@ -24,7 +33,8 @@ void launch_rows(const RowsArgs& args, int mode, RowsCfg c, hipStream_t st) {
   a.cols = rows_cols(a.n, mode, c);
   if (mode == kSwiglu) launch_mode<B, kSwiglu>(a, c, st);
   else if (mode == kDown) launch_mode<B, kDown>(a, c, st);
-  else launch_mode<B, kLora>(a, c, st);
+  else if (mode == kLora) launch_mode<B, kLora>(a, c, st);
+  else launch_mode<B, kToken>(a, c, st);
 }
 
 template void launch_rows<kB>(const RowsArgs&, int, RowsCfg, hipStream_t);

@@ -6,24 +6,37 @@
 
 namespace qlin {
 
-// The work-group form of a product over rows: 32 rows x 32 columns with K over
-// the waves, or 64 rows x 128 columns (kSwiglu: half as many of each matrix).
+// The work-group form of a product over rows: one row x 8 columns (kSwiglu,
+// kToken), up to 32 rows x 32 or 64 columns with K over 2 .. 16 waves, or 64
+// rows x 128 columns (kSwiglu: half as many of each matrix).
 struct RowsCfg {
-  int height;          // rows of X per work-group
+  int height;          // rows of X per work-group: 1, 32 or 64
   int tiles;           // row tiles of the grid (those past the plan's end exit)
+  int waves;           // (1 and 32 rows) waves per work-group
+  bool half;           // (32 rows) 32 columns per work-group
 };
+
+// (32 rows) The form for kb K-blocks and about `groups` work-groups of 64
+// columns.  A wave keeps 2 blocks in flight, so the work-group is sized to cover
+// K in few rounds of loads; a grid that would leave half of the CUs empty takes
+// 32 columns per work-group.
+inline void ksplit_form(RowsCfg& c, int kb, int64_t groups) {
+  c.half = groups < 128;
+  c.waves = c.half || kb > 32 ? 8 : kb > 8 ? 4 : 2;
+}
 
 // Work-group columns of a product with n outputs per row.
 inline int rows_cols(int n, int mode, RowsCfg c) {
   const int tiles = (n + kTile - 1) / kTile;
-  if (c.height == 32) return 2 * tiles;
+  if (c.height == 1) return 8 * tiles;
+  if (c.height == 32) return c.half ? 2 * tiles : tiles;
   return mode == kSwiglu ? tiles : (tiles + 1) / 2;
 }
 
 // Whether the grid of such a product can be launched (HIP counts threads in
 // 32 bits).
 inline bool rows_fits(int n, int mode, RowsCfg c) {
-  return (int64_t)rows_cols(n, mode, c) * c.tiles * 512 < ((int64_t)1 << 32);
+  return (int64_t)rows_cols(n, mode, c) * c.tiles * (c.height == 64 ? 256 : 64 * c.waves) < ((int64_t)1 << 32);
 }
 
 template <int B>
