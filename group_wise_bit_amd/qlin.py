@@ -532,38 +532,60 @@ def _same_device(dev: torch.device, named) -> None:
             raise ValueError(f"{name} is on {t.device}, the inputs on {dev}")
 
 
-class _on_device:
-    """The tensors' device made current for a call (a no-op where it is)."""
-
-    def __init__(self, dev: torch.device):
-        if dev.type != "cuda":
-            raise ValueError(f"the tensors must be on a GPU, not on {dev}")
-        self.guard = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+# The current stream's handle without the wrapper object torch.cuda.current_stream()
+# builds (about 3 us of a call's 12), where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _rows_workspace(ws, need: int, dev: torch.device) -> Optional[torch.Tensor]:
-    """The workspace of a row-wise call: the caller's, or the device and
-    stream's own.  Under stream capture a buffer of the graph's own memory:
-    one that a later, larger call may replace must not be recorded."""
-    if not isinstance(ws, str):
-        if ws is not None and ws.device != dev:
-            raise ValueError(f"ws is on {ws.device}, the inputs on {dev}")
-        if ws is not None and not ws.is_contiguous():
-            raise ValueError("ws must be contiguous")
-        return ws
-    if need <= 0:
-        return None
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    return workspace(need, dev)
+def _launch(dev: torch.device, call):
+    """call(raw stream) with the tensors' device current and its current stream."""
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be on a GPU, not on {dev}")
+    if dev.index == torch.cuda.current_device():
+        return call(_raw_stream(dev.index))
+    with torch.cuda.device(dev):
+        return call(_raw_stream(dev.index))
+
+
+def _with_workspace(ws, dev: torch.device, need, call, where: str) -> None:
+    """call(workspace pointer, bytes, raw stream) with the caller's workspace or
+    the device and stream's own (grown to need() bytes when the library finds
+    it too small, before any launch).  Under stream capture a buffer of the
+    graph's own memory: one that a later, larger call may replace must not be
+    recorded."""
+    def run(stream):
+        if not isinstance(ws, str):
+            if ws is None:
+                return call(None, 0, stream)
+            if ws.device != dev:
+                raise ValueError(f"ws is on {ws.device}, the inputs on {dev}")
+            if not ws.is_contiguous():
+                raise ValueError("ws must be contiguous")
+            return call(ws.data_ptr(), ws.numel() * ws.element_size(), stream)
+        if torch.cuda.is_current_stream_capturing():
+            size = need()
+            own = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
+            return call(_ptr(own), size, stream)
+        buf = _WS.get((dev.index, stream))
+        st = call(None, 0, stream) if buf is None else call(buf.data_ptr(), buf.numel(), stream)
+        if st == 8:                           # QLIN_ERR_WORKSPACE
+            buf = workspace(need(), dev)
+            st = call(_ptr(buf), 0 if buf is None else buf.numel(), stream)
+        return st
+    _check(_launch(dev, run), where)
+
+
+class _CStruct:
+    """The ctypes form of an object of tensors, built and checked again only
+    when one of its tensors is another (or has moved or changed its size)."""
+
+    def _cached(self, tensors, extra, build):
+        key = (*[(t.data_ptr(), t.numel(), t.dtype) for t in tensors if t is not None], *extra)
+        got = self.__dict__.get("_c")
+        if got is None or got[0] != key:
+            got = self.__dict__["_c"] = (key, build())
+        return got[1]
 
 
 def _need_rows_x(X: torch.Tensor, k: int) -> None:
@@ -585,27 +607,29 @@ def _need_flat(t: torch.Tensor, dtype: torch.dtype, shape: Tuple[int, ...], name
 
 def _row_outputs(m: int, n: int, dev, Y, Y16, want_y: bool, want_y16: bool):
     """fp32 and fp16 [m, n] outputs of a row-wise product and their common row stride."""
+    ld = n
+    if Y is not None or Y16 is not None:
+        given = [(t, dtype, name) for t, dtype, name in ((Y, torch.float32, "Y"),
+                                                         (Y16, torch.float16, "Y16"))
+                 if t is not None]
+        for t, dtype, name in given:
+            if m:
+                _need_out(t, dtype, dev, m, n, name)
+        if m > 1:
+            ld = given[0][0].stride(0)
+            if given[-1][0].stride(0) != ld or (len(given) < 2 and want_y and want_y16 and ld != n):
+                raise ValueError("Y and Y16 must share one row stride")
+    elif not want_y and not want_y16:
+        raise ValueError("one of Y and Y16 must be wanted")
     if Y is None and want_y:
         Y = torch.empty(m, n, dtype=torch.float32, device=dev)
     if Y16 is None and want_y16:
         Y16 = torch.empty(m, n, dtype=torch.float16, device=dev)
-    outs = []
-    for t, dtype, name in ((Y, torch.float32, "Y"), (Y16, torch.float16, "Y16")):
-        if t is not None:
-            _need_out(t, dtype, dev, m, n, name) if m else None
-            outs.append(t)
-    if not outs:
-        raise ValueError("one of Y and Y16 must be wanted")
-    ld = _row_pitch(outs[0])
-    if m > 1 and any(t.stride(0) != ld for t in outs):
-        raise ValueError("Y and Y16 must share one row stride")
-    if m <= 1:
-        ld = n
     return Y, Y16, ld
 
 
-@dataclass
-class Router:
+@dataclass(eq=False)
+class Router(_CStruct):
     """How route() turns logits into experts (qlin_router in qlin_rows.h)."""
     experts: int
     top_k: int
@@ -618,6 +642,11 @@ class Router:
     scale: float = 1.0
 
     def c_struct(self) -> QlinRouterC:
+        return self._cached((self.bias,), (self.experts, self.top_k, self.score, self.groups,
+                                           self.top_groups, self.group_top, self.renormalize,
+                                           self.scale), self._build)
+
+    def _build(self) -> QlinRouterC:
         if self.score not in ("softmax", "sigmoid"):
             raise ValueError("score must be 'softmax' or 'sigmoid'")
         if self.bias is not None:
@@ -639,22 +668,24 @@ def route(router: Router, logits: torch.Tensor, ids: Optional[torch.Tensor] = No
     c = router.c_struct()
     if router.top_k < 1:
         raise ValueError("top_k must be at least 1")
+    shape = (m, router.top_k)
     if ids is None:
-        ids = torch.empty(m, router.top_k, dtype=torch.int32, device=dev)
+        ids = torch.empty(shape, dtype=torch.int32, device=dev)
+    else:
+        _need_flat(ids, torch.int32, shape, "ids")
     if weights is None:
-        weights = torch.empty(m, router.top_k, dtype=torch.float32, device=dev)
-    _need_flat(ids, torch.int32, (m, router.top_k), "ids")
-    _need_flat(weights, torch.float32, (m, router.top_k), "weights")
+        weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _need_flat(weights, torch.float32, shape, "weights")
     _same_device(dev, (("bias", router.bias), ("ids", ids), ("weights", weights)))
-    with _on_device(dev):
-        st = _lib().qlin_route(ctypes.byref(c), logits.data_ptr(), m, _row_pitch(logits),
-                               ids.data_ptr(), weights.data_ptr(), _stream())
-    _check(st, "qlin_route")
+    _check(_launch(dev, lambda stream: _lib().qlin_route(
+        ctypes.byref(c), logits.data_ptr(), m, _row_pitch(logits), ids.data_ptr(),
+        weights.data_ptr(), stream)), "qlin_route")
     return ids, weights
 
 
-@dataclass
-class QExperts:
+@dataclass(eq=False)
+class QExperts(_CStruct):
     """A stack of packed weights of one shape, expert after expert (the layout
     qlin_moe_mlp takes): each tensor holds `count` times one QWeight's."""
     count: int
@@ -667,6 +698,10 @@ class QExperts:
     zero: torch.Tensor
 
     def c_struct(self) -> QlinWeightC:
+        return self._cached((self.data, self.scale, self.zero),
+                            (self.count, self.n, self.k, self.bits, self.group), self._build)
+
+    def _build(self) -> QlinWeightC:
         words = self.count * (packed_bytes(self.n, self.k, self.bits) // 4)
         entries = self.count * meta_entries(self.n, self.k, self.group)
         for t, dtype, size, name in ((self.data, torch.int32, words, "data"),
@@ -703,9 +738,9 @@ def quantize_experts(w16: torch.Tensor, bits: int, group) -> QExperts:
     q = QExperts(count, n, k, bits, g, torch.empty(count * words, dtype=torch.int32, device=dev),
                  torch.empty(count * entries, dtype=torch.float16, device=dev),
                  torch.empty(count * entries, dtype=torch.uint8, device=dev))
-    with _on_device(dev):
-        quantize_batch([w16[e] for e in range(count)], bits, "K" if g != 64 else 64,
-                       outs=[q.expert(e) for e in range(count)])
+    _launch(dev, lambda stream: quantize_batch(
+        [w16[e] for e in range(count)], bits, "K" if g != 64 else 64,
+        outs=[q.expert(e) for e in range(count)]))
     return q
 
 
@@ -728,25 +763,18 @@ def moe_mlp(gate: QExperts, up: QExperts, down: QExperts, X: torch.Tensor, ids: 
     _same_device(dev, (("gate", gate.data), ("up", up.data), ("down", down.data), ("ids", ids),
                        ("weights", weights)))
     Y, Y16, ld = _row_outputs(m, down.n, dev, Y, Y16, want_y, want_y16)
-    g, u, d = gate.c_struct(), up.c_struct(), down.c_struct()
+    g, u, d = (ctypes.byref(w.c_struct()) for w in (gate, up, down))
     lib = _lib()
-    with _on_device(dev):
-        if isinstance(ws, str):
-            need = lib.qlin_moe_mlp_workspace_bytes(ctypes.byref(g), ctypes.byref(d), gate.count,
-                                                    m, top_k)
-        else:
-            need = 0
-        ws = _rows_workspace(ws, need, dev)
-        st = lib.qlin_moe_mlp(ctypes.byref(g), ctypes.byref(u), ctypes.byref(d), gate.count,
-                              X.data_ptr(), m, _row_pitch(X), ids.data_ptr(), weights.data_ptr(),
-                              top_k, _ptr(Y), _ptr(Y16), ld, _ptr(ws),
-                              0 if ws is None else ws.numel() * ws.element_size(), _stream())
-    _check(st, "qlin_moe_mlp")
+    _with_workspace(
+        ws, dev, lambda: lib.qlin_moe_mlp_workspace_bytes(g, d, gate.count, m, top_k),
+        lambda wp, wb, stream: lib.qlin_moe_mlp(
+            g, u, d, gate.count, X.data_ptr(), m, _row_pitch(X), ids.data_ptr(),
+            weights.data_ptr(), top_k, _ptr(Y), _ptr(Y16), ld, wp, wb, stream), "qlin_moe_mlp")
     return Y, Y16
 
 
-@dataclass
-class Adapters:
+@dataclass(eq=False)
+class Adapters(_CStruct):
     """A pool of low-rank adapters of one projection: a fp16 [slots, rank, k],
     b fp16 [slots, n, rank], scale fp32 [slots] or None (all 1)."""
     a: torch.Tensor
@@ -754,6 +782,10 @@ class Adapters:
     scale: Optional[torch.Tensor] = None
 
     def c_struct(self, w: "QWeight") -> QlinAdaptersC:
+        return self._cached((self.a, self.b, self.scale), (w.n, w.k, *self.a.shape, *self.b.shape),
+                            lambda: self._build(w))
+
+    def _build(self, w: "QWeight") -> QlinAdaptersC:
         if self.a.dim() != 3:
             raise TypeError("a must be a contiguous torch.float16 [slots, rank, k] tensor")
         slots, rank = self.a.shape[0], self.a.shape[1]
@@ -777,14 +809,11 @@ def gemm_lora(w: QWeight, X: torch.Tensor, adapters: Adapters, ids: torch.Tensor
     _same_device(dev, (("w", w.data), ("a", adapters.a), ("b", adapters.b),
                        ("scale", adapters.scale), ("ids", ids)))
     Y, Y16, ld = _row_outputs(m, w.n, dev, Y, Y16, want_y, want_y16)
-    c = w.c_struct()
+    c, a = ctypes.byref(w.c_struct()), ctypes.byref(ad)
     lib = _lib()
-    with _on_device(dev):
-        need = (lib.qlin_gemm_lora_workspace_bytes(ctypes.byref(c), ctypes.byref(ad), m)
-                if isinstance(ws, str) else 0)
-        ws = _rows_workspace(ws, need, dev)
-        st = lib.qlin_gemm_lora(ctypes.byref(c), ctypes.byref(ad), X.data_ptr(), m, _row_pitch(X),
-                                ids.data_ptr(), _ptr(Y), _ptr(Y16), ld, _ptr(ws),
-                                0 if ws is None else ws.numel() * ws.element_size(), _stream())
-    _check(st, "qlin_gemm_lora")
+    _with_workspace(
+        ws, dev, lambda: lib.qlin_gemm_lora_workspace_bytes(c, a, m),
+        lambda wp, wb, stream: lib.qlin_gemm_lora(
+            c, a, X.data_ptr(), m, _row_pitch(X), ids.data_ptr(), _ptr(Y), _ptr(Y16), ld, wp, wb,
+            stream), "qlin_gemm_lora")
     return Y, Y16
