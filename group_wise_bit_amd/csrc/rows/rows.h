@@ -63,6 +63,14 @@ __device__ __forceinline__ f16x8 int_half(const uint32_t* wl, int s, const DeqT<
   return r;
 }
 
+// p + a wave-uniform offset, then a lane's 32-bit offset: the form in which a
+// load takes its base from scalar registers and costs no vector address.
+template <typename T>
+__device__ __forceinline__ const T* lane_ptr(const T* p, int64_t uniform, uint32_t lane_off) {
+  return reinterpret_cast<const T*>(reinterpret_cast<const char*>(p + uniform) +
+                                    lane_off * (uint32_t)sizeof(T));
+}
+
 // ------------------------------------------------------------------ launches --
 // What a product over rows does with its sums:
 //   kSwiglu  two matrices (gate, up): fp16 silu(g) * u, one row per position
@@ -300,8 +308,10 @@ struct RowAdapters {
 // w, w + WAVES, ..., U at a time with every load in flight before the first
 // decode, and add their sums in LDS in wave order.  Bound by the weights' bytes.
 // Lane (c, h) supplies X row c / weight row c and K positions 32h + 8s .. +7.
+// (Two waves per SIMD at least: with the register file to itself the compiler
+// keeps the MFMA results in accumulation registers and copies every one out.)
 template <int BITS, int MODE, int WAVES, int CB, int U>
-__global__ __launch_bounds__(WAVES * 64) void k_rows_ksplit(const RowsArgs a) {
+__global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a) {
   constexpr int WPB = 2 * BITS;
   constexpr int HW = BITS;                   // words of a half block
   constexpr int NM = MODE == kSwiglu ? 2 : 1;
@@ -321,8 +331,10 @@ __global__ __launch_bounds__(WAVES * 64) void k_rows_ksplit(const RowsArgs a) {
     rows = v.z;
   }
   const uint32_t magic = vreg_const(kMagic);
-  const int64_t woff = ((int64_t)t * a.kb * kTile + 32 * cb0 + c) * WPB;
-  const int64_t moff = (int64_t)t * a.G * kTile + 32 * cb0 + c;
+  // uniform: expert e, tile t, columns from cb0 on; a lane: its row of 32
+  const int64_t woff = e * a.code_step + ((int64_t)t * a.kb * kTile + 32 * cb0) * WPB;
+  const int64_t moff = e * a.meta_step + (int64_t)t * a.G * kTile + 32 * cb0;
+  const uint32_t wlane = c * WPB, mlane = c;
   // rows past the tile read its first row (never stored)
   const int64_t xr = x_row<MODE>(a, p0 + (c < rows ? c : 0));
   const uint16_t* xrow = a.X + xr * a.ldx + 32 * h;
@@ -351,11 +363,11 @@ __global__ __launch_bounds__(WAVES * 64) void k_rows_ksplit(const RowsArgs a) {
       for (int i = 0; i < NM; ++i)
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
-          const int64_t mi = e * a.meta_step + moff + g * kTile + 32 * cb;
-          sr[u][i][cb] = a.scale[i][mi];
-          zc[u][i][cb] = a.zero[i][mi];
-          load_half<BITS>(a.codes[i] + e * a.code_step + woff + ((int64_t)j * kTile + 32 * cb) * WPB,
-                          h, wl[u][i][cb]);
+          const int64_t mi = moff + g * kTile + 32 * cb;
+          sr[u][i][cb] = *lane_ptr(a.scale[i], mi, mlane);
+          zc[u][i][cb] = *lane_ptr(a.zero[i], mi, mlane);
+          load_half<BITS>(lane_ptr(a.codes[i], woff + ((int64_t)j * kTile + 32 * cb) * WPB, wlane), h,
+                          wl[u][i][cb]);
         }
       const f16x8* xp = reinterpret_cast<const f16x8*>(xrow + (int64_t)j * kBlock);
 #pragma unroll
@@ -421,84 +433,89 @@ __global__ __launch_bounds__(WAVES * 64) void k_rows_ksplit(const RowsArgs a) {
 }
 
 // ---------------------------------------------------------------- one row --
-// Work-group: 8 outputs of one (token, slot) pair (kSwiglu, from gate and up)
-// or of one token (kToken: the K-blocks of all its slots, each with its own row
-// of h, its own weights and its weight beside the group's scale).  Lane 8r + g:
-// weight row r, eighth g of every block, decoded and multiplied by vector dot
-// products: with one row of X the matrix cores would be idle in 31 of 32 rows,
-// and 8 outputs per work-group spread even a small product over all CUs (the
-// 2048 outputs of a token's down projections: 14.3 us as 64 work-groups of 32
-// columns).
-template <int BITS, int MODE, int WAVES, int U>
+// Work-group: 64 / NG outputs of one (token, slot) pair (kSwiglu, from gate and
+// up) or of one token (kToken: the K-blocks of all its slots, each with its own
+// row of h, its own weights and its weight beside the group's scale).  Lane NG r
+// + g: weight row r, slice g of every block, decoded and multiplied by vector
+// dot products: with one row of X the matrix cores would be idle in 31 of 32
+// rows, and few outputs per work-group spread even a small product over all CUs
+// (the 2048 outputs of a token's down projections: 14.3 us as 64 work-groups of
+// 32 columns).  Bound by vector instructions and launch latency.
+template <int BITS, int MODE, int NG, int WAVES, int U>
 __global__ __launch_bounds__(WAVES * 64) void k_rows_gemv(const RowsArgs a) {
   constexpr int WPB = 2 * BITS;
-  constexpr int NG = 8;
+  constexpr int RW = 64 / NG;                // outputs per work-group
+  constexpr int XQ = 8 / NG;                 // 16-byte chunks of x per slice
   constexpr int NM = MODE == kSwiglu ? 2 : 1;
   constexpr int SW = SliceWords<BITS, NG>::n;
-  __shared__ float red[NM][WAVES][8];
+  __shared__ float red[NM][WAVES][RW];
   const uint32_t magic = vreg_const(kMagic);
   const int lane = lane_id(), wave = wave_id();
   const int r = lane / NG, g = lane % NG;
   const int y = blockIdx.x / a.cols, gx = blockIdx.x % a.cols;
-  const int t = gx >> 3, R = 8 * (gx & 7) + r;
+  const int t = gx / NG, r0 = RW * (gx % NG);
   int e = 0;
   if constexpr (MODE == kSwiglu) {
     e = a.ids[y];
     if ((uint32_t)e >= (uint32_t)a.experts) return;
   }
-  const int64_t xr = MODE == kToken ? (int64_t)y * a.top_k : y / a.top_k;
-  const uint16_t* x = a.X + xr * a.ldx + 8 * g;
-  const int64_t woff = ((int64_t)t * a.kb * kTile + R) * WPB;
-  const int64_t moff = (int64_t)t * a.G * kTile + R;
+  const int64_t woff = ((int64_t)t * a.kb * kTile + r0) * WPB, moff = (int64_t)t * a.G * kTile + r0;
   float acc[NM];
 #pragma unroll
   for (int i = 0; i < NM; ++i) acc[i] = 0.f;
-  const int items = MODE == kToken ? a.top_k * a.kb : a.kb;
-  for (int it = wave; it < items; it += WAVES * U) {
-    uint32_t wd[U][NM][SW];
-    uint16_t sr[U][NM];
-    int zc[U][NM];
-    uint4 xv[U];
-    float fw[U];
-    bool use[U];
+  // K-blocks j0, j0 + step, ... of one row of x by one expert's weights
+  auto product = [&](int ex, const uint16_t* xrow, float f, int j0, int step) __attribute__((always_inline)) {
+    const int64_t wo = ex * a.code_step + woff, mo = ex * a.meta_step + moff;
+    for (int jb = j0; jb < a.kb; jb += step * U) {
+      uint32_t wd[U][NM][SW];
+      uint16_t sr[U][NM];
+      int zc[U][NM];
+      uint4 xv[U][XQ];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // past the range: the last item again, not used
-      const int n = min(it + WAVES * u, items - 1);
-      int j = n, ex = e;
-      const uint16_t* xp = x;
-      use[u] = it + WAVES * u < items;
-      fw[u] = 1.f;
-      if constexpr (MODE == kToken) {
-        const int slot = n / a.kb;
-        j = n % a.kb;
-        ex = a.ids[(int64_t)y * a.top_k + slot];
-        const bool there = (uint32_t)ex < (uint32_t)a.experts;
-        use[u] = use[u] && there;
-        ex = there ? ex : 0;
-        fw[u] = a.weights[(int64_t)y * a.top_k + slot];
-        xp += slot * a.ldx;
-      }
-      const int64_t mi = (a.G == 1 ? 0 : j) * (int64_t)kTile + moff;
+      for (int u = 0; u < U; ++u) {
+        const int j = min(jb + step * u, a.kb - 1);        // past the range: re-read, not used
+        const int64_t mi = mo + (a.G == 1 ? 0 : j) * (int64_t)kTile;
 #pragma unroll
-      for (int i = 0; i < NM; ++i) {
-        load_slice_words<BITS, NG>(a.codes[i] + ex * a.code_step + woff + (int64_t)j * kTile * WPB, g,
-                                   wd[u][i]);
-        sr[u][i] = a.scale[i][ex * a.meta_step + mi];
-        zc[u][i] = a.zero[i][ex * a.meta_step + mi];
+        for (int i = 0; i < NM; ++i) {
+          load_slice_words<BITS, NG>(lane_ptr(a.codes[i], wo + (int64_t)j * kTile * WPB, r * WPB), g,
+                                     wd[u][i]);
+          sr[u][i] = *lane_ptr(a.scale[i], mi, r);
+          zc[u][i] = *lane_ptr(a.zero[i], mi, r);
+        }
+        const uint4* xp = reinterpret_cast<const uint4*>(lane_ptr(xrow, (int64_t)j * kBlock, 8 * XQ * g));
+#pragma unroll
+        for (int q = 0; q < XQ; ++q) xv[u][q] = xp[q];
       }
-      xv[u] = *reinterpret_cast<const uint4*>(xp + (int64_t)j * kBlock);
+      loads_issued();
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (jb + step * u >= a.kb) break;
+        f16x2 xs[4 * XQ];
+#pragma unroll
+        for (int q = 0; q < XQ; ++q) {
+          xs[4 * q] = as_h2(xv[u][q].x);
+          xs[4 * q + 1] = as_h2(xv[u][q].y);
+          xs[4 * q + 2] = as_h2(xv[u][q].z);
+          xs[4 * q + 3] = as_h2(xv[u][q].w);
+        }
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+          const float s = MODE == kToken ? f * h2f(sr[u][i]) : h2f(sr[u][i]);
+          acc[i] = __builtin_fmaf(s, slice_dot<BITS, NG>(wd[u][i], xs, zc[u][i], g, magic), acc[i]);
+        }
+      }
     }
-    loads_issued();
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (!use[u]) continue;
-      const f16x2 xs[4] = {as_h2(xv[u].x), as_h2(xv[u].y), as_h2(xv[u].z), as_h2(xv[u].w)};
-#pragma unroll
-      for (int i = 0; i < NM; ++i) {
-        const float s = MODE == kToken ? fw[u] * h2f(sr[u][i]) : h2f(sr[u][i]);
-        acc[i] = __builtin_fmaf(s, slice_dot<BITS, NG>(wd[u][i], xs, zc[u][i], g, magic), acc[i]);
-      }
+  };
+  if constexpr (MODE == kSwiglu) {
+    product(e, a.X + (int64_t)(y / a.top_k) * a.ldx, 1.f, wave, WAVES);
+  } else {
+    // `parts` waves per slot share its K-blocks (more slots than waves: in turn)
+    const int parts = max(1, WAVES / a.top_k);
+    for (int s = wave / parts; s < a.top_k; s += WAVES / parts) {
+      const int64_t pair = (int64_t)y * a.top_k + s;
+      const int ex = a.ids[pair];
+      if ((uint32_t)ex >= (uint32_t)a.experts) continue;
+      product(ex, a.X + pair * a.ldx, a.weights[pair], wave % parts, parts);
     }
   }
 #pragma unroll
@@ -507,7 +524,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_rows_gemv(const RowsArgs a) {
     if (g == 0) red[i][wave][r] = acc[i];
   }
   lds_barrier();
-  if (wave != 0 || lane >= 8) return;
+  if (wave != 0 || lane >= RW) return;
   float tot[NM];
 #pragma unroll
   for (int i = 0; i < NM; ++i) {
@@ -515,7 +532,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_rows_gemv(const RowsArgs a) {
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) tot[i] += red[i][w][lane];
   }
-  const int64_t o = (int64_t)y * a.ldy + t * kTile + 8 * (gx & 7) + lane;   // (n % 64 == 0)
+  const int64_t o = (int64_t)y * a.ldy + t * kTile + r0 + lane;   // (n % 64 == 0)
   if constexpr (MODE == kSwiglu) {
     a.y16[o] = __builtin_bit_cast(uint16_t, (f16)(silu(tot[0]) * tot[1]));
   } else {

@@ -100,8 +100,8 @@ MoePlan moe_plan(int inner, int model, int experts, int m, int top_k, void* ws) 
   if (p.direct) {
     p.up.tiles = (int)p.pairs;
     p.down.tiles = m;
-    p.up.waves = km > 32 ? 16 : 8;
-    p.down.waves = top_k * ki > 32 ? 16 : 8;
+    gemv_form(p.up, km, p.pairs * 4 * tiles_of(inner));
+    gemv_form(p.down, top_k * ki, (int64_t)m * 4 * tiles_of(model));
   } else {
     p.up.tiles = p.down.tiles = (int)tile_bound(p.pairs, experts, height);
     const int64_t used = p.pairs < experts ? p.pairs : experts;   // at most

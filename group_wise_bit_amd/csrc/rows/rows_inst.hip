@@ -12,8 +12,13 @@ void launch_mode(const RowsArgs& a, RowsCfg c, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)a.cols * c.tiles)), block(c.height == 64 ? 256 : 64 * c.waves);
   if constexpr (MODE == kSwiglu || MODE == kToken) {
     if (c.height == 1) {
-      if (c.waves == 16) hipLaunchKernelGGL((k_rows_gemv<B, MODE, 16, 4>), grid, block, 0, st, a);
-      else hipLaunchKernelGGL((k_rows_gemv<B, MODE, 8, 4>), grid, block, 0, st, a);
+      if (c.half) {
+        if (c.waves == 16) hipLaunchKernelGGL((k_rows_gemv<B, MODE, 8, 16, 4>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((k_rows_gemv<B, MODE, 8, 8, 4>), grid, block, 0, st, a);
+      } else {
+        if (c.waves == 16) hipLaunchKernelGGL((k_rows_gemv<B, MODE, 4, 16, 4>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((k_rows_gemv<B, MODE, 4, 8, 4>), grid, block, 0, st, a);
+      }
       return;
     }
   }

@@ -6,14 +6,14 @@
 
 namespace qlin {
 
-// The work-group form of a product over rows: one row x 8 columns (kSwiglu,
+// The work-group form of a product over rows: one row x 8 or 16 columns (kSwiglu,
 // kToken), up to 32 rows x 32 or 64 columns with K over 2 .. 16 waves, or 64
 // rows x 128 columns (kSwiglu: half as many of each matrix).
 struct RowsCfg {
   int height;          // rows of X per work-group: 1, 32 or 64
   int tiles;           // row tiles of the grid (those past the plan's end exit)
   int waves;           // (1 and 32 rows) waves per work-group
-  bool half;           // (32 rows) 32 columns per work-group
+  bool half;           // 32 columns per work-group (32 rows), 8 (one row)
 };
 
 // (32 rows) The form for kb K-blocks and about `groups` work-groups of 64
@@ -25,10 +25,17 @@ inline void ksplit_form(RowsCfg& c, int kb, int64_t groups) {
   c.waves = c.half || kb > 32 ? 8 : kb > 8 ? 4 : 2;
 }
 
+// (1 row) The form for `items` K-blocks and `groups` work-groups of 16 columns: a
+// wave keeps 4 blocks in flight; 8 columns where 16 would not reach every CU.
+inline void gemv_form(RowsCfg& c, int items, int64_t groups) {
+  c.half = groups < 256;
+  c.waves = items > 32 ? 16 : 8;
+}
+
 // Work-group columns of a product with n outputs per row.
 inline int rows_cols(int n, int mode, RowsCfg c) {
   const int tiles = (n + kTile - 1) / kTile;
-  if (c.height == 1) return 8 * tiles;
+  if (c.height == 1) return (c.half ? 8 : 4) * tiles;
   if (c.height == 32) return c.half ? 2 * tiles : tiles;
   return mode == kSwiglu ? tiles : (tiles + 1) / 2;
 }
