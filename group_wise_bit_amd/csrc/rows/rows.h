@@ -545,185 +545,215 @@ __global__ __launch_bounds__(WAVES * 64) void k_rows_gemv(const RowsArgs a) {
 __device__ __forceinline__ void here(f16x8& v) { asm volatile("" : "+v"(v)); }
 
 // -------------------------------------------------- many rows per expert --
-// Work-group: 32 RB rows of one expert x 128 columns (two 64-row weight tiles;
-// kSwiglu: tile t of gate and of up), 4 waves of 32 RB rows x 32 columns
-// (kSwiglu: 16 columns of gate in lanes c < 16, the same 16 of up in the
-// others).  A wave decodes its columns' block once, straight into MFMA B
-// registers -- integers q - z, exact, no scale rounded into them -- and
-// multiplies it by all RB blocks of X, read from LDS (16-byte chunks permuted
-// within their row by xswz, so that operand reads fall on distinct banks).  The four MFMAs of a block start from 0 and the group's scale takes
-// their sum to the fp32 accumulators, 16 fma per lane beside the next four
-// MFMAs.  Two X buffers: while block j is multiplied, block j + 1's rows are
-// on their way to registers and then to the other buffer; codes run two blocks
-// ahead.  One barrier per block.
-template <int BITS, int MODE, int RB, int D>
+// Work-group: 64 rows of one expert x 256 columns, 4 waves of 64 rows x 64
+// columns: tile 4x + w (kSwiglu: 32 columns of gate and the same 32 of up, half
+// w % 2 of tile 2x + w / 2).  A wave decodes its two 32-column blocks straight
+// into MFMA B registers -- integers q - z, exact, no scale rounded into them --
+// and multiplies them by both 32-row blocks of X, read from LDS once for the
+// two (16-byte chunks permuted within their row by xswz, so that the reads fall
+// on distinct banks).  The four MFMAs of 32 x 32 outputs and a K-block start
+// from 0, and the group's scale takes their sum to the fp32 accumulators: 16 fma
+// per lane, laid beside the next four MFMAs with a quarter of the next decode.
+// Three X buffers, so that the next block's first operands are read before the
+// barrier; rows two and codes one to two blocks ahead; one barrier per block.
+template <int BITS, int MODE>
 __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
   constexpr int WPB = 2 * BITS;
   constexpr int HW = BITS;
-  constexpr int BM = 32 * RB;
-  __shared__ f16x8 xs[2][BM * 8];
+  constexpr int BM = 64;
+  __shared__ f16x8 xs[3][BM * 8];
   const RowTile rt = row_tile<MODE>(a, BM);
   if (rt.rows <= 0) return;
   const int gx = rt.col;
   const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
   const int c = lane & 31, h = lane >> 5;
   const uint32_t magic = vreg_const(kMagic);
-  // the lane's weight row: row drow of tile dt of matrix di (a tile past the
-  // matrix re-reads its last one, never stored)
   const int tiles = (a.n + kTile - 1) / kTile;
-  const int tile = MODE == kSwiglu ? gx : 2 * gx + (wave >> 1);
-  const int drow = MODE == kSwiglu ? 16 * wave + (c & 15) : 32 * (wave & 1) + c;
-  const int di = MODE == kSwiglu ? c >> 4 : 0;
-  const int dt = min(tile, tiles - 1);
-  const uint32_t* wsrc = (di ? a.codes[1] : a.codes[0]) + rt.e * a.code_step +
-                         ((int64_t)dt * a.kb * kTile + drow) * WPB;
-  const int64_t mt = rt.e * a.meta_step + (int64_t)dt * a.G * kTile + drow;
-  const uint16_t* ssrc = (di ? a.scale[1] : a.scale[0]) + mt;
-  const uint8_t* zsrc = (di ? a.zero[1] : a.zero[0]) + mt;
+  const int tile = MODE == kSwiglu ? 2 * gx + (wave >> 1) : 4 * gx + wave;
+  const int dt = min(tile, tiles - 1);     // (a tile past the matrix: its last one, never stored)
+  // block f: rows 32 (wave % 2) of the tile of matrix f, or rows 32 f
+  const int half[2] = {MODE == kSwiglu ? wave & 1 : 0, MODE == kSwiglu ? wave & 1 : 1};
+  const int64_t woff = rt.e * a.code_step + (int64_t)dt * a.kb * kTile * WPB;
+  const int64_t moff = rt.e * a.meta_step + (int64_t)dt * a.G * kTile;
   const int t8 = tid >> 3, xk = tid & 7;
-  const uint16_t* xsrc[RB];
+  const uint16_t* xsrc[2];
 #pragma unroll
-  for (int i = 0; i < RB; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const int r = t8 + 32 * i;
     xsrc[i] = a.X + x_row<MODE>(a, rt.p0 + (r < rt.rows ? r : 0)) * a.ldx + 8 * xk;
   }
   const int xw = 8 * t8 + xswz(t8, xk);      // (rows 32 apart: the same place in their row)
 
-  uint32_t wl[D][HW];
-  uint16_t sr[D];
-  int zc[D];
-  f16x8 xg[D][RB];
+  uint32_t wl[2][2][HW];                     // [slot][block]
+  uint16_t sr[2][2];
+  int zc[2][2];
+  f16x8 xg[2][2];
   auto request_x = [&](auto S, int j) __attribute__((always_inline)) {
     constexpr int u = decltype(S)::value;
     const int jj = min(j, a.kb - 1);
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
+    for (int i = 0; i < 2; ++i)
       xg[u][i] = *reinterpret_cast<const f16x8*>(xsrc[i] + (int64_t)jj * kBlock);
   };
-  auto request_w = [&](auto S, int j) __attribute__((always_inline)) {
-    constexpr int u = decltype(S)::value;
+  auto request_w = [&](auto S, auto F, int j) __attribute__((always_inline)) {
+    constexpr int u = decltype(S)::value, f = decltype(F)::value;
+    constexpr int mi = MODE == kSwiglu ? f : 0;
     const int jj = min(j, a.kb - 1);
-    load_half<BITS>(wsrc + (int64_t)jj * kTile * WPB, h, wl[u]);
     const int64_t g = (a.G == 1) ? 0 : jj;
-    sr[u] = ssrc[g * kTile];
-    zc[u] = zsrc[g * kTile];
+    load_half<BITS>(lane_ptr(a.codes[mi], woff + ((int64_t)jj * kTile + 32 * half[f]) * WPB, c * WPB), h,
+                    wl[u][f]);
+    sr[u][f] = *lane_ptr(a.scale[mi], moff + g * kTile + 32 * half[f], c);
+    zc[u][f] = *lane_ptr(a.zero[mi], moff + g * kTile + 32 * half[f], c);
   };
   auto store_x = [&](auto S, int b) __attribute__((always_inline)) {
     constexpr int u = decltype(S)::value;
 #pragma unroll
-    for (int i = 0; i < RB; ++i) xs[b][xw + 256 * i] = xg[u][i];
+    for (int i = 0; i < 2; ++i) xs[b][xw + 256 * i] = xg[u][i];
   };
-  f32x16 acc[RB];
+  f32x16 acc[2][2], blk[2];                  // [row block][column block]; sums not yet scaled
+  f16x8 av[2][4], bv[2][4];
+  float scl[2], old = 0.f;                   // scales of the blocks in bv; of the pending sums
+  auto read_a = [&](auto R, int b) __attribute__((always_inline)) {
+    constexpr int rb = decltype(R)::value;
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb)
+    for (int q = 0; q < 4; ++q) av[rb][q] = xs[b][8 * (32 * rb + c) + xswz(c, 4 * h + q)];
+  };
+  const std::integral_constant<int, 0> I0;
+  const std::integral_constant<int, 1> I1;
+  request_w(I0, I0, 0);
+  request_w(I0, I1, 0);
+  request_x(I0, 0);
+  request_x(I1, 1);
+  request_w(I1, I0, 1);
+  request_w(I1, I1, 1);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[rb][r] = 0.f;
-  f16x8 bv[2][4];
-  float scl[2];
-  f32x16 blk[2];               // sums of one block and 32 rows, not yet scaled
+  for (int f = 0; f < 2; ++f) {
 #pragma unroll
-  for (int r = 0; r < 16; ++r) blk[0][r] = blk[1][r] = 0.f;
-  scl[1] = 0.f;
-  static_for<0, D>([&](auto S) __attribute__((always_inline)) {
-    request_w(S, decltype(S)::value);
-    request_x(S, decltype(S)::value);
-  });
-  const std::integral_constant<int, 0> S0;
-  {
-    const DeqT<BITS> d = make_deq_b<BITS>(1.f, zc[0]);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) bv[0][q] = int_half<BITS>(wl[0], q, d, magic);
-    scl[0] = h2f(sr[0]);
-    store_x(S0, 0);
-    request_w(S0, D);
+    for (int r = 0; r < 16; ++r) acc[0][f][r] = acc[1][f][r] = blk[f][r] = 0.f;
   }
-  lds_barrier();
-  // block j (slot U of D): from X buffer and operand registers j % 2; block
-  // j + 1's codes and rows wait in slot U + 1, slot U's rows are free
-  auto step = [&](auto U, int j) __attribute__((always_inline)) {
-    constexpr int u = decltype(U)::value, b = u & 1;
-    const std::integral_constant<int, (u + 1) % D> N;
-    constexpr int n = (u + 1) % D;
-    f16x8 av[2][4];
-    auto read_a = [&](int rb) __attribute__((always_inline)) {
+  // block f of the operand from slot u: a quarter of it, and its scale
+  auto decode = [&](auto S, auto F, int q0, int q1) __attribute__((always_inline)) {
+    constexpr int u = decltype(S)::value, f = decltype(F)::value;
+    const DeqT<BITS> d = make_deq_b<BITS>(1.f, zc[u][f]);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        av[rb & 1][q] = xs[b][8 * (32 * rb + c) + xswz(c, 4 * h + q)];
-    };
-    auto scale_block = [&](int rb, float s) __attribute__((always_inline)) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[rb][r] = __builtin_fmaf(s, blk[rb & 1][r], acc[rb][r]);
-    };
-    read_a(0);
-    request_x(U, j + D);
-    const DeqT<BITS> d = make_deq_b<BITS>(1.f, zc[n]);
-    // the previous block's last rows, while this block's first operands arrive
-    scale_block(RB - 1, scl[1 - b]);
-    scl[1 - b] = h2f(sr[n]);
-    asm volatile("" : "+v"(scl[1 - b]));
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      if (rb + 1 < RB) read_a(rb + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      const f32x16 none = {};
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        blk[rb & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-            av[rb & 1][q], bv[b][q], q == 0 ? none : blk[rb & 1], 0, 0, 0);
-#pragma unroll
-      for (int q = rb * 4 / RB; q < (rb + 1) * 4 / RB; ++q) {
-        bv[1 - b][q] = int_half<BITS>(wl[n], q, d, magic);
-        here(bv[1 - b][q]);
-      }
-      if (rb > 0) scale_block(rb - 1, scl[b]);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int q = 0; q < 4; ++q) {
+      if (q < q0 || q >= q1) continue;
+      bv[f][q] = int_half<BITS>(wl[u][f], q, d, magic);
+      here(bv[f][q]);
     }
-    store_x(N, 1 - b);
-    request_w(N, j + 1 + D);
+  };
+  auto scale_of = [&](auto S, auto F) __attribute__((always_inline)) {
+    constexpr int u = decltype(S)::value, f = decltype(F)::value;
+    float s = h2f(sr[u][f]);
+    asm volatile("" : "+v"(s));
+    return s;
+  };
+  decode(I0, I0, 0, 4);
+  scl[0] = scale_of(I0, I0);
+  store_x(I0, 0);
+  store_x(I1, 1);
+  request_x(I0, 2);
+  request_x(I1, 3);
+  lds_barrier();
+  read_a(I0, 0);
+  int b0 = 0, b1 = 1, b2 = 2;                // X buffers of blocks j, j + 1, j + 2
+  // four MFMAs of row block R and column block F into blk[P], beside the scaling
+  // of the sums in blk[1 - P] (row block PR, column block PF)
+  auto product = [&](auto R, auto F, auto P) __attribute__((always_inline)) {
+    constexpr int rb = decltype(R)::value, f = decltype(F)::value, pp = decltype(P)::value;
+    const f32x16 none = {};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      blk[pp] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av[rb][q], bv[f][q], q == 0 ? none : blk[pp],
+                                                       0, 0, 0);
+  };
+  auto scaled = [&](auto R, auto F, auto P, float s) __attribute__((always_inline)) {
+    constexpr int rb = decltype(R)::value, f = decltype(F)::value, pp = decltype(P)::value;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[rb][f][r] = __builtin_fmaf(s, blk[pp][r], acc[rb][f][r]);
+  };
+  // block j, its codes in slot U; block j + 1's in slot 1 - U; rows of block
+  // j + 2 in slot U
+  auto step = [&](auto U, int j) __attribute__((always_inline)) {
+    constexpr int u = decltype(U)::value;
+    const std::integral_constant<int, 1 - u> N;
+    read_a(I1, b0);
+    __builtin_amdgcn_sched_barrier(0);
+    product(I0, I0, I0);
+    decode(U, I1, 0, 2);
+    scaled(I1, I1, I1, old);                 // of block j - 1
+    __builtin_amdgcn_sched_barrier(0);
+    product(I1, I0, I1);
+    decode(U, I1, 2, 4);
+    scl[1] = scale_of(U, I1);
+    scaled(I0, I0, I0, scl[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    request_w(U, I0, j + 2);
+    request_w(U, I1, j + 2);
+    product(I0, I1, I0);
+    decode(N, I0, 0, 2);
+    scaled(I1, I0, I1, scl[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    read_a(I0, b1);                          // (of block j + 1)
+    product(I1, I1, I1);
+    decode(N, I0, 2, 4);
+    scl[0] = scale_of(N, I0);
+    scaled(I0, I1, I0, scl[1]);
+    old = scl[1];
+    __builtin_amdgcn_sched_barrier(0);
+    store_x(U, b2);
+    request_x(U, j + 4);
     lds_barrier();
+    const int b3 = b0;
+    b0 = b1;
+    b1 = b2;
+    b2 = b3;
   };
   int j0 = 0;
-  for (; j0 + D <= a.kb; j0 += D)
-    static_for<0, D>([&](auto U) __attribute__((always_inline)) {
-      step(U, j0 + decltype(U)::value);
-    });
-  static_for<0, D - 1>([&](auto U) __attribute__((always_inline)) {
-    if (j0 + decltype(U)::value < a.kb) step(U, j0 + decltype(U)::value);
-  });
-  {
-    const float s = a.kb & 1 ? scl[0] : scl[1];
-#pragma unroll
-    for (int r = 0; r < 16; ++r)
-      acc[RB - 1][r] = __builtin_fmaf(s, blk[(RB - 1) & 1][r], acc[RB - 1][r]);
+  for (; j0 + 2 <= a.kb; j0 += 2) {
+    step(I0, j0);
+    step(I1, j0 + 1);
   }
+  if (j0 < a.kb) step(I0, j0);
+  scaled(I1, I1, I1, old);
 
-  const int col = tile * kTile + drow;
-  if constexpr (MODE == kLora) {
-    const int cols[1] = {col};
+  int col[2];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      RowAdapters<1> adapters;
-      adapters.begin(a, 32 * rb + c < rt.rows ? x_row<MODE>(a, rt.p0 + 32 * rb + c) : -1, cols, 0, 1);
-      adapters.add(a, reinterpret_cast<f32x16(&)[1]>(acc[rb]));
+  for (int f = 0; f < 2; ++f) col[f] = tile * kTile + 32 * half[f] + c;
+  if constexpr (MODE == kLora) {
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) {
+      const int64_t row = 32 * rb + c < rt.rows ? x_row<MODE>(a, rt.p0 + 32 * rb + c) : -1;
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int cols[1] = {col[f]};
+        RowAdapters<1> adapters;
+        adapters.begin(a, row, cols, 0, 1);
+        adapters.add(a, reinterpret_cast<f32x16(&)[1]>(acc[rb][f]));
+      }
     }
   }
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb)
+  for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int row = 32 * rb + 8 * (r >> 2) + 4 * h + (r & 3);
+      if (row >= rt.rows) continue;
       if constexpr (MODE == kSwiglu) {
-        const float u = __shfl_xor(acc[rb][r], 16);
-        if (row >= rt.rows || c >= 16) continue;
-        const float hv = silu(acc[rb][r]) * u;
-        a.y16[(int64_t)(rt.p0 + row) * a.ldy + col] = __builtin_bit_cast(uint16_t, (f16)hv);
+        if (tile >= tiles) continue;
+        const float hv = silu(acc[rb][0][r]) * acc[rb][1][r];
+        a.y16[(int64_t)(rt.p0 + row) * a.ldy + col[0]] = __builtin_bit_cast(uint16_t, (f16)hv);
       } else {
-        if (row >= rt.rows || col >= a.n) continue;
         const int64_t out = MODE == kDown ? a.plan.order[rt.p0 + row] : x_row<MODE>(a, rt.p0 + row);
-        const float v = MODE == kDown ? a.weights[out] * acc[rb][r] : acc[rb][r];
-        if (MODE == kDown || a.y != nullptr) a.y[out * a.ldy + col] = v;
-        if (MODE == kLora && a.y16 != nullptr)
-          a.y16[out * a.ldy + col] = __builtin_bit_cast(uint16_t, (f16)v);
+        const float w = MODE == kDown ? a.weights[out] : 1.f;
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          if (col[f] >= a.n) continue;
+          const float v = MODE == kDown ? w * acc[rb][f][r] : acc[rb][f][r];
+          if (MODE == kDown || a.y != nullptr) a.y[out * a.ldy + col[f]] = v;
+          if (MODE == kLora && a.y16 != nullptr)
+            a.y16[out * a.ldy + col[f]] = __builtin_bit_cast(uint16_t, (f16)v);
+        }
       }
     }
 }

@@ -24,7 +24,7 @@ void launch_mode(const RowsArgs& a, RowsCfg c, hipStream_t st) {
   }
   if constexpr (MODE != kToken) {
     constexpr int U = MODE == kSwiglu && B > 4 ? 1 : 2;   // by the registers of a block
-    if (c.height == 64) hipLaunchKernelGGL((k_rows_tiled<B, MODE, 2, 4>), grid, block, 0, st, a);
+    if (c.height == 64) hipLaunchKernelGGL((k_rows_tiled<B, MODE>), grid, block, 0, st, a);
     else if (c.half) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 8, 1, 2>), grid, block, 0, st, a);
     else if (c.waves == 8) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 8, 2, U>), grid, block, 0, st, a);
     else if (c.waves == 4) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 4, 2, U>), grid, block, 0, st, a);

@@ -37,7 +37,7 @@ inline int rows_cols(int n, int mode, RowsCfg c) {
   const int tiles = (n + kTile - 1) / kTile;
   if (c.height == 1) return (c.half ? 8 : 4) * tiles;
   if (c.height == 32) return c.half ? 2 * tiles : tiles;
-  return mode == kSwiglu ? tiles : (tiles + 1) / 2;
+  return mode == kSwiglu ? (tiles + 1) / 2 : (tiles + 3) / 4;
 }
 
 // Whether the grid of such a product can be launched (HIP counts threads in
