@@ -114,8 +114,9 @@ __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
     const int p0 = first[lo].y + (i - first[lo].x) * rows;
     plan.tiles[i] = make_int4(lo, p0, min(rows, first[lo + 1].y - p0), 0);
   }
+  const bool kept = i1 - i0 <= 64 * U;       // the first pass's ids are all of the wave's
   for (int b0 = i0; b0 < i1; b0 += 64 * U) {
-    load_ids(b0);
+    if (!kept) load_ids(b0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int b = b0 + 64 * u, id = id8[u];
@@ -142,7 +143,8 @@ __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
 
 // ------------------------------------------------- sum over a token's experts --
 // Y[i, :] = the rows of its valid (token, slot) pairs, added in slot order.
-// One thread: 4 columns of one token (n is a multiple of 64).
+// One thread: 4 columns of one token (n is a multiple of 64), the rows of 8
+// slots requested together.
 __global__ __launch_bounds__(256) void k_rows_combine(
     const float* __restrict__ d, const int32_t* __restrict__ ids, int m, int top_k, int experts,
     int n, float* __restrict__ y, uint16_t* __restrict__ y16, int64_t ldy) {
@@ -152,9 +154,20 @@ __global__ __launch_bounds__(256) void k_rows_combine(
     const int64_t i = q / n4;
     const int c = (int)(q % n4) * 4;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < top_k; ++j)
-      if ((uint32_t)ids[i * top_k + j] < (uint32_t)experts)
-        s += *reinterpret_cast<const f32x4*>(d + (i * top_k + j) * n + c);
+    constexpr int U = 8;
+    for (int j0 = 0; j0 < top_k; j0 += U) {
+      f32x4 v[U];
+      int id[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t p = i * top_k + min(j0 + u, top_k - 1);
+        id[u] = ids[p];
+        v[u] = *reinterpret_cast<const f32x4*>(d + p * n + c);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)     // (rows of pairs without an expert are not written: any bits)
+        if (j0 + u < top_k && (uint32_t)id[u] < (uint32_t)experts) s += v[u];
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (y != nullptr) y[i * ldy + c + e] = s[e];
