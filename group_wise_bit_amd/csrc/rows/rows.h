@@ -556,6 +556,42 @@ __device__ __forceinline__ void here(f16x8& v) { asm volatile("" : "+v"(v)); }
 // per lane, laid beside the next four MFMAs with a quarter of the next decode.
 // Three X buffers, so that the next block's first operands are read before the
 // barrier; rows two and codes one to two blocks ahead; one barrier per block.
+// Codes, scales and zeros come through buffer descriptors: the base and the
+// block's offset are scalars, so a load costs no vector address, neither the
+// instructions that form one nor the registers that a loop keeps one in (48
+// bytes per lane for the six pointers of two matrices).
+using Buffer = __amdgpu_buffer_rsrc_t;
+__device__ __forceinline__ Buffer buffer_of(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+// load_half through a descriptor: the words of half h of a row of 64 codes.
+// lane = half_offsets(): where its first (BITS < 5: all) and its high plane's lie.
+template <int BITS>
+__device__ __forceinline__ int2 half_offsets(int c, int h) {
+  constexpr int high = BITS == 5 ? 4 : BITS == 6 ? 8 : 12;
+  const int row = 8 * BITS * c;
+  if constexpr (BITS >= 5 && BITS <= 7) return make_int2(row + 16 * h, row + 32 + high * h);
+  else return make_int2(row + 4 * BITS * h, 0);
+}
+template <int BITS>
+__device__ __forceinline__ void load_half(Buffer b, int2 lane, int at, uint32_t* wl) {
+  auto put = [&](auto v, int n, uint32_t* w) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) w[i] = v[i];
+  };
+  if constexpr (BITS == 2) {
+    put(__builtin_amdgcn_raw_buffer_load_b64(b, lane.x, at, 0), 2, wl);
+  } else if constexpr (BITS == 3) {
+    put(__builtin_amdgcn_raw_buffer_load_b96(b, lane.x, at, 0), 3, wl);
+  } else {
+    put(__builtin_amdgcn_raw_buffer_load_b128(b, lane.x, at, 0), 4, wl);
+    if constexpr (BITS == 5) wl[4] = __builtin_amdgcn_raw_buffer_load_b32(b, lane.y, at, 0);
+    if constexpr (BITS == 6) put(__builtin_amdgcn_raw_buffer_load_b64(b, lane.y, at, 0), 2, wl + 4);
+    if constexpr (BITS == 7) put(__builtin_amdgcn_raw_buffer_load_b96(b, lane.y, at, 0), 3, wl + 4);
+    if constexpr (BITS == 8) put(__builtin_amdgcn_raw_buffer_load_b128(b, lane.x + 16, at, 0), 4, wl + 4);
+  }
+}
+
 template <int BITS, int MODE>
 __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
   constexpr int WPB = 2 * BITS;
@@ -575,6 +611,15 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
   const int half[2] = {MODE == kSwiglu ? wave & 1 : 0, MODE == kSwiglu ? wave & 1 : 1};
   const int64_t woff = rt.e * a.code_step + (int64_t)dt * a.kb * kTile * WPB;
   const int64_t moff = rt.e * a.meta_step + (int64_t)dt * a.G * kTile;
+  constexpr int NM = MODE == kSwiglu ? 2 : 1;
+  Buffer codes[NM], scale[NM], zero[NM];
+#pragma unroll
+  for (int i = 0; i < NM; ++i) {
+    codes[i] = buffer_of(a.codes[i] + woff, (int64_t)a.kb * kTile * WPB * 4);
+    scale[i] = buffer_of(a.scale[i] + moff, (int64_t)a.G * kTile * 2);
+    zero[i] = buffer_of(a.zero[i] + moff, (int64_t)a.G * kTile);
+  }
+  const int2 wlane = half_offsets<BITS>(c, h);
   const int t8 = tid >> 3, xk = tid & 7;
   const uint16_t* xsrc[2];
 #pragma unroll
@@ -599,11 +644,10 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
     constexpr int u = decltype(S)::value, f = decltype(F)::value;
     constexpr int mi = MODE == kSwiglu ? f : 0;
     const int jj = min(j, a.kb - 1);
-    const int64_t g = (a.G == 1) ? 0 : jj;
-    load_half<BITS>(lane_ptr(a.codes[mi], woff + ((int64_t)jj * kTile + 32 * half[f]) * WPB, c * WPB), h,
-                    wl[u][f]);
-    sr[u][f] = *lane_ptr(a.scale[mi], moff + g * kTile + 32 * half[f], c);
-    zc[u][f] = *lane_ptr(a.zero[mi], moff + g * kTile + 32 * half[f], c);
+    const int g = (a.G == 1) ? 0 : jj;
+    load_half<BITS>(codes[mi], wlane, (jj * kTile + 32 * half[f]) * WPB * 4, wl[u][f]);
+    sr[u][f] = __builtin_amdgcn_raw_buffer_load_b16(scale[mi], 2 * c, 2 * (g * kTile + 32 * half[f]), 0);
+    zc[u][f] = __builtin_amdgcn_raw_buffer_load_b8(zero[mi], c, g * kTile + 32 * half[f], 0);
   };
   auto store_x = [&](auto S, int b) __attribute__((always_inline)) {
     constexpr int u = decltype(S)::value;
@@ -672,11 +716,9 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[rb][f][r] = __builtin_fmaf(s, blk[pp][r], acc[rb][f][r]);
   };
-  // block j, its codes in slot U; block j + 1's in slot 1 - U; rows of block
-  // j + 2 in slot U
+  // block j, its codes in slot U, as the rows of block j + 2
   auto step = [&](auto U, int j) __attribute__((always_inline)) {
-    constexpr int u = decltype(U)::value;
-    const std::integral_constant<int, 1 - u> N;
+    const std::integral_constant<int, 1 - decltype(U)::value> N;
     read_a(I1, b0);
     __builtin_amdgcn_sched_barrier(0);
     product(I0, I0, I0);
