@@ -217,10 +217,10 @@ struct RowAdapters {
       }
     }
   }
-  // xrow: the lane's row c of X, or -1; col[cb]: its column of block cb
-  __device__ __forceinline__ void begin(const RowsArgs& a, int64_t xrow, const int (&col)[CB],
+  // xrow: the lane's row c of X, or -1, its id; col[cb]: its column of block cb
+  __device__ __forceinline__ void begin(const RowsArgs& a, int64_t xrow, int xid, const int (&col)[CB],
                                         int part, int of) {
-    id = xrow >= 0 ? a.ids[xrow] : -1;
+    id = xid;
     const bool has = (uint32_t)id < (uint32_t)a.slots;
     row = has ? xrow : -1;
     parts = of;
@@ -349,7 +349,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
   int col[CB];
 #pragma unroll
   for (int cb = 0; cb < CB; ++cb) col[cb] = t * kTile + 32 * (cb0 + cb) + c;
-  if constexpr (MODE == kLora) adapters.begin(a, c < rows ? xr : -1, col, wave, WAVES);
+  if constexpr (MODE == kLora)
+    adapters.begin(a, c < rows ? xr : -1, c < rows ? a.ids[xr] : -1, col, wave, WAVES);
   for (int jb = wave; jb < a.kb; jb += WAVES * U) {
     f16x8 xa[U][4];
     uint32_t wl[U][NM][CB][HW];
@@ -554,8 +555,9 @@ __device__ __forceinline__ void here(f16x8& v) { asm volatile("" : "+v"(v)); }
 // on distinct banks).  The four MFMAs of 32 x 32 outputs and a K-block start
 // from 0, and the group's scale takes their sum to the fp32 accumulators: 16 fma
 // per lane, laid beside the next four MFMAs with a quarter of the next decode.
-// Three X buffers, so that the next block's first operands are read before the
-// barrier; rows two and codes one to two blocks ahead; one barrier per block.
+// X by direct-to-LDS loads into four stages, three blocks ahead (and the next
+// block's first operands are read before the barrier), codes two blocks ahead in
+// registers; one barrier per block.
 // Codes, scales and zeros come through buffer descriptors: the base and the
 // block's offset are scalars, so a load costs no vector address, neither the
 // instructions that form one nor the registers that a loop keeps one in (48
@@ -563,6 +565,11 @@ __device__ __forceinline__ void here(f16x8& v) { asm volatile("" : "+v"(v)); }
 using Buffer = __amdgpu_buffer_rsrc_t;
 __device__ __forceinline__ Buffer buffer_of(const void* p, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+// 16 bytes per lane to LDS, lane l's to lds + 16 l.
+__device__ __forceinline__ void buffer_to_lds(Buffer b, void* lds, uint32_t lane, int at) {
+  typedef __attribute__((address_space(3))) void lds_void;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)lds, 16, lane, at, 0, 0);
 }
 // load_half through a descriptor: the words of half h of a row of 64 codes.
 // lane = half_offsets(): where its first (BITS < 5: all) and its high plane's lie.
@@ -592,13 +599,28 @@ __device__ __forceinline__ void load_half(Buffer b, int2 lane, int at, uint32_t*
   }
 }
 
+// X stages: LDS objects of their own, so that the compiler can tell which
+// direct-to-LDS loads a read depends on.
+constexpr int kXStages = 4;
+template <int I>
+__device__ __forceinline__ f16x8* x_stage() {
+  __shared__ f16x8 xs[64 * 8];
+  return xs;
+}
+
+// Waits for the wave's LDS accesses and for all but its N newest loads, then a
+// work-group barrier.  (One asm block: a fence, as in lds_barrier(), would wait
+// for every direct-to-LDS load in flight.)
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 template <int BITS, int MODE>
 __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
   constexpr int WPB = 2 * BITS;
   constexpr int HW = BITS;
-  constexpr int BM = 64;
-  __shared__ f16x8 xs[3][BM * 8];
-  const RowTile rt = row_tile<MODE>(a, BM);
+  const RowTile rt = row_tile<MODE>(a, 64);
   if (rt.rows <= 0) return;
   const int gx = rt.col;
   const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
@@ -606,9 +628,9 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
   const uint32_t magic = vreg_const(kMagic);
   const int tiles = (a.n + kTile - 1) / kTile;
   const int tile = MODE == kSwiglu ? 2 * gx + (wave >> 1) : 4 * gx + wave;
-  const int dt = min(tile, tiles - 1);     // (a tile past the matrix: its last one, never stored)
-  // block f: rows 32 (wave % 2) of the tile of matrix f, or rows 32 f
+  // column block f: rows 32 half[f] of the tile (kSwiglu: of matrix f)
   const int half[2] = {MODE == kSwiglu ? wave & 1 : 0, MODE == kSwiglu ? wave & 1 : 1};
+  const int dt = min(tile, tiles - 1);       // (a tile past the matrix: its last one, never stored)
   const int64_t woff = rt.e * a.code_step + (int64_t)dt * a.kb * kTile * WPB;
   const int64_t moff = rt.e * a.meta_step + (int64_t)dt * a.G * kTile;
   constexpr int NM = MODE == kSwiglu ? 2 : 1;
@@ -620,62 +642,56 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
     zero[i] = buffer_of(a.zero[i] + moff, (int64_t)a.G * kTile);
   }
   const int2 wlane = half_offsets<BITS>(c, h);
-  const int t8 = tid >> 3, xk = tid & 7;
-  const uint16_t* xsrc[2];
+  // Direct-to-LDS loads of X: instruction i of a wave brings 8 rows from row
+  // 32 i + 8 wave on, lane l to chunk l of the 64: row l / 8, slot l % 8.  32-bit
+  // offsets: from the first row of kDown's consecutive ones, else from X, whose
+  // span the host has checked (rows_span_ok).
+  const Buffer xbuf = buffer_of(a.X + (MODE == kDown ? rt.p0 * a.ldx : 0), 0xffffffff);
+  uint32_t xoff[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int r = t8 + 32 * i;
-    xsrc[i] = a.X + x_row<MODE>(a, rt.p0 + (r < rt.rows ? r : 0)) * a.ldx + 8 * xk;
+    const int r = 32 * i + (tid >> 3), p = r < rt.rows ? r : 0;
+    const int64_t row = MODE == kDown ? p : x_row<MODE>(a, rt.p0 + p);
+    xoff[i] = (uint32_t)(row * a.ldx + 8 * xswz(r, tid & 7)) * 2;
   }
-  const int xw = 8 * t8 + xswz(t8, xk);      // (rows 32 apart: the same place in their row)
 
-  uint32_t wl[2][2][HW];                     // [slot][block]
+  uint32_t wl[2][2][HW];                    // [slot][block]
   uint16_t sr[2][2];
   int zc[2][2];
-  f16x8 xg[2][2];
-  auto request_x = [&](auto S, int j) __attribute__((always_inline)) {
-    constexpr int u = decltype(S)::value;
+  auto request_x = [&](auto T, int j) __attribute__((always_inline)) {
+    f16x8* xs = x_stage<decltype(T)::value>();
     const int jj = min(j, a.kb - 1);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      xg[u][i] = *reinterpret_cast<const f16x8*>(xsrc[i] + (int64_t)jj * kBlock);
+      buffer_to_lds(xbuf, xs + 256 * i + 64 * wave, xoff[i], jj * kBlock * 2);
+    __builtin_amdgcn_sched_barrier(0);
   };
-  auto request_w = [&](auto S, auto F, int j) __attribute__((always_inline)) {
-    constexpr int u = decltype(S)::value, f = decltype(F)::value;
-    constexpr int mi = MODE == kSwiglu ? f : 0;
+  auto request_w = [&](auto S, int j) __attribute__((always_inline)) {
+    constexpr int u = decltype(S)::value;
     const int jj = min(j, a.kb - 1);
     const int g = (a.G == 1) ? 0 : jj;
-    load_half<BITS>(codes[mi], wlane, (jj * kTile + 32 * half[f]) * WPB * 4, wl[u][f]);
-    sr[u][f] = __builtin_amdgcn_raw_buffer_load_b16(scale[mi], 2 * c, 2 * (g * kTile + 32 * half[f]), 0);
-    zc[u][f] = __builtin_amdgcn_raw_buffer_load_b8(zero[mi], c, g * kTile + 32 * half[f], 0);
-  };
-  auto store_x = [&](auto S, int b) __attribute__((always_inline)) {
-    constexpr int u = decltype(S)::value;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) xs[b][xw + 256 * i] = xg[u][i];
+    for (int f = 0; f < 2; ++f) {
+      const int i = min(f, NM - 1);
+      load_half<BITS>(codes[i], wlane, (jj * kTile + 32 * half[f]) * WPB * 4, wl[u][f]);
+      sr[u][f] = __builtin_amdgcn_raw_buffer_load_b16(scale[i], 2 * c, 2 * (g * kTile + 32 * half[f]), 0);
+      zc[u][f] = __builtin_amdgcn_raw_buffer_load_b8(zero[i], c, g * kTile + 32 * half[f], 0);
+    }
   };
-  f32x16 acc[2][2], blk[2];                  // [row block][column block]; sums not yet scaled
-  f16x8 av[2][4], bv[2][4];
-  float scl[2], old = 0.f;                   // scales of the blocks in bv; of the pending sums
-  auto read_a = [&](auto R, int b) __attribute__((always_inline)) {
+  f32x16 acc[2][2], blk[2];                // [row block][column block]; sums not yet scaled
+  f16x8 av[2][4], bv[2][4];                  // [row / column block][K quarter]
+  float scl[2];                              // the scales of bv's operands
+  auto read_a = [&](auto R, auto T) __attribute__((always_inline)) {
     constexpr int rb = decltype(R)::value;
+    const f16x8* xs = x_stage<decltype(T)::value>();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) av[rb][q] = xs[b][8 * (32 * rb + c) + xswz(c, 4 * h + q)];
+    for (int q = 0; q < 4; ++q) av[rb][q] = xs[8 * (32 * rb + c) + xswz(c, 4 * h + q)];
   };
   const std::integral_constant<int, 0> I0;
   const std::integral_constant<int, 1> I1;
-  request_w(I0, I0, 0);
-  request_w(I0, I1, 0);
-  request_x(I0, 0);
-  request_x(I1, 1);
-  request_w(I1, I0, 1);
-  request_w(I1, I1, 1);
-#pragma unroll
-  for (int f = 0; f < 2; ++f) {
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[0][f][r] = acc[1][f][r] = blk[f][r] = 0.f;
-  }
-  // block f of the operand from slot u: a quarter of it, and its scale
+  const std::integral_constant<int, 2> I2;
+  const std::integral_constant<int, 3> I3;
+  // quarters q0 .. q1 - 1 of column block F from slot S
   auto decode = [&](auto S, auto F, int q0, int q1) __attribute__((always_inline)) {
     constexpr int u = decltype(S)::value, f = decltype(F)::value;
     const DeqT<BITS> d = make_deq_b<BITS>(1.f, zc[u][f]);
@@ -692,72 +708,84 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
     asm volatile("" : "+v"(s));
     return s;
   };
-  decode(I0, I0, 0, 4);
-  scl[0] = scale_of(I0, I0);
-  store_x(I0, 0);
-  store_x(I1, 1);
-  request_x(I0, 2);
-  request_x(I1, 3);
-  lds_barrier();
-  read_a(I0, 0);
-  int b0 = 0, b1 = 1, b2 = 2;                // X buffers of blocks j, j + 1, j + 2
-  // four MFMAs of row block R and column block F into blk[P], beside the scaling
-  // of the sums in blk[1 - P] (row block PR, column block PF)
-  auto product = [&](auto R, auto F, auto P) __attribute__((always_inline)) {
-    constexpr int rb = decltype(R)::value, f = decltype(F)::value, pp = decltype(P)::value;
+  // four MFMAs of row block R and column block F into blk[R]
+  auto product = [&](auto R, auto F) __attribute__((always_inline)) {
+    constexpr int rb = decltype(R)::value, f = decltype(F)::value;
     const f32x16 none = {};
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      blk[pp] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av[rb][q], bv[f][q], q == 0 ? none : blk[pp],
+      blk[rb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av[rb][q], bv[f][q], q == 0 ? none : blk[rb],
                                                        0, 0, 0);
   };
-  auto scaled = [&](auto R, auto F, auto P, float s) __attribute__((always_inline)) {
-    constexpr int rb = decltype(R)::value, f = decltype(F)::value, pp = decltype(P)::value;
+  // those sums, times s, to the accumulators
+  auto scaled = [&](auto R, auto F, float s) __attribute__((always_inline)) {
+    constexpr int rb = decltype(R)::value, f = decltype(F)::value;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[rb][f][r] = __builtin_fmaf(s, blk[pp][r], acc[rb][f][r]);
+    for (int r = 0; r < 16; ++r) acc[rb][f][r] = __builtin_fmaf(s, blk[rb][r], acc[rb][f][r]);
   };
-  // block j, its codes in slot U, as the rows of block j + 2
-  auto step = [&](auto U, int j) __attribute__((always_inline)) {
-    const std::integral_constant<int, 1 - decltype(U)::value> N;
-    read_a(I1, b0);
+  request_x(I0, 0);
+  request_w(I0, 0);
+  request_x(I1, 1);
+  request_w(I1, 1);
+  request_x(I2, 2);
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    acc[0][0][r] = acc[0][1][r] = acc[1][0][r] = acc[1][1][r] = 0.f;
+    blk[1][r] = 0.f;
+  }
+  scl[1] = 0.f;
+  decode(I0, I0, 0, 4);
+  scl[0] = scale_of(I0, I0);
+  stage_barrier<0>();
+  read_a(I0, I0);
+  // loads of a wave and a block behind the one that must be there: X's of the
+  // next block and the codes', scales' and zeros' issued after it
+  constexpr int kNewer = 2 + 2 * ((BITS >= 5 ? 2 : 1) + 2);
+  // Block j, its codes in slot j % 2, its rows in stage j % 4 = T; block j + 3's
+  // rows go where block j - 1's were.
+  auto step = [&](auto T, int j) __attribute__((always_inline)) {
+    constexpr int kT = decltype(T)::value;
+    const std::integral_constant<int, kT % 2> U;
+    const std::integral_constant<int, (kT + 1) % 2> N;
+    const std::integral_constant<int, (kT + 1) % kXStages> T1;
+    const std::integral_constant<int, (kT + 3) % kXStages> T3;
+    request_x(T3, j + 3);
+    read_a(I1, T);
     __builtin_amdgcn_sched_barrier(0);
-    product(I0, I0, I0);
+    product(I0, I0);
+    scaled(I1, I1, scl[1]);                  // of block j - 1
     decode(U, I1, 0, 2);
-    scaled(I1, I1, I1, old);                 // of block j - 1
     __builtin_amdgcn_sched_barrier(0);
-    product(I1, I0, I1);
+    product(I1, I0);
     decode(U, I1, 2, 4);
     scl[1] = scale_of(U, I1);
-    scaled(I0, I0, I0, scl[0]);
+    scaled(I0, I0, scl[0]);
     __builtin_amdgcn_sched_barrier(0);
-    request_w(U, I0, j + 2);
-    request_w(U, I1, j + 2);
-    product(I0, I1, I0);
+    request_w(U, j + 2);
+    product(I0, I1);
     decode(N, I0, 0, 2);
-    scaled(I1, I0, I1, scl[0]);
+    scaled(I1, I0, scl[0]);
     __builtin_amdgcn_sched_barrier(0);
-    read_a(I0, b1);                          // (of block j + 1)
-    product(I1, I1, I1);
+    read_a(I0, T1);                          // (of block j + 1)
+    product(I1, I1);
     decode(N, I0, 2, 4);
     scl[0] = scale_of(N, I0);
-    scaled(I0, I1, I0, scl[1]);
-    old = scl[1];
+    scaled(I0, I1, scl[1]);
     __builtin_amdgcn_sched_barrier(0);
-    store_x(U, b2);
-    request_x(U, j + 4);
-    lds_barrier();
-    const int b3 = b0;
-    b0 = b1;
-    b1 = b2;
-    b2 = b3;
+    stage_barrier<kNewer>();                 // block j + 2's rows are there
   };
   int j0 = 0;
-  for (; j0 + 2 <= a.kb; j0 += 2) {
+  for (; j0 + 4 <= a.kb; j0 += 4) {
     step(I0, j0);
     step(I1, j0 + 1);
+    step(I2, j0 + 2);
+    step(I3, j0 + 3);
   }
   if (j0 < a.kb) step(I0, j0);
-  scaled(I1, I1, I1, old);
+  if (j0 + 1 < a.kb) step(I1, j0 + 1);
+  if (j0 + 2 < a.kb) step(I2, j0 + 2);
+  stage_barrier<0>();                        // (rows requested past the end)
+  scaled(I1, I1, scl[1]);
 
   int col[2];
 #pragma unroll
@@ -766,35 +794,46 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
 #pragma unroll
     for (int rb = 0; rb < 2; ++rb) {
       const int64_t row = 32 * rb + c < rt.rows ? x_row<MODE>(a, rt.p0 + 32 * rb + c) : -1;
+      RowAdapters<2> adapters;
+      adapters.begin(a, row, row >= 0 ? a.ids[row] : -1, col, 0, 1);
+      adapters.add(a, acc[rb]);
+    }
+  }
+  // (kDown, kLora) lane c's row c of each row block: its output row and weight,
+  // read together and handed to the lanes that store it
+  int out[2];
+  float w[2];
+  if constexpr (MODE != kSwiglu) {
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int cols[1] = {col[f]};
-        RowAdapters<1> adapters;
-        adapters.begin(a, row, cols, 0, 1);
-        adapters.add(a, reinterpret_cast<f32x16(&)[1]>(acc[rb][f]));
-      }
+    for (int rb = 0; rb < 2; ++rb) {
+      const int p = rt.p0 + (32 * rb + c < rt.rows ? 32 * rb + c : 0);
+      out[rb] = MODE == kDown ? a.plan.order[p] : (int)x_row<MODE>(a, p);
+    }
+    if constexpr (MODE == kDown) {
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb) w[rb] = a.weights[out[rb]];
     }
   }
 #pragma unroll
   for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const int row = 32 * rb + 8 * (r >> 2) + 4 * h + (r & 3);
-      if (row >= rt.rows) continue;
+      const int at = 8 * (r >> 2) + 4 * h + (r & 3);
       if constexpr (MODE == kSwiglu) {
-        if (tile >= tiles) continue;
+        if (32 * rb + at >= rt.rows || tile >= tiles) continue;
         const float hv = silu(acc[rb][0][r]) * acc[rb][1][r];
-        a.y16[(int64_t)(rt.p0 + row) * a.ldy + col[0]] = __builtin_bit_cast(uint16_t, (f16)hv);
+        a.y16[(int64_t)(rt.p0 + 32 * rb + at) * a.ldy + col[0]] = __builtin_bit_cast(uint16_t, (f16)hv);
       } else {
-        const int64_t out = MODE == kDown ? a.plan.order[rt.p0 + row] : x_row<MODE>(a, rt.p0 + row);
-        const float w = MODE == kDown ? a.weights[out] : 1.f;
+        const int64_t y0 = (int64_t)__shfl(out[rb], at) * a.ldy;
+        const float ws = MODE == kDown ? __shfl(w[rb], at) : 1.f;
+        if (32 * rb + at >= rt.rows) continue;
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           if (col[f] >= a.n) continue;
-          const float v = MODE == kDown ? w * acc[rb][f][r] : acc[rb][f][r];
-          if (MODE == kDown || a.y != nullptr) a.y[out * a.ldy + col[f]] = v;
+          const float v = MODE == kDown ? ws * acc[rb][f][r] : acc[rb][f][r];
+          if (MODE == kDown || a.y != nullptr) a.y[y0 + col[f]] = v;
           if (MODE == kLora && a.y16 != nullptr)
-            a.y16[out * a.ldy + col[f]] = __builtin_bit_cast(uint16_t, (f16)v);
+            a.y16[y0 + col[f]] = __builtin_bit_cast(uint16_t, (f16)v);
         }
       }
     }

@@ -75,10 +75,20 @@ bool stack_overlaps(const qlin_weight* w, int64_t experts, Range r) {
 }
 
 // ---------------------------------------------------------------- experts --
-// Up to this many (token, slot) pairs each pair reads its expert's weights by
-// itself: no plan, and a token's slots are added by the work-group that
-// multiplies them.
+// Up to this many (token, slot) pairs, and up to this many bytes of codes if no
+// two of them share an expert, each pair reads its expert's weights by itself: no
+// plan, and a token's slots are added by the work-group that multiplies them.
+// Alone : grouped, 64 experts of 2048 x 1024 at 4 bits (3.4 MB each) took
+// 13 : 24 us for 8 pairs, 35 : 35 us for 32, 68 : 50 us for 64; 8 of 4096 x 1792
+// at 8 bits (22 MB) 24 : 27 us for 4 pairs, 50 : 43 us for 8, 82 : 48 us for 16.
 constexpr int kDirectPairs = 32;
+constexpr int64_t kDirectBytes = 112 << 20;
+
+// From this many rows per expert on 64-row tiles are used, if tiled_form()
+// agrees: 32-row : 64-row tiles, 64 experts of 2048 x 1024 at 4 bits 81 : 81 us at
+// 16 rows each, 105 : 104 us at 32, 131 : 113 us at 48; 16 of 4096 x 1792 at 8
+// bits 100 : 106 us at 16, 128 : 112 us at 32.
+constexpr int kTiledRows = 32;
 
 struct MoePlan {
   int64_t pairs;
@@ -90,11 +100,17 @@ struct MoePlan {
   int64_t bytes;
 };
 
-MoePlan moe_plan(int inner, int model, int experts, int m, int top_k, void* ws) {
+MoePlan moe_plan(const qlin_weight* gate, const qlin_weight* down, int experts, int m, int64_t ld_x,
+                 int top_k, void* ws) {
+  const int inner = gate->n, model = gate->k;
   MoePlan p{};
   p.pairs = (int64_t)m * top_k;
-  p.direct = p.pairs <= kDirectPairs;
-  const int height = p.direct ? 1 : p.pairs >= 16 * (int64_t)experts ? 64 : 32;
+  p.direct = p.pairs <= kDirectPairs &&
+             p.pairs * (2 * packed_bytes(inner, model, gate->bits) +
+                        packed_bytes(model, inner, down->bits)) <= kDirectBytes;
+  const bool tiled = p.pairs >= kTiledRows * (int64_t)experts &&
+                     tiled_form(inner, kSwiglu, p.pairs / 64 + experts / 2, m, ld_x, model);
+  const int height = p.direct ? 1 : tiled ? 64 : 32;
   p.up.height = p.down.height = height;
   const int ki = inner / kBlock, km = model / kBlock;
   if (p.direct) {
@@ -111,7 +127,7 @@ MoePlan moe_plan(int inner, int model, int experts, int m, int top_k, void* ws) 
   Arena ar{static_cast<char*>(ws)};
   p.h = ar.take<uint16_t>(p.pairs * inner);
   if (!p.direct) {
-    p.rows = take_plan(ar, p.pairs, experts, height);
+    p.rows = take_plan(ar, p.pairs, experts, 32);    // (enough for 64-row tiles)
     p.d = ar.take<float>(p.pairs * model);
   }
   p.bytes = ar.at;
@@ -135,10 +151,13 @@ qlin_status check_moe(const qlin_weight* gate, const qlin_weight* up, const qlin
 }
 
 // --------------------------------------------------------------- adapters --
-// From this many rows on they are ordered by adapter: A x is then formed on the
-// matrix cores, 16 rows of one adapter at a time, and a tile of the product
-// holds few adapters.  Below, each row reads its own adapter.
-constexpr int kSortRows = 128;
+// Rows are ordered by adapter if m * rank reaches this, and always for 64-row
+// tiles: A x is then formed on the matrix cores, 16 rows of one adapter at a time,
+// and a tile of the product holds few adapters.  Below, each row reads its own
+// adapter.  Rows as they come : ordered, rank 64 on 2048 x 2048 25 : 28 us for 256
+// rows, 40 : 34 us for 512; rank 16 on 4096 x 4096 58 : 66 us for 512; rank 8 on 896
+// x 4864 41 : 47 us for 1024.
+constexpr int64_t kSortRanks = 20480;
 
 struct LoraPlan {
   RowsCfg cfg;
@@ -151,13 +170,14 @@ struct LoraPlan {
   int64_t bytes;
 };
 
-LoraPlan lora_plan(const qlin_weight* w, const qlin_adapters* ad, int m, void* ws) {
+LoraPlan lora_plan(const qlin_weight* w, const qlin_adapters* ad, int m, int64_t ld_x, void* ws) {
   LoraPlan p{};
-  p.cfg.height = m >= 1024 ? 64 : 32;
+  const bool tiled = tiled_form(w->n, kLora, (m + 63) / 64, m, ld_x, w->k);
+  p.cfg.height = tiled ? 64 : 32;
   p.cfg.tiles = (m + p.cfg.height - 1) / p.cfg.height;
   ksplit_form(p.cfg, w->k / kBlock, tiles_of(w->n) * p.cfg.tiles);
   p.rp = (ad->rank + 15) / 16 * 16;
-  p.sorted = m >= kSortRows;
+  p.sorted = tiled || (int64_t)m * ad->rank >= kSortRanks;
   p.splits = 1;
   const int steps = (w->k + 127) / 128;
   p.steps = steps;
@@ -229,7 +249,7 @@ qlin_status qlin_route(const qlin_router* r, const float* logits, int32_t m, int
 int64_t qlin_moe_mlp_workspace_bytes(const qlin_weight* gate, const qlin_weight* down,
                                      int32_t experts, int32_t m, int32_t top_k) {
   if (check_moe(gate, gate, down, experts, m, top_k) != QLIN_OK || m == 0) return 0;
-  return moe_plan(gate->n, gate->k, experts, m, top_k, nullptr).bytes;
+  return moe_plan(gate, down, experts, m, gate->k, top_k, nullptr).bytes;
 }
 
 qlin_status qlin_moe_mlp(const qlin_weight* gate, const qlin_weight* up, const qlin_weight* down,
@@ -248,7 +268,7 @@ qlin_status qlin_moe_mlp(const qlin_weight* gate, const qlin_weight* up, const q
       !aligned16(workspace))
     return QLIN_ERR_ALIGN;
   const int inner = gate->n, model = gate->k;
-  const MoePlan p = moe_plan(inner, model, experts, m, top_k, workspace);
+  const MoePlan p = moe_plan(gate, down, experts, m, ld_x, top_k, workspace);
   if (!rows_fits(inner, kSwiglu, p.up) || !rows_fits(model, kDown, p.down)) return QLIN_ERR_SHAPE;
   if (workspace == nullptr || workspace_bytes < p.bytes) return QLIN_ERR_WORKSPACE;
   const int64_t span = (int64_t)(m - 1) * ld_y + model;
@@ -312,7 +332,8 @@ qlin_status qlin_moe_mlp(const qlin_weight* gate, const qlin_weight* up, const q
 
 int64_t qlin_gemm_lora_workspace_bytes(const qlin_weight* w, const qlin_adapters* ad, int32_t m) {
   if (check_lora(w, ad, m) != QLIN_OK || m == 0) return 0;
-  return lora_plan(w, ad, m, nullptr).bytes;
+  // (a larger stride of X never needs more)
+  return lora_plan(w, ad, m, w->k, nullptr).bytes;
 }
 
 qlin_status qlin_gemm_lora(const qlin_weight* w, const qlin_adapters* ad, const uint16_t* X,
@@ -330,7 +351,7 @@ qlin_status qlin_gemm_lora(const qlin_weight* w, const qlin_adapters* ad, const 
   if (!aligned16(X) || !aligned16(Y) || !aligned16(Y16) || !aligned16(ad->a) ||
       !aligned16(ad->b) || !aligned4(ad->scale) || !aligned4(ids) || !aligned16(workspace))
     return QLIN_ERR_ALIGN;
-  const LoraPlan p = lora_plan(w, ad, m, workspace);
+  const LoraPlan p = lora_plan(w, ad, m, ld_x, workspace);
   if (!rows_fits(w->n, kLora, p.cfg)) return QLIN_ERR_SHAPE;
   if (workspace == nullptr || workspace_bytes < p.bytes) return QLIN_ERR_WORKSPACE;
   const int64_t span = (int64_t)(m - 1) * ld_y + w->n;

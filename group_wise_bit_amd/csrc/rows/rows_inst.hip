@@ -6,10 +6,9 @@ namespace qlin {
 
 constexpr int kB = QLIN_INST_BITS;
 
-
 template <int B, int MODE>
 void launch_mode(const RowsArgs& a, RowsCfg c, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.cols * c.tiles)), block(c.height == 64 ? 256 : 64 * c.waves);
+  const dim3 grid((unsigned)((int64_t)a.cols * c.tiles)), block(rows_threads(c));
   if constexpr (MODE == kSwiglu || MODE == kToken) {
     if (c.height == 1) {
       if (c.half) {

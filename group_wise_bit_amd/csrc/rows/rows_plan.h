@@ -40,10 +40,25 @@ inline int rows_cols(int n, int mode, RowsCfg c) {
   return mode == kSwiglu ? (tiles + 1) / 2 : (tiles + 3) / 4;
 }
 
+inline int rows_threads(RowsCfg c) { return c.height == 64 ? 256 : 64 * c.waves; }
+
 // Whether the grid of such a product can be launched (HIP counts threads in
 // 32 bits).
 inline bool rows_fits(int n, int mode, RowsCfg c) {
-  return (int64_t)rows_cols(n, mode, c) * c.tiles * (c.height == 64 ? 256 : 64 * c.waves) < ((int64_t)1 << 32);
+  return (int64_t)rows_cols(n, mode, c) * c.tiles * rows_threads(c) < ((int64_t)1 << 32);
+}
+
+// Whether the 64-row form is used for about `tiles` row tiles of m rows of
+// stride ld, k values each.  It takes 0.5 us per K-block and work-group on a CU
+// however few there are, so it needs a work-group for every other CU: of 32-row
+// against 64-row tiles, adapters on 4096 x 4096 (4 bits) took 58 : 73 us for 512
+// rows (128 work-groups), 82 : 75 us for 768; on 2048 x 2048 40 : 62 us for 512
+// (64), 69 : 63 us for 1024; 8 experts of 1024 x 512 32 : 36 us at 128 rows each
+// (80), 42 : 40 us at 256.  It reads X by 32-bit offsets.
+inline bool tiled_form(int n, int mode, int64_t tiles, int64_t m, int64_t ld, int64_t k) {
+  RowsCfg c{};
+  c.height = 64;
+  return rows_cols(n, mode, c) * tiles >= 144 && ((m - 1) * ld + k) * 2 < ((int64_t)1 << 32);
 }
 
 template <int B>
