@@ -234,13 +234,18 @@ __global__ __launch_bounds__(512) void k_lora_shrink_row(const ShrinkArgs s) {
 // Many rows, ordered by adapter: one work-group per 16 rows of one adapter and
 // K split.  v_mfma_f32_16x16x32_f16: lane (c, q) supplies row c of X and rank
 // row 16 i + c of A at K positions 8q .. +7 of each 32; the 8 waves take
-// 128-column steps in turn and add their sums in LDS in wave order.
+// 128-column steps in turn and add their sums in LDS in wave order.  Bound by the
+// first reads of A and X: the tiles of one adapter go to one XCD, which brought
+// 2048 rows of rank 64 and 8 adapters of 4096 columns from 22 to 15 us (32 rows
+// per work-group, half of the reads of A: 16 us; 4 splits of K for 2 cost the
+// product that adds them 5 us).
 template <int NR>
 __global__ __launch_bounds__(512) void k_lora_shrink_tile(const ShrinkArgs s) {
   __shared__ f32x4 red[8][NR][64];
-  const int y = blockIdx.x, sp = blockIdx.y;
-  if (y >= *s.plan.ntiles) return;
-  const int4 tile = s.plan.tiles[y];
+  const int total = *s.plan.ntiles * s.splits;
+  if ((int)blockIdx.x >= total) return;
+  const int at = xcd_position(total), sp = at % s.splits;
+  const int4 tile = s.plan.tiles[at / s.splits];
   const int slot = tile.x, p0 = tile.y, rows = tile.z;
   const int lane = lane_id(), wave = wave_id();
   const int c = lane & 15, q = lane >> 4;

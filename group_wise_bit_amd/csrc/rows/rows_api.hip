@@ -390,7 +390,7 @@ qlin_status qlin_gemm_lora(const qlin_weight* w, const qlin_adapters* ad, const 
     s.steps = p.steps;
     hipLaunchKernelGGL(k_rows_plan, dim3(1), dim3(kPlanWaves * 64), 0, stream, ids, m, ad->slots, 16,
                        p.rows);
-    const dim3 grid(p.tiles, p.splits), block(512);
+    const dim3 grid(p.tiles * p.splits), block(512);
     if (p.rp <= 16) hipLaunchKernelGGL((k_lora_shrink_tile<1>), grid, block, 0, stream, s);
     else if (p.rp <= 32) hipLaunchKernelGGL((k_lora_shrink_tile<2>), grid, block, 0, stream, s);
     else if (p.rp <= 64) hipLaunchKernelGGL((k_lora_shrink_tile<4>), grid, block, 0, stream, s);
