@@ -10,14 +10,26 @@ namespace qlin {
 // A stable counting sort of `count` ids: positions 0 .. count-1 hold the
 // indexes of the ids, bucket after bucket, in order within a bucket; ids
 // outside [0, buckets) share a last bucket.  Also the table of row tiles: up
-// to `rows` positions of one bucket each.  One work-group: wave w takes the
-// w-th 16th of the ids and counts it in counters of its own, the counters are
-// turned into starts, and a second pass writes the positions, 64 ids at a
-// time: each lane sets its bit in its bucket's mask, and the bits below its own
-// are the equal ids before it.  The atomics (LDS, one wave's) count and OR, so
-// the order is the ids' own.  (Masks by ballots over the id's bits took 60 of
-// 90 instructions per 64 ids: 16384 ids over 32 buckets 29 us.)
+// to `rows` positions of one bucket each.  A work-group takes a share of the ids
+// (few ids: all of them), wave w the w-th 16th of it, counted in counters of its
+// own; the counters are turned into starts, and a second pass writes the
+// positions, 64 ids at a time: each lane sets its bit in its bucket's mask, and the
+// bits below its own are the equal ids before it.  The atomics (LDS, one wave's)
+// count and OR, so the order is the ids' own.  (Masks by ballots over the id's bits took 60 of
+// 90 instructions per 64 ids: one work-group took 29 us for 16384 ids over 32
+// buckets; with the masks 18 us.)  Beyond kPlanIds the ids are shared out, each
+// work-group's counts having been written by k_rows_count before: 4096 ids took 5.5
+// us in one work-group and 8.6 us shared, 16384 18 and 8.3 us, 65536 10.4 us shared.
 constexpr int kPlanWaves = 16;
+constexpr int kPlanIds = 8192;
+constexpr int kPlanGroups = 64;          // work-groups at most
+
+// Ids of a work-group's share (count: of all).
+__host__ __device__ inline int plan_share(int count) {
+  if (count <= kPlanIds) return count;
+  const int groups = count / 1024 < kPlanGroups ? count / 1024 : kPlanGroups;
+  return ((count + groups - 1) / groups + 1023) / 1024 * 1024;
+}
 
 // Sum of v over the lanes below this one.
 __device__ __forceinline__ int lanes_before(int v) {
@@ -49,8 +61,28 @@ __device__ __forceinline__ void counters_written() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// counts[work-group][bucket] of the shares, bucket `buckets` the ids outside.
+__global__ __launch_bounds__(1024) void k_rows_count(const int32_t* __restrict__ ids, int count,
+                                                     int buckets, int32_t* __restrict__ counts) {
+  __shared__ int hist[kMaxExperts + 1];
+  for (int i = threadIdx.x; i <= buckets; i += 1024) hist[i] = 0;
+  __syncthreads();
+  const int share = plan_share(count);
+  const int64_t i0 = (int64_t)blockIdx.x * share;
+  const int end = (int)min((int64_t)count, i0 + share);
+  for (int i = (int)i0 + threadIdx.x; i < end; i += 1024) {
+    const int id = ids[i];
+    atomicAdd(&hist[(uint32_t)id < (uint32_t)buckets ? id : buckets], 1);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i <= buckets; i += 1024)
+    counts[(int64_t)blockIdx.x * (buckets + 1) + i] = hist[i];
+}
+
+// counts: of the shares, or null where one work-group takes all ids.
 __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
-    const int32_t* __restrict__ ids, int count, int buckets, int rows, RowPlan plan) {
+    const int32_t* __restrict__ ids, int count, int buckets, int rows,
+    const int32_t* __restrict__ counts, RowPlan plan) {
   __shared__ int hist[kPlanWaves][kMaxExperts + 1];
   __shared__ unsigned long long mask[kPlanWaves][kMaxExperts + 1];
   __shared__ int part[kPlanWaves][2];
@@ -62,8 +94,10 @@ __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
       mask[w][i] = 0;
     }
   __syncthreads();
-  const int share = ((count + kPlanWaves * 64 - 1) / (kPlanWaves * 64)) * 64;
-  const int i0 = min(count, wave * share), i1 = min(count, i0 + share);
+  const int all = plan_share(count);
+  const int g0 = blockIdx.x * all, g1 = min(count, g0 + all);   // (the last share starts below count)
+  const int share = ((g1 - g0 + kPlanWaves * 64 - 1) / (kPlanWaves * 64)) * 64;
+  const int i0 = min(g1, g0 + wave * share), i1 = min(g1, i0 + share);
   // the buckets of 8 x 64 ids, loaded together
   constexpr int U = 8;
   int id8[U];
@@ -83,8 +117,9 @@ __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
     }
   }
   __syncthreads();
-  // thread t: bucket t's count, starts of its waves, its start and its tiles'
-  int total = 0;
+  // thread t: bucket t's count, starts of its waves, its start and its tiles'; the
+  // ids of earlier shares come first in it
+  int total = 0, earlier = 0;
   if (tid <= buckets) {
     for (int w = 0; w < kPlanWaves; ++w) {
       const int c = hist[w][tid];
@@ -92,19 +127,33 @@ __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
       total += c;
     }
   }
+  if (counts != nullptr && tid <= buckets) {
+    total = 0;
+    const int groups = gridDim.x;
+    for (int b = 0; b < groups; b += 16) {
+      int c[16];
+#pragma unroll
+      for (int g = 0; g < 16; ++g) c[g] = counts[min(b + g, groups - 1) * (buckets + 1) + tid];
+#pragma unroll
+      for (int g = 0; g < 16; ++g) {
+        if (b + g < groups) total += c[g];
+        if (b + g < (int)blockIdx.x) earlier += c[g];
+      }
+    }
+  }
   const int mine = tid < buckets ? (total + rows - 1) / rows : 0;
   int end = total, tend = mine;
   group_scan2(end, tend, part);
   const int start = end - total;
   if (tid <= buckets) {
-    for (int w = 0; w < kPlanWaves; ++w) hist[w][tid] += start;
-    if (tid == buckets) *plan.ntiles = tend;
+    for (int w = 0; w < kPlanWaves; ++w) hist[w][tid] += start + earlier;
+    if (tid == buckets && blockIdx.x == 0) *plan.ntiles = tend;
     first[tid] = make_int2(tend - mine, start);
   }
   __syncthreads();
   // tile i belongs to the last bucket that starts at or before it
   const int ntiles = first[buckets].x;
-  for (int i = tid; i < ntiles; i += kPlanWaves * 64) {
+  for (int i = blockIdx.x * kPlanWaves * 64 + tid; i < ntiles; i += gridDim.x * kPlanWaves * 64) {
     int lo = 0, hi = buckets;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -144,7 +193,8 @@ __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
 // ------------------------------------------------- sum over a token's experts --
 // Y[i, :] = the rows of its valid (token, slot) pairs, added in slot order.
 // One thread: 4 columns of one token (n is a multiple of 64), the rows of 8
-// slots requested together.
+// slots requested together.  Bound by the fp32 rows' bytes: 4 slots of 4096 tokens
+// of 2048 columns, 151 MB, 22 us (6.9 TB/s: part of them is still in the caches).
 __global__ __launch_bounds__(256) void k_rows_combine(
     const float* __restrict__ d, const int32_t* __restrict__ ids, int m, int top_k, int experts,
     int n, float* __restrict__ y, uint16_t* __restrict__ y16, int64_t ldy) {

@@ -306,7 +306,10 @@ struct RowAdapters {
 // Work-group: up to 32 rows of one expert x 32 CB columns (half or all of a
 // 64-row weight tile; kSwiglu: of gate and of up).  Its waves take the K-blocks
 // w, w + WAVES, ..., U at a time with every load in flight before the first
-// decode, and add their sums in LDS in wave order.  Bound by the weights' bytes.
+// decode, and add their sums in LDS in wave order.  Bound by the latency of the
+// few loads between start and sums: 216 pairs over 128 experts of 512 x 1024 at 3
+// bits, 44 MB of gate and up, take 18 us (2.4 TB/s), their down projections at 4
+// bits 10 us, 40 rows on 6144 x 4096 at 4 bits 19 us.
 // Lane (c, h) supplies X row c / weight row c and K positions 32h + 8s .. +7.
 // (Two waves per SIMD at least: with the register file to itself the compiler
 // keeps the MFMA results in accumulation registers and copies every one out.)
@@ -441,7 +444,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
 // dot products: with one row of X the matrix cores would be idle in 31 of 32
 // rows, and few outputs per work-group spread even a small product over all CUs
 // (the 2048 outputs of a token's down projections: 14.3 us as 64 work-groups of
-// 32 columns).  Bound by vector instructions and launch latency.
+// 32 columns; now 6.0 us, and 7.7 us for gate and up of 8 experts of 1024 x 2048 at
+// 4 bits, 9.4 MB).  Bound by launch latency and one round of loads.
 template <int BITS, int MODE, int NG, int WAVES, int U>
 __global__ __launch_bounds__(WAVES * 64) void k_rows_gemv(const RowsArgs a) {
   constexpr int WPB = 2 * BITS;
@@ -558,6 +562,14 @@ __device__ __forceinline__ void here(f16x8& v) { asm volatile("" : "+v"(v)); }
 // X by direct-to-LDS loads into four stages, three blocks ahead (and the next
 // block's first operands are read before the barrier), codes two blocks ahead in
 // registers; one barrier per block.
+// Bound by instruction issue: 205 vector instructions beside 16 MFMAs a block, of
+// them 64 the scaling and 72 decoding (4 bits); one issues in 93 % of the cycles of
+// 16384 pairs through 32 experts of 2 x 1408 x 2048 (243 us, 780 TFLOP/s; MFMA busy
+// 50 %), in 82 % of their down projections (147 us, K of 22 blocks only).  2048
+// rows on 4096 x 4096 without adapters: 81 us, 64 of them in the loop.  128 rows x
+// 128 columns (130 vector instructions a block, twice the operand reads) took the
+// same 81 us there and 359 for 331 us over 64 experts of 256 rows; two waves a
+// work-group 402 for 386 us.
 // Codes, scales and zeros come through buffer descriptors: the base and the
 // block's offset are scalars, so a load costs no vector address, neither the
 // instructions that form one nor the registers that a loop keeps one in (48

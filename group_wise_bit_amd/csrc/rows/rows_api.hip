@@ -43,6 +43,20 @@ RowPlan take_plan(Arena& ar, int64_t count, int buckets, int height) {
   return p;
 }
 
+// Scratch of the grouping of `count` ids: its work-groups' counts.
+int32_t* take_counts(Arena& ar, int64_t count, int buckets) {
+  return count > kPlanIds ? ar.take<int32_t>((int64_t)kPlanGroups * (buckets + 1)) : nullptr;
+}
+
+void run_plan(const int32_t* ids, int count, int buckets, int rows, int32_t* counts, RowPlan plan,
+              hipStream_t st) {
+  const int share = plan_share(count), groups = (count + share - 1) / share;
+  if (counts != nullptr)
+    hipLaunchKernelGGL(k_rows_count, dim3(groups), dim3(1024), 0, st, ids, count, buckets, counts);
+  hipLaunchKernelGGL(k_rows_plan, dim3(groups), dim3(kPlanWaves * 64), 0, st, ids, count, buckets,
+                     rows, counts, plan);
+}
+
 int64_t code_words(const qlin_weight* w) { return packed_bytes(w->n, w->k, w->bits) / 4; }
 
 void set_weight(RowsArgs& a, int i, const qlin_weight* w) {
@@ -95,6 +109,7 @@ struct MoePlan {
   bool direct;
   RowsCfg up, down;    // forms of the two products
   RowPlan rows;
+  int32_t* counts;
   uint16_t* h;
   float* d;
   int64_t bytes;
@@ -128,6 +143,7 @@ MoePlan moe_plan(const qlin_weight* gate, const qlin_weight* down, int experts, 
   p.h = ar.take<uint16_t>(p.pairs * inner);
   if (!p.direct) {
     p.rows = take_plan(ar, p.pairs, experts, 32);    // (enough for 64-row tiles)
+    p.counts = take_counts(ar, p.pairs, experts);
     p.d = ar.take<float>(p.pairs * model);
   }
   p.bytes = ar.at;
@@ -163,6 +179,7 @@ struct LoraPlan {
   RowsCfg cfg;
   bool sorted;         // rows are ordered by adapter first
   RowPlan rows;
+  int32_t* counts;
   int tiles;           // (sorted) 16-row tiles of one adapter, at most
   int splits, steps;   // K splits of A x, 128-column steps of each
   float* t;
@@ -189,6 +206,7 @@ LoraPlan lora_plan(const qlin_weight* w, const qlin_adapters* ad, int m, int64_t
     p.steps = (steps + p.splits - 1) / p.splits;
     p.splits = (steps + p.steps - 1) / p.steps;
     p.rows = take_plan(ar, m, ad->slots, 16);
+    p.counts = take_counts(ar, m, ad->slots);
   }
   p.t = ar.take<float>((int64_t)p.splits * m * p.rp);
   p.bytes = ar.at;
@@ -289,8 +307,7 @@ qlin_status qlin_moe_mlp(const qlin_weight* gate, const qlin_weight* up, const q
   st = check_device();
   if (st != QLIN_OK) return st;
   if (!p.direct)
-    hipLaunchKernelGGL(k_rows_plan, dim3(1), dim3(kPlanWaves * 64), 0, stream, ids, (int)p.pairs,
-                       experts, p.up.height, p.rows);
+    run_plan(ids, (int)p.pairs, experts, p.up.height, p.counts, p.rows, stream);
   RowsArgs a{};
   set_weight(a, 0, gate);
   set_weight(a, 1, up);
@@ -388,8 +405,7 @@ qlin_status qlin_gemm_lora(const qlin_weight* w, const qlin_adapters* ad, const 
     s.plan = p.rows;
     s.splits = p.splits;
     s.steps = p.steps;
-    hipLaunchKernelGGL(k_rows_plan, dim3(1), dim3(kPlanWaves * 64), 0, stream, ids, m, ad->slots, 16,
-                       p.rows);
+    run_plan(ids, m, ad->slots, 16, p.counts, p.rows, stream);
     const dim3 grid(p.tiles * p.splits), block(512);
     if (p.rp <= 16) hipLaunchKernelGGL((k_lora_shrink_tile<1>), grid, block, 0, stream, s);
     else if (p.rp <= 32) hipLaunchKernelGGL((k_lora_shrink_tile<2>), grid, block, 0, stream, s);

@@ -87,7 +87,7 @@ qlin_status qlin_route(const qlin_router* r, const float* logits, int32_t m, int
  * Every product x * (q - z) is exact, scales are applied and sums held in fp32;
  * silu(g) * u is rounded once to fp16 (infinite from 65520 on), the down
  * projection's operand.  Deterministic: each row's result depends on its own
- * inputs, m, top_k and experts only.
+ * inputs and on the call's sizes and strides only.
  * workspace_bytes >= qlin_moe_mlp_workspace_bytes(gate, down, experts, m,
  * top_k), or QLIN_ERR_WORKSPACE (0 is returned there for invalid arguments).
  */
@@ -117,8 +117,10 @@ typedef struct qlin_adapters {
  * Outputs as for qlin_moe_mlp: Y fp32 and / or Y16 fp16, both [m, ld_y],
  * ld_y >= n.  Every product x * (q - z) and x * a is exact, scales are applied
  * and sums held in fp32; A_a x_i enters the second product with 22 bits.
- * Deterministic.  A row that is not finite through its adapter changes no
- * other row.
+ * Deterministic: each row's result depends on its own inputs, on the call's
+ * sizes and strides and, to the order of fp32 sums, on the ids of the rows that
+ * share its tile.  A row that is not finite through its adapter changes no other
+ * row.
  * workspace_bytes >= qlin_gemm_lora_workspace_bytes(w, ad, m), or
  * QLIN_ERR_WORKSPACE (0 is returned there for invalid arguments).
  */

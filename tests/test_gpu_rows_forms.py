@@ -83,6 +83,20 @@ def test_many_ids_to_group(m, experts, top_k):
     moe_check(ws, what, rows(rng, m, 64), ids, w, "many ids")
 
 
+@pytest.mark.parametrize("m", [8191, 8193, 66000, 540000])
+def test_many_ids_of_few_kinds(m):
+    """Rows of 5 kinds through 3 experts or none: 20 results, each at its rows."""
+    rng = np.random.default_rng(m)
+    ws, what = experts_of(rng, 3, 64, 64, 4, 4)
+    kinds = rows(rng, 5, 64)
+    kind, e = rng.integers(0, 5, m), rng.integers(-1, 3, m)
+    ref, err = rr.moe_ref(np.repeat(kinds, 4, 0), *what, np.tile(np.arange(-1, 3, dtype=np.int32), 5)[:, None],
+                          np.ones((20, 1), np.float32))
+    y, _ = call(ws, kinds[kind], e.astype(np.int32)[:, None], np.ones((m, 1), np.float32))
+    at = 4 * kind + e + 1
+    rr.check(y.cpu().numpy(), ref[at], err[at], f"{m} ids")
+
+
 def test_rows_far_apart():
     """Rows of X over more than 4 GB take the forms with 64-bit addresses."""
     m, pitch = 660, 1 << 22
