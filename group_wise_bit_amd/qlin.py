@@ -532,20 +532,25 @@ def _same_device(dev: torch.device, named) -> None:
             raise ValueError(f"{name} is on {t.device}, the inputs on {dev}")
 
 
-# The current stream's handle without the wrapper object torch.cuda.current_stream()
-# builds (about 3 us of a call's 12), where torch offers it.
+# The current stream's handle, device and capture state without the wrappers (the
+# object torch.cuda.current_stream() builds takes about 3 us of a call's 12, the
+# initialization checks 1), where torch offers them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing",
+                     torch.cuda.is_current_stream_capturing)
 
 
 def _launch(dev: torch.device, call):
     """call(raw stream) with the tensors' device current and its current stream."""
     if dev.type != "cuda":
         raise ValueError(f"the tensors must be on a GPU, not on {dev}")
-    if dev.index == torch.cuda.current_device():
-        return call(_raw_stream(dev.index))
+    index = dev.index
+    if index == _current_device():
+        return call(_raw_stream(index))
     with torch.cuda.device(dev):
-        return call(_raw_stream(dev.index))
+        return call(_raw_stream(index))
 
 
 def _with_workspace(ws, dev: torch.device, need, call, where: str) -> None:
@@ -563,7 +568,7 @@ def _with_workspace(ws, dev: torch.device, need, call, where: str) -> None:
             if not ws.is_contiguous():
                 raise ValueError("ws must be contiguous")
             return call(ws.data_ptr(), ws.numel() * ws.element_size(), stream)
-        if torch.cuda.is_current_stream_capturing():
+        if _capturing():
             size = need()
             own = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
             return call(_ptr(own), size, stream)
@@ -600,7 +605,7 @@ def _row_pitch(t: torch.Tensor) -> int:
 
 
 def _need_flat(t: torch.Tensor, dtype: torch.dtype, shape: Tuple[int, ...], name: str) -> None:
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape or \
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or \
             not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
 
@@ -660,15 +665,17 @@ class Router(_CStruct):
 def route(router: Router, logits: torch.Tensor, ids: Optional[torch.Tensor] = None,
           weights: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """qlin_route: (ids int32, weights fp32), both [m, top_k], of fp32 logits [m, experts]."""
+    experts = router.experts
     if not isinstance(logits, torch.Tensor) or logits.dtype != torch.float32 or \
-            logits.dim() != 2 or logits.shape[1] != router.experts or \
-            (logits.shape[0] > 0 and logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise TypeError(f"logits must be a float32 [m, {router.experts}] tensor with contiguous rows")
+            logits.dim() != 2 or logits.shape[1] != experts or \
+            (experts > 1 and logits.shape[0] > 0 and logits.stride(1) != 1):
+        raise TypeError(f"logits must be a float32 [m, {experts}] tensor with contiguous rows")
     m, dev = logits.shape[0], logits.device
     c = router.c_struct()
     if router.top_k < 1:
         raise ValueError("top_k must be at least 1")
     shape = (m, router.top_k)
+    _same_device(dev, (("bias", router.bias), ("ids", ids), ("weights", weights)))
     if ids is None:
         ids = torch.empty(shape, dtype=torch.int32, device=dev)
     else:
@@ -677,7 +684,6 @@ def route(router: Router, logits: torch.Tensor, ids: Optional[torch.Tensor] = No
         weights = torch.empty(shape, dtype=torch.float32, device=dev)
     else:
         _need_flat(weights, torch.float32, shape, "weights")
-    _same_device(dev, (("bias", router.bias), ("ids", ids), ("weights", weights)))
     _check(_launch(dev, lambda stream: _lib().qlin_route(
         ctypes.byref(c), logits.data_ptr(), m, _row_pitch(logits), ids.data_ptr(),
         weights.data_ptr(), stream)), "qlin_route")
