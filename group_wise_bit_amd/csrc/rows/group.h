@@ -18,8 +18,8 @@ namespace qlin {
 // count and OR, so the order is the ids' own.  (Masks by ballots over the id's bits took 60 of
 // 90 instructions per 64 ids: one work-group took 29 us for 16384 ids over 32
 // buckets; with the masks 18 us.)  Beyond kPlanIds the ids are shared out, each
-// work-group's counts having been written by k_rows_count before: 4096 ids took 5.5
-// us in one work-group and 8.6 us shared, 16384 18 and 8.3 us, 65536 10.4 us shared.
+// work-group's counts having been written by k_rows_count before: 8192 ids take 6.9
+// us in one work-group, 16384 18 us and shared 7.7, 65536 shared 10.
 constexpr int kPlanWaves = 16;
 constexpr int kPlanIds = 8192;
 constexpr int kPlanGroups = 64;          // work-groups at most
@@ -88,12 +88,11 @@ __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
   __shared__ int part[kPlanWaves][2];
   __shared__ int2 first[kMaxExperts + 1];    // each bucket's first tile and position
   const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
-  for (int w = 0; w < kPlanWaves; ++w)
-    for (int i = tid; i <= buckets; i += kPlanWaves * 64) {
-      hist[w][i] = 0;
-      mask[w][i] = 0;
-    }
-  __syncthreads();
+  for (int i = lane; i <= buckets; i += 64) {
+    hist[wave][i] = 0;
+    mask[wave][i] = 0;
+  }
+  counters_written();
   const int all = plan_share(count);
   const int g0 = blockIdx.x * all, g1 = min(count, g0 + all);   // (the last share starts below count)
   const int share = ((g1 - g0 + kPlanWaves * 64 - 1) / (kPlanWaves * 64)) * 64;
@@ -119,13 +118,14 @@ __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
   __syncthreads();
   // thread t: bucket t's count, starts of its waves, its start and its tiles'; the
   // ids of earlier shares come first in it
-  int total = 0, earlier = 0;
-  if (tid <= buckets) {
-    for (int w = 0; w < kPlanWaves; ++w) {
-      const int c = hist[w][tid];
-      hist[w][tid] = total;
-      total += c;
-    }
+  int total = 0, earlier = 0, before[kPlanWaves];
+#pragma unroll
+  for (int w = 0; w < kPlanWaves; ++w) before[w] = tid <= buckets ? hist[w][tid] : 0;
+#pragma unroll
+  for (int w = 0; w < kPlanWaves; ++w) {
+    const int c = before[w];
+    before[w] = total;
+    total += c;
   }
   if (counts != nullptr && tid <= buckets) {
     total = 0;
@@ -146,7 +146,8 @@ __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
   group_scan2(end, tend, part);
   const int start = end - total;
   if (tid <= buckets) {
-    for (int w = 0; w < kPlanWaves; ++w) hist[w][tid] += start + earlier;
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) hist[w][tid] = start + earlier + before[w];
     if (tid == buckets && blockIdx.x == 0) *plan.ntiles = tend;
     first[tid] = make_int2(tend - mine, start);
   }
@@ -174,14 +175,14 @@ __global__ __launch_bounds__(kPlanWaves * 64) void k_rows_plan(
       if (in) atomicOr(&mask[wave][id], 1ull << lane);
       counters_written();
       const uint64_t m = mask[wave][id];
-      const int before = __builtin_popcountll(m & ((1ull << lane) - 1));
+      const int below = __builtin_popcountll(m & ((1ull << lane) - 1));
       int at = 0;
       if (in) {
-        at = hist[wave][id] + before;
+        at = hist[wave][id] + below;
         plan.order[at] = b + lane;
       }
       counters_written();
-      if (in && before == 0) {
+      if (in && below == 0) {
         hist[wave][id] = at + __builtin_popcountll(m);
         mask[wave][id] = 0;
       }
