@@ -79,6 +79,13 @@ __device__ __forceinline__ const T* lane_ptr(const T* p, int64_t uniform, uint32
 //   kToken   one token: its slots' sums times their weights, fp32 and / or fp16
 enum RowsMode { kSwiglu = 0, kDown = 1, kLora = 2, kToken = 3 };
 
+// Adapters of rows as they come, up to this rank: each thread adds those of its own
+// outputs by fp32 fma, all of B requested at once.  Above, one adapter after the
+// other on the matrix cores: 40 rows of 64 adapters of rank 32 on 6144 x 4096 took
+// 24.7 us so and 21.2 by threads, 16 rows 16.4 and 13.6; 512 rows in runs of one
+// adapter of rank 16 on 4096 x 4096 61 and 63, in mixed order 72 and 63.
+constexpr int kDotRank = 32;
+
 struct RowsArgs {
   const uint32_t* codes[2];
   const uint16_t* scale[2];
@@ -99,6 +106,7 @@ struct RowsArgs {
   const float* t;                 // [splits][m][rp]: scale * A x, partial sums over K
   const uint16_t* b;              // [slots][n][rank]
   int slots, rank, rp, tsplits;   // rp: rank rounded up to 16, t is 0 from rank on
+  bool dots;                      // 32-row form, rank <= kDotRank, one split
 };
 
 // A work-group's rows: positions p0 .. p0 + rows - 1 of expert e, and its column.
@@ -352,8 +360,37 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
   int col[CB];
 #pragma unroll
   for (int cb = 0; cb < CB; ++cb) col[cb] = t * kTile + 32 * (cb0 + cb) + c;
-  if constexpr (MODE == kLora)
-    adapters.begin(a, c < rows ? xr : -1, c < rows ? a.ids[xr] : -1, col, wave, WAVES);
+  // (dots) A x of the tile's rows goes to LDS, and every thread adds its own outputs'
+  // adapters: their ids, of output p at row out_row(p), column out_col(p)
+  constexpr int kDotQ = kDotRank / 8;
+  __shared__ f32x4 ts[MODE == kLora ? 32 * 2 * kDotQ : 1];
+  auto out_row = [&](int p) __attribute__((always_inline)) {
+    const int r = (wave + WAVES * p) & 15;
+    return 8 * (r >> 2) + 4 * h + (r & 3);
+  };
+  auto out_col = [&](int p) __attribute__((always_inline)) {
+    return t * kTile + 32 * (cb0 + ((wave + WAVES * p) >> 4)) + c;
+  };
+  constexpr int TV = MODE == kLora ? (32 * 2 * kDotQ + WAVES * 64 - 1) / (WAVES * 64) : 1;
+  f32x4 tv[TV];
+  int slot[PT];
+  if constexpr (MODE == kLora) {
+    if (a.dots) {
+#pragma unroll
+      for (int i = 0; i < TV; ++i) {
+        // (a row without an adapter has any bits there, and no use for them)
+        const int e = threadIdx.x + WAVES * 64 * i, row = e / (2 * kDotQ), r = 4 * (e % (2 * kDotQ));
+        tv[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        if (row < rows && r < a.rp)
+          tv[i] = *reinterpret_cast<const f32x4*>(a.t + x_row<MODE>(a, p0 + row) * a.rp + r);
+      }
+#pragma unroll
+      for (int p = 0; p < PT; ++p)
+        slot[p] = out_row(p) < rows ? a.ids[x_row<MODE>(a, p0 + out_row(p))] : -1;
+    } else {
+      adapters.begin(a, c < rows ? xr : -1, c < rows ? a.ids[xr] : -1, col, wave, WAVES);
+    }
+  }
   for (int jb = wave; jb < a.kb; jb += WAVES * U) {
     f16x8 xa[U][4];
     uint32_t wl[U][NM][CB][HW];
@@ -397,7 +434,30 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
         }
     }
   }
-  if constexpr (MODE == kLora) adapters.add(a, acc[0]);
+  constexpr int PC = PT < 4 ? PT : 4;        // outputs whose B is requested together
+  uint4 bq[PC][kDotQ];
+  auto request_b = [&](int p1) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < PC; ++i) {
+      const bool has = (uint32_t)slot[p1 + i] < (uint32_t)a.slots && out_col(p1 + i) < a.n;
+      const uint16_t* b = a.b + (has ? ((int64_t)slot[p1 + i] * a.n + out_col(p1 + i)) * a.rank : 0);
+#pragma unroll
+      for (int q = 0; q < kDotQ; ++q)
+        if (8 * q < a.rank) bq[i][q] = *reinterpret_cast<const uint4*>(b + 8 * q);
+    }
+  };
+  if constexpr (MODE == kLora) {
+    if (a.dots) {
+#pragma unroll
+      for (int i = 0; i < TV; ++i) {
+        const int e = threadIdx.x + WAVES * 64 * i;
+        if (e < 32 * 2 * kDotQ) ts[e] = tv[i];
+      }
+      request_b(0);
+    } else {
+      adapters.add(a, acc[0]);
+    }
+  }
   // thread (wave, lane) finishes registers wave, wave + WAVES, ... of the CB x 16
   float v[NM][PT];
 #pragma unroll
@@ -416,11 +476,32 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
       v[i][p] = sum;
     }
   }
+  if constexpr (MODE == kLora) {
+    if (a.dots) {
+#pragma unroll
+      for (int p1 = 0; p1 < PT; p1 += PC) {
+        if (p1 > 0) request_b(p1);
+#pragma unroll
+        for (int i = 0; i < PC; ++i) {
+          float s = 0.f;
+#pragma unroll
+          for (int q = 0; q < kDotQ; ++q) {
+            if (8 * q >= a.rank) continue;
+            const f32x4 x = ts[2 * kDotQ * out_row(p1 + i) + 2 * q], y = ts[2 * kDotQ * out_row(p1 + i) + 2 * q + 1];
+            const f16x8 b = u4_to_f16x8(bq[i][q]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s = __builtin_fmaf(x[e], (float)b[e], s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s = __builtin_fmaf(y[e], (float)b[4 + e], s);
+          }
+          if ((uint32_t)slot[p1 + i] < (uint32_t)a.slots) v[0][p1 + i] += s;
+        }
+      }
+    }
+  }
 #pragma unroll
   for (int p = 0; p < PT; ++p) {
-    const int r = (wave + WAVES * p) & 15;
-    const int cl = t * kTile + 32 * (cb0 + ((wave + WAVES * p) >> 4)) + c;
-    const int row = 8 * (r >> 2) + 4 * h + (r & 3);
+    const int cl = out_col(p), row = out_row(p);
     if (row >= rows || cl >= a.n) continue;
     if constexpr (MODE == kSwiglu) {
       const float hv = silu(v[0][p]) * v[1][p];

@@ -431,6 +431,7 @@ qlin_status qlin_gemm_lora(const qlin_weight* w, const qlin_adapters* ad, const 
   a.slots = ad->slots;
   a.rank = ad->rank;
   a.rp = p.rp;
+  a.dots = !p.sorted && ad->rank <= kDotRank;
   run_rows(a, w->bits, kLora, p.cfg, stream);
   return hip_status(hipGetLastError());
 }

@@ -116,7 +116,7 @@ typedef struct qlin_adapters {
  * X fp16 [m, ld_x] (ld_x >= k, % 8 == 0); ids int32 [m], 4-byte aligned.
  * Outputs as for qlin_moe_mlp: Y fp32 and / or Y16 fp16, both [m, ld_y],
  * ld_y >= n.  Every product x * (q - z) and x * a is exact, scales are applied
- * and sums held in fp32; A_a x_i enters the second product with 22 bits.
+ * and sums held in fp32; A_a x_i enters the second product with 22 bits or more.
  * Deterministic: each row's result depends on its own inputs, on the call's
  * sizes and strides and, to the order of fp32 sums, on the ids of the rows that
  * share its tile.  A row that is not finite through its adapter changes no other
