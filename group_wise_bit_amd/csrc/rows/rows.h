@@ -106,7 +106,6 @@ struct RowsArgs {
   const float* t;                 // [splits][m][rp]: scale * A x, partial sums over K
   const uint16_t* b;              // [slots][n][rank]
   int slots, rank, rp, tsplits;   // rp: rank rounded up to 16, t is 0 from rank on
-  bool dots;                      // 32-row form, rank <= kDotRank, one split
 };
 
 // A work-group's rows: positions p0 .. p0 + rows - 1 of expert e, and its column.
@@ -321,7 +320,7 @@ struct RowAdapters {
 // Lane (c, h) supplies X row c / weight row c and K positions 32h + 8s .. +7.
 // (Two waves per SIMD at least: with the register file to itself the compiler
 // keeps the MFMA results in accumulation registers and copies every one out.)
-template <int BITS, int MODE, int WAVES, int CB, int U>
+template <int BITS, int MODE, int WAVES, int CB, int U, bool DOTS>
 __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a) {
   constexpr int WPB = 2 * BITS;
   constexpr int HW = BITS;                   // words of a half block
@@ -360,10 +359,10 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
   int col[CB];
 #pragma unroll
   for (int cb = 0; cb < CB; ++cb) col[cb] = t * kTile + 32 * (cb0 + cb) + c;
-  // (dots) A x of the tile's rows goes to LDS, and every thread adds its own outputs'
+  // (DOTS) A x of the tile's rows goes to LDS, and every thread adds its own outputs'
   // adapters: their ids, of output p at row out_row(p), column out_col(p)
   constexpr int kDotQ = kDotRank / 8;
-  __shared__ f32x4 ts[MODE == kLora ? 32 * 2 * kDotQ : 1];
+  __shared__ f32x4 ts[DOTS ? 32 * 2 * kDotQ : 1];
   auto out_row = [&](int p) __attribute__((always_inline)) {
     const int r = (wave + WAVES * p) & 15;
     return 8 * (r >> 2) + 4 * h + (r & 3);
@@ -375,7 +374,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
   f32x4 tv[TV];
   int slot[PT];
   if constexpr (MODE == kLora) {
-    if (a.dots) {
+    if constexpr (DOTS) {
 #pragma unroll
       for (int i = 0; i < TV; ++i) {
         // (a row without an adapter has any bits there, and no use for them)
@@ -447,7 +446,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
     }
   };
   if constexpr (MODE == kLora) {
-    if (a.dots) {
+    if constexpr (DOTS) {
 #pragma unroll
       for (int i = 0; i < TV; ++i) {
         const int e = threadIdx.x + WAVES * 64 * i;
@@ -477,7 +476,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
     }
   }
   if constexpr (MODE == kLora) {
-    if (a.dots) {
+    if constexpr (DOTS) {
 #pragma unroll
       for (int p1 = 0; p1 < PT; p1 += PC) {
         if (p1 > 0) request_b(p1);

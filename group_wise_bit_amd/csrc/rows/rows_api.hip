@@ -195,6 +195,7 @@ LoraPlan lora_plan(const qlin_weight* w, const qlin_adapters* ad, int m, int64_t
   ksplit_form(p.cfg, w->k / kBlock, tiles_of(w->n) * p.cfg.tiles);
   p.rp = (ad->rank + 15) / 16 * 16;
   p.sorted = tiled || (int64_t)m * ad->rank >= kSortRanks;
+  p.cfg.dots = !p.sorted && ad->rank <= kDotRank;
   p.splits = 1;
   const int steps = (w->k + 127) / 128;
   p.steps = steps;
@@ -431,7 +432,6 @@ qlin_status qlin_gemm_lora(const qlin_weight* w, const qlin_adapters* ad, const 
   a.slots = ad->slots;
   a.rank = ad->rank;
   a.rp = p.rp;
-  a.dots = !p.sorted && ad->rank <= kDotRank;
   run_rows(a, w->bits, kLora, p.cfg, stream);
   return hip_status(hipGetLastError());
 }

@@ -6,6 +6,16 @@ namespace qlin {
 
 constexpr int kB = QLIN_INST_BITS;
 
+template <int B, int MODE, bool DOTS>
+void launch_ksplit(const RowsArgs& a, RowsCfg c, dim3 grid, hipStream_t st) {
+  constexpr int U = MODE == kSwiglu && B > 4 ? 1 : 2;   // by the registers of a block
+  const dim3 block(64 * c.waves);
+  if (c.half) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 8, 1, 2, DOTS>), grid, block, 0, st, a);
+  else if (c.waves == 8) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 8, 2, U, DOTS>), grid, block, 0, st, a);
+  else if (c.waves == 4) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 4, 2, U, DOTS>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 2, 2, U, DOTS>), grid, block, 0, st, a);
+}
+
 template <int B, int MODE>
 void launch_mode(const RowsArgs& a, RowsCfg c, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)a.cols * c.tiles)), block(rows_threads(c));
@@ -22,12 +32,17 @@ void launch_mode(const RowsArgs& a, RowsCfg c, hipStream_t st) {
     }
   }
   if constexpr (MODE != kToken) {
-    constexpr int U = MODE == kSwiglu && B > 4 ? 1 : 2;   // by the registers of a block
-    if (c.height == 64) hipLaunchKernelGGL((k_rows_tiled<B, MODE>), grid, block, 0, st, a);
-    else if (c.half) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 8, 1, 2>), grid, block, 0, st, a);
-    else if (c.waves == 8) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 8, 2, U>), grid, block, 0, st, a);
-    else if (c.waves == 4) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 4, 2, U>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 2, 2, U>), grid, block, 0, st, a);
+    if (c.height == 64) {
+      hipLaunchKernelGGL((k_rows_tiled<B, MODE>), grid, block, 0, st, a);
+      return;
+    }
+    if constexpr (MODE == kLora) {
+      if (c.dots) {
+        launch_ksplit<B, MODE, true>(a, c, grid, st);
+        return;
+      }
+    }
+    launch_ksplit<B, MODE, false>(a, c, grid, st);
   }
 }
 

@@ -14,6 +14,7 @@ struct RowsCfg {
   int tiles;           // row tiles of the grid (those past the plan's end exit)
   int waves;           // (1 and 32 rows) waves per work-group
   bool half;           // 32 columns per work-group (32 rows), 8 (one row)
+  bool dots;           // (32 rows) adapters of rank <= kDotRank, rows as they come
 };
 
 // (32 rows) The form for kb K-blocks and about `groups` work-groups of 64
