@@ -82,7 +82,7 @@ enum RowsMode { kSwiglu = 0, kDown = 1, kLora = 2, kToken = 3 };
 // Adapters of rows as they come, up to this rank: each thread adds those of its own
 // outputs by fp32 fma, all of B requested at once.  Above, one adapter after the
 // other on the matrix cores: 40 rows of 64 adapters of rank 32 on 6144 x 4096 took
-// 24.7 us so and 21.2 by threads, 16 rows 16.4 and 13.6; 512 rows in runs of one
+// 24.7 us so and 20.4 by threads, 16 rows 16.4 and 13.6; 512 rows in runs of one
 // adapter of rank 16 on 4096 x 4096 61 and 63, in mixed order 72 and 63.
 constexpr int kDotRank = 32;
 
@@ -316,7 +316,8 @@ struct RowAdapters {
 // decode, and add their sums in LDS in wave order.  Bound by the latency of the
 // few loads between start and sums: 216 pairs over 128 experts of 512 x 1024 at 3
 // bits, 44 MB of gate and up, take 18 us (2.4 TB/s), their down projections at 4
-// bits 10 us, 40 rows on 6144 x 4096 at 4 bits 19 us.
+// bits 10 us, 40 rows on 6144 x 4096 at 4 bits with adapters 16 us.  More blocks in
+// flight (3, 4) changed nothing (16.4, 15.9 us).
 // Lane (c, h) supplies X row c / weight row c and K positions 32h + 8s .. +7.
 // (Two waves per SIMD at least: with the register file to itself the compiler
 // keeps the MFMA results in accumulation registers and copies every one out.)
