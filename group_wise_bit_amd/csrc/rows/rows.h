@@ -646,10 +646,10 @@ __device__ __forceinline__ void here(f16x8& v) { asm volatile("" : "+v"(v)); }
 // Bound by instruction issue: 205 vector instructions beside 16 MFMAs a block, of
 // them 64 the scaling and 72 decoding (4 bits); one issues in 93 % of the cycles of
 // 16384 pairs through 32 experts of 2 x 1408 x 2048 (243 us, 780 TFLOP/s; MFMA busy
-// 50 %), in 82 % of their down projections (147 us, K of 22 blocks only).  2048
-// rows on 4096 x 4096 without adapters: 81 us, 64 of them in the loop.  128 rows x
-// 128 columns (130 vector instructions a block, twice the operand reads) took the
-// same 81 us there and 359 for 331 us over 64 experts of 256 rows; two waves a
+// 50 %), in 82 % of their down projections (147 us; K has 22 blocks only).  2048
+// rows on 4096 x 4096 without adapters: 78 us, 64 of them in the loop.  128 rows x
+// 128 columns (130 vector instructions a block, twice the operand reads) took 81
+// us there, as this form did then, and 359 for 331 us over 64 experts of 256 rows; two waves a
 // work-group 402 for 386 us.
 // Codes, scales and zeros come through buffer descriptors: the base and the
 // block's offset are scalars, so a load costs no vector address, neither the
@@ -892,11 +892,22 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
       adapters.add(a, acc[rb]);
     }
   }
-  // (kDown, kLora) lane c's row c of each row block: its output row and weight,
-  // read together and handed to the lanes that store it
-  int out[2];
-  float w[2];
-  if constexpr (MODE != kSwiglu) {
+  if constexpr (MODE == kSwiglu) {
+    if (tile >= tiles) return;
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int at = 32 * rb + 8 * (r >> 2) + 4 * h + (r & 3);
+        if (at >= rt.rows) continue;
+        const float hv = silu(acc[rb][0][r]) * acc[rb][1][r];
+        a.y16[(int64_t)(rt.p0 + at) * a.ldy + col[0]] = __builtin_bit_cast(uint16_t, (f16)hv);
+      }
+  } else {
+    // lane c's row c of each row block: its output row and weight, read together
+    // and handed to the lanes that store it
+    int out[2];
+    float w[2] = {1.f, 1.f};
 #pragma unroll
     for (int rb = 0; rb < 2; ++rb) {
       const int p = rt.p0 + (32 * rb + c < rt.rows ? 32 * rb + c : 0);
@@ -906,30 +917,41 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
 #pragma unroll
       for (int rb = 0; rb < 2; ++rb) w[rb] = a.weights[out[rb]];
     }
-  }
 #pragma unroll
-  for (int rb = 0; rb < 2; ++rb)
+    for (int rb = 0; rb < 2; ++rb)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int at = 8 * (r >> 2) + 4 * h + (r & 3);
-      if constexpr (MODE == kSwiglu) {
-        if (32 * rb + at >= rt.rows || tile >= tiles) continue;
-        const float hv = silu(acc[rb][0][r]) * acc[rb][1][r];
-        a.y16[(int64_t)(rt.p0 + 32 * rb + at) * a.ldy + col[0]] = __builtin_bit_cast(uint16_t, (f16)hv);
-      } else {
-        const int64_t y0 = (int64_t)__shfl(out[rb], at) * a.ldy;
-        const float ws = MODE == kDown ? __shfl(w[rb], at) : 1.f;
-        if (32 * rb + at >= rt.rows) continue;
+      for (int r = 0; r < 16; ++r) {
+        if constexpr (MODE == kDown) {
+          const int at = 8 * (r >> 2) + 4 * h + (r & 3);
+          const int64_t y0 = (int64_t)__shfl(out[rb], at) * a.ldy;
+          const float ws = __shfl(w[rb], at);
+          if (32 * rb + at >= rt.rows) continue;
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          if (col[f] >= a.n) continue;
-          const float v = MODE == kDown ? ws * acc[rb][f][r] : acc[rb][f][r];
-          if (MODE == kDown || a.y != nullptr) a.y[y0 + col[f]] = v;
-          if (MODE == kLora && a.y16 != nullptr)
-            a.y16[y0 + col[f]] = __builtin_bit_cast(uint16_t, (f16)v);
+          for (int f = 0; f < 2; ++f)
+            if (col[f] < a.n) a.y[y0 + col[f]] = ws * acc[rb][f][r];
+        } else {
+          // A register of either column block holds rows R and R + 4 in the wave's
+          // halves: with the inner halves swapped, each is 64 columns of one row,
+          // a whole line of fp16 (81 -> 77 us for 2048 rows on 4096 x 4096; fp32 rows
+          // of the experts, two half lines a store as they are, lost by it: 145 -> 165).
+          const float x = acc[rb][0][r], y = acc[rb][1][r];
+          const auto v = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x),
+                                                          __builtin_bit_cast(uint32_t, y), false, false);
+          const int cl = tile * kTile + lane;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int at = 8 * (r >> 2) + (r & 3) + 4 * i;
+            if (32 * rb + at >= rt.rows) continue;
+            const int64_t o = (int64_t)__builtin_amdgcn_readlane(out[rb], at) * a.ldy + cl;
+            const uint32_t bits = v[i];
+            const float s = __builtin_bit_cast(float, bits);
+            if (cl >= a.n) continue;
+            if (a.y != nullptr) a.y[o] = s;
+            if (a.y16 != nullptr) a.y16[o] = __builtin_bit_cast(uint16_t, (f16)s);
+          }
         }
       }
-    }
+  }
 }
 
 }  // namespace qlin
