@@ -136,8 +136,8 @@ MoePlan moe_plan(const qlin_weight* gate, const qlin_weight* down, int experts, 
   } else {
     p.up.tiles = p.down.tiles = (int)tile_bound(p.pairs, experts, height);
     const int64_t used = p.pairs < experts ? p.pairs : experts;   // at most
-    ksplit_form(p.up, km, tiles_of(inner) * used);
-    ksplit_form(p.down, ki, tiles_of(model) * used);
+    ksplit_form(p.up, tiles_of(inner) * used);
+    ksplit_form(p.down, tiles_of(model) * used);
   }
   Arena ar{static_cast<char*>(ws)};
   p.h = ar.take<uint16_t>(p.pairs * inner);
@@ -192,7 +192,7 @@ LoraPlan lora_plan(const qlin_weight* w, const qlin_adapters* ad, int m, int64_t
   const bool tiled = tiled_form(w->n, kLora, (m + 63) / 64, m, ld_x, w->k);
   p.cfg.height = tiled ? 64 : 32;
   p.cfg.tiles = (m + p.cfg.height - 1) / p.cfg.height;
-  ksplit_form(p.cfg, w->k / kBlock, tiles_of(w->n) * p.cfg.tiles);
+  ksplit_form(p.cfg, tiles_of(w->n) * p.cfg.tiles);
   p.rp = (ad->rank + 15) / 16 * 16;
   p.sorted = tiled || (int64_t)m * ad->rank >= kSortRanks;
   p.cfg.dots = !p.sorted && ad->rank <= kDotRank;

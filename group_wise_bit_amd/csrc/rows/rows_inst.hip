@@ -12,8 +12,7 @@ void launch_ksplit(const RowsArgs& a, RowsCfg c, dim3 grid, hipStream_t st) {
   const dim3 block(64 * c.waves);
   if (c.half) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 8, 1, 2, DOTS>), grid, block, 0, st, a);
   else if (c.waves == 8) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 8, 2, U, DOTS>), grid, block, 0, st, a);
-  else if (c.waves == 4) hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 4, 2, U, DOTS>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 2, 2, U, DOTS>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_rows_ksplit<B, MODE, 4, 2, U, DOTS>), grid, block, 0, st, a);
 }
 
 template <int B, int MODE>
@@ -21,13 +20,9 @@ void launch_mode(const RowsArgs& a, RowsCfg c, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)a.cols * c.tiles)), block(rows_threads(c));
   if constexpr (MODE == kSwiglu || MODE == kToken) {
     if (c.height == 1) {
-      if (c.half) {
-        if (c.waves == 16) hipLaunchKernelGGL((k_rows_gemv<B, MODE, 8, 16, 4>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((k_rows_gemv<B, MODE, 8, 8, 4>), grid, block, 0, st, a);
-      } else {
-        if (c.waves == 16) hipLaunchKernelGGL((k_rows_gemv<B, MODE, 4, 16, 4>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((k_rows_gemv<B, MODE, 4, 8, 4>), grid, block, 0, st, a);
-      }
+      if (!c.half) hipLaunchKernelGGL((k_rows_gemv<B, MODE, 4, 8, 4>), grid, block, 0, st, a);
+      else if (c.waves == 16) hipLaunchKernelGGL((k_rows_gemv<B, MODE, 8, 16, 4>), grid, block, 0, st, a);
+      else hipLaunchKernelGGL((k_rows_gemv<B, MODE, 8, 8, 4>), grid, block, 0, st, a);
       return;
     }
   }

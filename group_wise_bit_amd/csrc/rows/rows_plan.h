@@ -7,8 +7,8 @@
 namespace qlin {
 
 // The work-group form of a product over rows: one row x 8 or 16 columns (kSwiglu,
-// kToken), up to 32 rows x 32 or 64 columns with K over 2 .. 16 waves, or 64
-// rows x 128 columns (kSwiglu: half as many of each matrix).
+// kToken), up to 32 rows x 32 or 64 columns with K over 4 or 8 waves, or 64
+// rows x 256 columns (kSwiglu: half as many of each matrix).
 struct RowsCfg {
   int height;          // rows of X per work-group: 1, 32 or 64
   int tiles;           // row tiles of the grid (those past the plan's end exit)
@@ -17,20 +17,28 @@ struct RowsCfg {
   bool dots;           // (32 rows) adapters of rank <= kDotRank, rows as they come
 };
 
-// (32 rows) The form for kb K-blocks and about `groups` work-groups of 64
-// columns.  A wave keeps 2 blocks in flight, so the work-group is sized to cover
-// K in few rounds of loads; a grid that would leave half of the CUs empty takes
-// 32 columns per work-group.
-inline void ksplit_form(RowsCfg& c, int kb, int64_t groups) {
-  c.half = groups < 128;
-  c.waves = c.half || kb > 32 ? 8 : kb > 8 ? 4 : 2;
+// (32 rows) The form for about `groups` work-groups of 64 columns.  Few of them
+// take K over 8 waves, or 32 columns each: of 64 against 32 columns 40 rows on 2048 x
+// 2048 (64 work-groups) took 13.5 : 11.7 us, on 4096 x 4096 (128) 18.6 : 16.4, on 6144 x
+// 4096 (192) 20.5 : 21.7, 333 rows on 896 x 4864 (154) 17 : 24, beyond a work-group
+// per CU.  Of 8 against 4 waves 100 rows on 4096 x 4096 (256) took 19.8 :
+// 21.4 us, on 6144 x 4096 (384) 36.1 : 34.9, on 8192 x 512 (512) 15.8 : 12.7; 27 rows
+// through 8 of 128 experts of 512 x 1024 (1024) 47 : 38, and 39 with 2 waves.
+inline void ksplit_form(RowsCfg& c, int64_t groups) {
+  c.half = groups <= 128;
+  c.waves = groups < 320 ? 8 : 4;
 }
 
-// (1 row) The form for `items` K-blocks and `groups` work-groups of 16 columns: a
-// wave keeps 4 blocks in flight; 8 columns where 16 would not reach every CU.
+// (1 row) The form for `items` K-blocks and `groups` work-groups of 16 columns: 8
+// columns where 16 would not reach every CU, and then 16 waves for a long K.  Of 16
+// against 8 columns a row through 4 of 64 experts of 256 x 512 took 7.4 : 6.7 us, 3 rows
+// through 8 of 64 of 1024 x 2048 27.9 : 28.4; a row through those (first product 512
+// work-groups of 16 columns, second 128, of 128 blocks) 13.3 by this rule, 14.4 with
+// 16 columns and 8 waves in both, 18 with 16 waves in both; of 16 against 8 waves a
+// row through 2 of 8 experts of 512 x 1024 8.0 : 6.8.
 inline void gemv_form(RowsCfg& c, int items, int64_t groups) {
   c.half = groups < 256;
-  c.waves = items > 32 ? 16 : 8;
+  c.waves = c.half && items > 32 ? 16 : 8;
 }
 
 // Work-group columns of a product with n outputs per row.

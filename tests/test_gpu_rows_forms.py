@@ -1,5 +1,5 @@
 """GPU parity of the row-wise products at sizes that take each of their work-group
-forms: one row with 8 and 16 columns and 8 and 16 waves, 32 rows with K over 2, 4
+forms: one row with 8 and 16 columns and 8 and 16 waves, 32 rows with K over 4
 and 8 waves, 64 rows with every remainder of its four K stages, many ids to group,
 rows further apart than 32-bit offsets reach, ranks above one pass."""
 import numpy as np
