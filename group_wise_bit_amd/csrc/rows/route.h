@@ -276,8 +276,11 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, int row, void* val
   if constexpr (kExact) {
     if (mine >= 0) w = a.sigmoid ? 1 / (1 + exp(-(T)xm)) : exp((T)xm - (T)top);
   } else {
-    // (a sigmoid this small needs 64 bits to be renormalized)
-    if (a.sigmoid && __builtin_amdgcn_ballot_w64(xm < -80.f) != 0) return false;
+    // (a score this small, exp(-80) = 1.8e-35 of a softmax's largest, is left to 64 bits:
+    // fp32 has few or no bits of it, and renormalizing or the scale can make it large.
+    // With a bias all of the chosen can be so far below the row's largest logit.)
+    const float below = a.sigmoid ? xm : xm - top;
+    if (__builtin_amdgcn_ballot_w64(mine >= 0 && below < -80.f) != 0) return false;
     if (mine >= 0) w = a.sigmoid ? 1.f / (1.f + expf(-xm)) : exp_below(xm, top);
   }
   const T sum = a.renormalize ? sum64(w) : total;

@@ -57,7 +57,9 @@ typedef struct qlin_router {
  * The choice is that of 64-bit arithmetic on the fp32 logits and bias; without
  * a bias experts are ordered by their logits, which is the order of the exact
  * scores.  Equal values go to the lowest index, among groups too.  Weights
- * are correct to a few units of fp32.
+ * are correct to a few units of fp32, however far below the row's largest logit
+ * the chosen ones lie (scores are 64-bit values: they are whole down to 2^-1022,
+ * exp(-708), and 0 from about exp(-745) on).
  * Masked experts: a logit of -inf or NaN, or a bias of -inf or NaN, takes the
  * expert out of the row (and, a logit, out of the softmax's sum); +inf counts
  * as the largest finite logit.  A row with fewer than top_k experts left has
