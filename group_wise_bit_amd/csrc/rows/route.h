@@ -99,16 +99,18 @@ __device__ __forceinline__ double unordered(uint64_t k) {
   return __builtin_bit_cast(double, k ^ ((uint64_t)((int64_t)~k >> 63) | 0x8000000000000000ull));
 }
 
-// How far a key formed in 32 bits can be from its exact value, `terms` scores
-// added, with u = 2^-24.  Sigmoid: the exponential is off by 2u (1 ulp) + 1.5u |x|
-// (its argument's rounding), which p (1 - p) <= 1/4, p (1 - p) |x| <= 0.23 times
-// reaches p; the sum's rounding and the reciprocal (1 ulp) are 3u: under 4u in
-// all, taken as 6u < 3.6e-7.  Softmax: 2u + 2.5u |x - top| of the exponential (the
-// difference's and its argument's rounding), p |x - top| <= 0.37 of it, 10u of
-// the sum (9 additions deep), 4u of its reciprocal and the product: under 17u,
-// taken as 30u < 1.8e-6.  And the rounding of the sum with the bias, u |key|.
-__device__ __forceinline__ float slack(const RouteArgs& a, float key, float terms) {
-  return terms * ((a.sigmoid ? 3.6e-7f : 1.8e-6f) + 6e-8f * __builtin_fabsf(key));
+// How far a key formed in 32 bits can be from its exact value, with u = 2^-24.
+// Sigmoid: the exponential is off by 2u (1 ulp) + 1.5u |x| (its argument's rounding),
+// which p (1 - p) <= 1/4, p (1 - p) |x| <= 0.23 times reaches p; the sum's rounding
+// and the reciprocal (1 ulp) are 3u: under 4u in all, taken as 6u < 3.6e-7.
+// Softmax, d = top - x: the exponential is off by 2u + 2.5u d (the difference's and
+// its argument's rounding).  The sum is off by its terms' mean of that, and a mean
+// of d over 512 experts or fewer is below 3.9, and by 13u of its additions (7 in a
+// lane, 6 across lanes): 25u; the reciprocal and the product are 3u.  With p <= 1 and
+// p d <= 0.37 that is under 31u, taken as 40u < 2.4e-6.  And the rounding of the sum
+// with the bias, u |key|.
+__device__ __forceinline__ float slack(const RouteArgs& a, float key) {
+  return (a.sigmoid ? 3.6e-7f : 2.4e-6f) + 6e-8f * __builtin_fabsf(key);
 }
 
 // exp(x - top) for finite x <= top, the rounding error of the difference (Knuth's
@@ -188,10 +190,10 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, int row, void* val
       key[i] = live[i] && bias[i] > -kInf ? ordered(p[i] + (T)bias[i]) : 0;
   }
   // whether 32 bits leave it open which of two keys is larger
-  auto close = [&](K larger, K smaller, float terms) __attribute__((always_inline)) {
+  auto close = [&](K larger, K smaller) __attribute__((always_inline)) {
     if constexpr (kExact) return false;
     const float v = unordered((uint32_t)larger);
-    return !(v - unordered((uint32_t)smaller) > 2.f * slack(a, v, terms));
+    return !(v - unordered((uint32_t)smaller) > 2.f * slack(a, v));
   };
   if (a.groups > 1) {
     const int per = a.experts / a.groups;
@@ -223,21 +225,35 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, int row, void* val
     if (s > 2) merge(dpp_u<0x141>(first), dpp_u<0x141>(second));
     if (s > 3) merge(dpp_u<0x140>(first), dpp_u<0x140>(second));
     if (s > 4) merge(__shfl_xor(first, 16), __shfl_xor(second, 16));
-    K gv = a.group_top == 1 || second == 0 ? first : ordered(unordered(first) + unordered(second));
+    const K value =
+        a.group_top == 1 || second == 0 ? first : ordered(unordered(first) + unordered(second));
+    K gv = value;
     uint64_t kept = 0;
-    K last = 0;
     for (int j = 0; j < a.top_groups; ++j) {
       const K best = max64(gv);
       if (best == 0) break;
       const int at = __builtin_ctzll(__builtin_amdgcn_ballot_w64(gv == best)) >> s;
       kept |= 1ull << at;
       gv = g == at ? 0 : gv;
-      last = best;
     }
-    // the last group in and the first one out
-    if (scored && !kExact) {
-      const K out = max64(gv);
-      if (out != 0 && close(last, out, a.group_top == 2 ? 2.f : 1.f)) return false;
+    // 32 bits tell the groups apart if the least that a kept one can be is above the
+    // most that one left out can be.  A value is off by its scores' errors and the
+    // rounding of their sum (6e-8 of their sizes, not of the sum's: they may cancel),
+    // and as much again is taken for the bound's own rounding.
+    if constexpr (!kExact) {
+      if (scored) {
+        const float v = unordered(value), v1 = unordered(first);
+        const bool two = a.group_top == 2 && second != 0;
+        const float v2 = two ? unordered(second) : 0.f;
+        const float off = slack(a, v1) + (two ? slack(a, v2) : 0.f) + 1.2e-7f * __builtin_fabsf(v1) +
+                          1.2e-7f * __builtin_fabsf(v2);
+        const bool in = (kept >> g) & 1;
+        float x = in ? off - v : off + v;
+        x = x < kInf ? x : kInf;             // (NaN: it cannot be told)
+        const uint32_t least = max64(in && value != 0 ? ordered(x) : 0u);
+        const uint32_t most_out = max64(!in && value != 0 ? ordered(x) : 0u);
+        if (least != 0 && most_out != 0 && !(unordered(least) + unordered(most_out) < 0.f)) return false;
+      }
     }
     const float inv = 1.f / (float)per;
 #pragma unroll
@@ -257,7 +273,7 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, int row, void* val
     for (int i = 1; i < EPL; ++i) mx = max(mx, key[i]);
     const K best = max64(mx);
     if (best == 0) break;
-    if (a.bias != nullptr && j > 0 && close(last, best, 1.f)) return false;
+    if (a.bias != nullptr && j > 0 && close(last, best)) return false;
     if (j == a.top_k) break;
     last = best;
     // the lowest expert that has it: the first lane, and its first place
