@@ -296,11 +296,14 @@ def master_weight(w16: torch.Tensor, bits: int, group: int, scale=None, zero=Non
 
 
 _WS: dict = {}
+_WS_RECORDED: list = []       # buffers whose addresses a graph may hold: never freed
 
 
 def workspace(nbytes: int, device: torch.device) -> Optional[torch.Tensor]:
     """Zero-filled workspace, cached per (device, stream); the kernels leave it
-    zero-filled again after every call."""
+    zero-filled again after every call.  A buffer handed out under stream capture
+    stays allocated when a larger one takes its place in the cache: the graph
+    goes on writing to it."""
     if nbytes <= 0:
         return None
     key = (device.index, _stream())
@@ -308,6 +311,8 @@ def workspace(nbytes: int, device: torch.device) -> Optional[torch.Tensor]:
     if buf is None or buf.numel() < nbytes:
         buf = torch.zeros(nbytes, dtype=torch.uint8, device=device)
         _WS[key] = buf
+    if _capturing() and not any(b is buf for b in _WS_RECORDED):
+        _WS_RECORDED.append(buf)
     return buf
 
 
@@ -553,6 +558,11 @@ def _launch(dev: torch.device, call):
         return call(_raw_stream(index))
 
 
+# Workspaces of the row-wise calls, by device and stream: apart from workspace()'s,
+# whose users do not grow with a batch's rows and are recorded by graphs.
+_ROWS_WS: dict = {}
+
+
 def _with_workspace(ws, dev: torch.device, need, call, where: str) -> None:
     """call(workspace pointer, bytes, raw stream) with the caller's workspace or
     the device and stream's own (grown to need() bytes when the library finds
@@ -572,11 +582,12 @@ def _with_workspace(ws, dev: torch.device, need, call, where: str) -> None:
             size = need()
             own = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
             return call(_ptr(own), size, stream)
-        buf = _WS.get((dev.index, stream))
+        buf = _ROWS_WS.get((dev.index, stream))
         st = call(None, 0, stream) if buf is None else call(buf.data_ptr(), buf.numel(), stream)
         if st == 8:                           # QLIN_ERR_WORKSPACE
-            buf = workspace(need(), dev)
-            st = call(_ptr(buf), 0 if buf is None else buf.numel(), stream)
+            buf = torch.empty(need(), dtype=torch.uint8, device=dev)
+            _ROWS_WS[dev.index, stream] = buf
+            st = call(buf.data_ptr(), buf.numel(), stream)
         return st
     _check(_launch(dev, run), where)
 
