@@ -593,11 +593,12 @@ def _with_workspace(ws, dev: torch.device, need, call, where: str) -> None:
 
 
 class _CStruct:
-    """The ctypes form of an object of tensors, built and checked again only
-    when one of its tensors is another (or has moved or changed its size)."""
+    """The ctypes form of an object of tensors, built and checked again whenever
+    one of its tensors is at another address or of another shape, stride or type."""
 
     def _cached(self, tensors, extra, build):
-        key = (*[(t.data_ptr(), t.numel(), t.dtype) for t in tensors if t is not None], *extra)
+        key = (*[None if t is None else (t.data_ptr(), t.shape, t.stride(), t.dtype)
+                 for t in tensors], *extra)
         got = self.__dict__.get("_c")
         if got is None or got[0] != key:
             got = self.__dict__["_c"] = (key, build())
@@ -799,8 +800,7 @@ class Adapters(_CStruct):
     scale: Optional[torch.Tensor] = None
 
     def c_struct(self, w: "QWeight") -> QlinAdaptersC:
-        return self._cached((self.a, self.b, self.scale), (w.n, w.k, *self.a.shape, *self.b.shape),
-                            lambda: self._build(w))
+        return self._cached((self.a, self.b, self.scale), (w.n, w.k), lambda: self._build(w))
 
     def _build(self, w: "QWeight") -> QlinAdaptersC:
         if self.a.dim() != 3:
