@@ -613,7 +613,7 @@ def _need_rows_x(X: torch.Tensor, k: int) -> None:
 
 def _row_pitch(t: torch.Tensor) -> int:
     """Elements from one row to the next (one row has no next: its own length)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def _need_flat(t: torch.Tensor, dtype: torch.dtype, shape: Tuple[int, ...], name: str) -> None:
