@@ -13,6 +13,21 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: long-running CPU check")
 
 
+# Tests with a call that passes every host check with made-up addresses, so that only the
+# absence of a GPU ends it: with one, its kernel would read and write there.
+NO_GPU_ONLY = ("test_rows_boundary.py::test_route_refusals",)
+
+
+def pytest_collection_modifyitems(items):
+    import torch
+    if not torch.cuda.is_available():
+        return
+    for item in items:
+        if item.nodeid.endswith(NO_GPU_ONLY):
+            item.add_marker(pytest.mark.skip(reason="makes a call with made-up addresses: "
+                                                    "only without a GPU"))
+
+
 @pytest.fixture
 def launch_override():
     """Set a launch-shape override (qlin_set_launch_override) for one test;
