@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 from typing import List, Optional, Sequence, Tuple
 
@@ -561,6 +562,9 @@ def _launch(dev: torch.device, call):
 # Workspaces of the row-wise calls, by device and stream: apart from workspace()'s,
 # whose users do not grow with a batch's rows and are recorded by graphs.
 _ROWS_WS: dict = {}
+# Held while a call is enqueued on such a buffer: its launches hand their results on in
+# it, and another thread's call on the same stream must not come between them.
+_ROWS_LOCK = threading.Lock()
 
 
 def _with_workspace(ws, dev: torch.device, need, call, where: str) -> None:
@@ -582,13 +586,14 @@ def _with_workspace(ws, dev: torch.device, need, call, where: str) -> None:
             size = need()
             own = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
             return call(_ptr(own), size, stream)
-        buf = _ROWS_WS.get((dev.index, stream))
-        st = call(None, 0, stream) if buf is None else call(buf.data_ptr(), buf.numel(), stream)
-        if st == 8:                           # QLIN_ERR_WORKSPACE
-            buf = torch.empty(need(), dtype=torch.uint8, device=dev)
-            _ROWS_WS[dev.index, stream] = buf
-            st = call(buf.data_ptr(), buf.numel(), stream)
-        return st
+        with _ROWS_LOCK:
+            buf = _ROWS_WS.get((dev.index, stream))
+            st = call(None, 0, stream) if buf is None else call(buf.data_ptr(), buf.numel(), stream)
+            if st == 8:                       # QLIN_ERR_WORKSPACE
+                buf = torch.empty(need(), dtype=torch.uint8, device=dev)
+                _ROWS_WS[dev.index, stream] = buf
+                st = call(buf.data_ptr(), buf.numel(), stream)
+            return st
     _check(_launch(dev, run), where)
 
 

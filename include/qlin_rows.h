@@ -13,7 +13,9 @@
  * calls, and it needs no initialization, with one exception that lets it be
  * the buffer that qlin_gemm and the others share: its first 65536 bytes are
  * left as they are.  Calls that can run at the same time (other streams, two
- * captured graphs) need workspaces of their own.
+ * captured graphs) need workspaces of their own, and so do calls that two
+ * threads enqueue on one stream at the same time: a call's kernels hand their
+ * results on in its workspace.
  */
 #ifndef QLIN_ROWS_H
 #define QLIN_ROWS_H
