@@ -73,7 +73,14 @@ __device__ __forceinline__ const T* lane_ptr(const T* p, int64_t uniform, uint32
 
 // ------------------------------------------------------------------ launches --
 // What a product over rows does with its sums:
-//   kSwiglu  two matrices (gate, up): fp16 silu(g) * u, one row per position
+//   kSwiglu  two matrices (gate, up): fp16 silu(g) * u, one row per position.  The one
+//            rounding to fewer bits on the way: it is the operand of the next product,
+//            as x itself is, and as in the dense gate/up and down calls.  It leaves fp16
+//            outputs off by 2.9e-4 (rms, relative) where rounding the output alone
+//            leaves 2.1e-4, and is infinite from 65520 on.  Two halves of 22 bits would
+//            be two MFMAs for each of the down product's: those alone took 16384 pairs
+//            through 32 experts of 2 x 1408 x 2048 from 379 to 425 us, 1018 pairs
+//            through 16 of 1792 x 4096 at 8 bits from 136 to 145.
 //   kDown    fp32 weights[index] * sum, one row per index (pair of token and slot)
 //   kLora    sum + the row's adapter, fp32 and / or fp16
 //   kToken   one token: its slots' sums times their weights, fp32 and / or fp16
@@ -315,8 +322,8 @@ struct RowAdapters {
 // w, w + WAVES, ..., U at a time with every load in flight before the first
 // decode, and add their sums in LDS in wave order.  Bound by the latency of the
 // few loads between start and sums: 216 pairs over 128 experts of 512 x 1024 at 3
-// bits, 44 MB of gate and up, take 18 us (2.4 TB/s), their down projections at 4
-// bits 10 us, 40 rows on 6144 x 4096 at 4 bits with adapters 16 us.  More blocks in
+// bits, 38 MB of gate and up fetched (all 128 are 57 MB), take 18 us (2.1 TB/s), their
+// down projections at 4 bits 10 us, 40 rows on 6144 x 4096 at 4 bits with adapters 16 us.  More blocks in
 // flight (3, 4) changed nothing (16.4, 15.9 us).
 // Lane (c, h) supplies X row c / weight row c and K positions 32h + 8s .. +7.
 // (Two waves per SIMD at least: with the register file to itself the compiler
@@ -525,8 +532,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
 // dot products: with one row of X the matrix cores would be idle in 31 of 32
 // rows, and few outputs per work-group spread even a small product over all CUs
 // (the 2048 outputs of a token's down projections: 14.3 us as 64 work-groups of
-// 32 columns; now 6.0 us, and 7.7 us for gate and up of 8 experts of 1024 x 2048 at
-// 4 bits, 9.4 MB).  Bound by launch latency and one round of loads.
+// 32 columns; now 6.0 us, and 7.8 us for gate and up of 8 experts of 1024 x 2048 at
+// 4 bits, 18.4 MB).  Bound by launch latency and one round of loads.
 template <int BITS, int MODE, int NG, int WAVES, int U>
 __global__ __launch_bounds__(WAVES * 64) void k_rows_gemv(const RowsArgs a) {
   constexpr int WPB = 2 * BITS;
@@ -645,8 +652,9 @@ __device__ __forceinline__ void here(f16x8& v) { asm volatile("" : "+v"(v)); }
 // registers; one barrier per block.
 // Bound by instruction issue: 205 vector instructions beside 16 MFMAs a block, of
 // them 64 the scaling and 72 decoding (4 bits); one issues in 93 % of the cycles of
-// 16384 pairs through 32 experts of 2 x 1408 x 2048 (243 us, 780 TFLOP/s; MFMA busy
-// 50 %), in 82 % of their down projections (147 us; K has 22 blocks only).  2048
+// 16384 pairs through 32 experts of 2 x 1408 x 2048 (212 to 264 us over 12 calls, 890 to
+// 720 TFLOP/s; MFMA busy 50 %), in 82 % of their down projections (127 to 160 us; K has
+// 22 blocks only).  2048
 // rows on 4096 x 4096 without adapters: 78 us, 64 of them in the loop.  128 rows x
 // 128 columns (130 vector instructions a block, twice the operand reads) took 81
 // us there, as this form did then, and 359 for 331 us over 64 experts of 256 rows; two waves a
@@ -738,7 +746,7 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
   // Direct-to-LDS loads of X: instruction i of a wave brings 8 rows from row
   // 32 i + 8 wave on, lane l to chunk l of the 64: row l / 8, slot l % 8.  32-bit
   // offsets: from the first row of kDown's consecutive ones, else from X, whose
-  // span the host has checked (rows_span_ok).
+  // span the host has checked (tiled_form).
   const Buffer xbuf = buffer_of(a.X + (MODE == kDown ? rt.p0 * a.ldx : 0), 0xffffffff);
   uint32_t xoff[2];
 #pragma unroll

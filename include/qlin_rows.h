@@ -7,7 +7,8 @@
  * enqueues kernels on the caller's stream and returns without synchronizing;
  * nothing about the ids is read on the host.  All of a call's pointers must
  * belong to the current device.  m = 0 is a no-op in every call (pointers are
- * then not looked at).
+ * then not looked at).  A product whose grid would have 2^32 threads is refused
+ * with QLIN_ERR_SHAPE (rows, one per token and slot, times columns: none below 2^35).
  *
  * Workspaces.  A call's workspace is scratch: nothing in it is kept between
  * calls, and it needs no initialization, with one exception that lets it be
@@ -89,8 +90,9 @@ qlin_status qlin_route(const qlin_router* r, const float* logits, int32_t m, int
  * Outputs, either may be NULL (not both), leading dimension ld_y >= down.n for
  * both: Y fp32, Y16 the same rounded to fp16 (nearest even).
  * Every product x * (q - z) is exact, scales are applied and sums held in fp32;
- * silu(g) * u is rounded once to fp16 (infinite from 65520 on), the down
- * projection's operand.  Deterministic: each row's result depends on its own
+ * silu(g) * u is rounded once to fp16 (infinite from 65520 on, in steps of 2^-24
+ * below 2^-14), the down projection's operand: that is what outputs, fp32 ones
+ * too, are off by most (3e-4 of a row's usual size).  Deterministic: each row's result depends on its own
  * inputs and on the call's sizes and strides only.
  * workspace_bytes >= qlin_moe_mlp_workspace_bytes(gate, down, experts, m,
  * top_k), or QLIN_ERR_WORKSPACE (0 is returned there for invalid arguments).

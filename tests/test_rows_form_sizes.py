@@ -66,3 +66,14 @@ def test_the_rules_are_the_library_s():
             ad = qlin.QlinAdaptersC(slots, rank, 0x7F0000000000, 0x7F0000000000, None)
             got = q(ctypes.byref(packed(n, k)), ctypes.byref(ad), m)
             assert got == rf.lora_workspace(m, n, k, slots, rank), (m, n, k, rank)
+
+
+def test_a_grid_too_large_is_refused():
+    """A host check before those of the call's addresses and workspace: 2^25 rows of 8192
+    columns, and at 32 rows of X further apart 2^22 rows; not 2^21 rows of them."""
+    import test_rows_boundary as tb
+    big = dict(gate=tb.weight(64, 8192), up=tb.weight(64, 8192, at=4), down=tb.weight(8192, 64, at=8),
+               experts=64, m=1 << 20, ldx=8192, ldy=8192)
+    for top_k in (32, 4):
+        assert tb.moe(qlin.library(), top_k=top_k, wsb=0, **big) == tb.SHAPE
+    assert tb.moe(qlin.library(), top_k=2, wsb=0, **big) == tb.WORKSPACE
