@@ -73,18 +73,33 @@ __device__ __forceinline__ const T* lane_ptr(const T* p, int64_t uniform, uint32
 
 // ------------------------------------------------------------------ launches --
 // What a product over rows does with its sums:
-//   kSwiglu  two matrices (gate, up): fp16 silu(g) * u, one row per position.  The one
-//            rounding to fewer bits on the way: it is the operand of the next product,
-//            as x itself is, and as in the dense gate/up and down calls.  It leaves fp16
-//            outputs off by 2.9e-4 (rms, relative) where rounding the output alone
-//            leaves 2.1e-4, and is infinite from 65520 on.  Two halves of 22 bits would
-//            be two MFMAs for each of the down product's: those alone took 16384 pairs
-//            through 32 experts of 2 x 1408 x 2048 from 379 to 425 us, 1018 pairs
-//            through 16 of 1792 x 4096 at 8 bits from 136 to 145.
+//   kSwiglu  two matrices (gate, up): silu(g) * u as two fp16 halves, one row per
+//            position (put_halves)
 //   kDown    fp32 weights[index] * sum, one row per index (pair of token and slot)
 //   kLora    sum + the row's adapter, fp32 and / or fp16
 //   kToken   one token: its slots' sums times their weights, fp32 and / or fp16
 enum RowsMode { kSwiglu = 0, kDown = 1, kLora = 2, kToken = 3 };
+
+// h = silu(g) * u goes to the down product as a high and a low fp16 half: the low one is
+// what rounding to the high one left, so that the two hold 22 bits of it (in steps of
+// 2^-24 below 2^-3; infinite from 65520 on, as fp16 is).  Each half's products with q - z
+// are exact.  One half left outputs off by 2e-4 (rms, relative), fp32 ones too; two cost
+// twice the MFMAs of the down product: 374 : 440 us for 16384 pairs through 32 experts of
+// 2 x 1408 x 2048, 136 : 149 for 1018 through 16 of 1792 x 4096 at 8 bits, 32.7 : 34.4 for
+// 216 through 128 of 512 x 1024, 12.9 : 13.6 for a row through 8 of 1024 x 2048.
+// A row holds K-block after K-block, 64 high halves and the 64 low ones behind.
+constexpr int kHalvesBlock = 2 * kBlock;
+__device__ __forceinline__ void put_halves(uint16_t* row, int col, float h) {
+  const f16 hi = (f16)h;
+  const f16 lo = (f16)(h - (float)hi);
+  uint16_t* p = row + (int64_t)(col / kBlock) * kHalvesBlock + col % kBlock;
+  p[0] = __builtin_bit_cast(uint16_t, hi);
+  // (an infinite high half stands alone: the difference would be NaN or infinite again)
+  p[kBlock] = __builtin_isinf((float)hi) ? 0 : __builtin_bit_cast(uint16_t, lo);
+}
+// The halves that the values of X are given as in a mode.
+template <int MODE>
+constexpr int kHalves = MODE == kDown || MODE == kToken ? 2 : 1;
 
 // Adapters of rows as they come, up to this rank: each thread adds those of its own
 // outputs by fp32 fma, all of B requested at once.  Above, one adapter after the
@@ -106,7 +121,7 @@ struct RowsArgs {
   RowPlan plan;                   // order null: positions are rows themselves
   int experts;                    // one row: ids outside [0, experts) are no expert
   const float* weights;           // kDown, kToken
-  uint16_t* y16;                  // kSwiglu: h; kLora: Y16 or null
+  uint16_t* y16;                  // kSwiglu: h in halves; kLora: Y16 or null
   float* y;                       // kDown: partial rows; kLora: Y or null
   int64_t ldy;
   const int32_t* ids;             // kLora, and one row
@@ -323,7 +338,7 @@ struct RowAdapters {
 // decode, and add their sums in LDS in wave order.  Bound by the latency of the
 // few loads between start and sums: 216 pairs over 128 experts of 512 x 1024 at 3
 // bits, 38 MB of gate and up fetched (all 128 are 57 MB), take 18 us (2.1 TB/s), their
-// down projections at 4 bits 10 us, 40 rows on 6144 x 4096 at 4 bits with adapters 16 us.  More blocks in
+// down projections at 4 bits 12 us, 40 rows on 6144 x 4096 at 4 bits with adapters 16 us.  More blocks in
 // flight (3, 4) changed nothing (16.4, 15.9 us).
 // Lane (c, h) supplies X row c / weight row c and K positions 32h + 8s .. +7.
 // (Two waves per SIMD at least: with the register file to itself the compiler
@@ -333,6 +348,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
   constexpr int WPB = 2 * BITS;
   constexpr int HW = BITS;                   // words of a half block
   constexpr int NM = MODE == kSwiglu ? 2 : 1;
+  constexpr int XH = kHalves<MODE>;
   constexpr int PT = CB * 16 / WAVES;        // outputs per thread
   static_assert(CB * 16 % WAVES == 0, "reduction split");
   __shared__ float red[WAVES][CB * 1024];
@@ -399,7 +415,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
     }
   }
   for (int jb = wave; jb < a.kb; jb += WAVES * U) {
-    f16x8 xa[U][4];
+    f16x8 xa[U][XH][4];
     uint32_t wl[U][NM][CB][HW];
     uint16_t sr[U][NM][CB];
     int zc[U][NM][CB];
@@ -417,9 +433,11 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
           load_half<BITS>(lane_ptr(a.codes[i], woff + ((int64_t)j * kTile + 32 * cb) * WPB, wlane), h,
                           wl[u][i][cb]);
         }
-      const f16x8* xp = reinterpret_cast<const f16x8*>(xrow + (int64_t)j * kBlock);
+      const f16x8* xp = reinterpret_cast<const f16x8*>(xrow + (int64_t)j * (XH * kBlock));
 #pragma unroll
-      for (int s = 0; s < 4; ++s) xa[u][s] = xp[s];
+      for (int x = 0; x < XH; ++x)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) xa[u][x][s] = xp[8 * x + s];
     }
     loads_issued();
 #pragma unroll
@@ -432,9 +450,12 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
           const DeqT<BITS> d = make_deq_b<BITS>(1.f, zc[u][i][cb]);
           f32x16 blk = {};
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
-            blk = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                xa[u][s], int_half<BITS>(wl[u][i][cb], s, d, magic), blk, 0, 0, 0);
+          for (int s = 0; s < 4; ++s) {
+            const f16x8 w = int_half<BITS>(wl[u][i][cb], s, d, magic);
+#pragma unroll
+            for (int x = 0; x < XH; ++x)
+              blk = __builtin_amdgcn_mfma_f32_32x32x16_f16(xa[u][x][s], w, blk, 0, 0, 0);
+          }
           const float sc = h2f(sr[u][i][cb]);
 #pragma unroll
           for (int r = 0; r < 16; ++r) acc[i][cb][r] = __builtin_fmaf(sc, blk[r], acc[i][cb][r]);
@@ -511,8 +532,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
     const int cl = out_col(p), row = out_row(p);
     if (row >= rows || cl >= a.n) continue;
     if constexpr (MODE == kSwiglu) {
-      const float hv = silu(v[0][p]) * v[1][p];
-      a.y16[(int64_t)(p0 + row) * a.ldy + cl] = __builtin_bit_cast(uint16_t, (f16)hv);
+      put_halves(a.y16 + (int64_t)(p0 + row) * a.ldy, cl, silu(v[0][p]) * v[1][p]);
     } else if constexpr (MODE == kDown) {
       const int64_t pair = a.plan.order[p0 + row];
       a.y[pair * a.ldy + cl] = a.weights[pair] * v[0][p];
@@ -532,13 +552,14 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_rows_ksplit(const RowsArgs a)
 // dot products: with one row of X the matrix cores would be idle in 31 of 32
 // rows, and few outputs per work-group spread even a small product over all CUs
 // (the 2048 outputs of a token's down projections: 14.3 us as 64 work-groups of
-// 32 columns; now 6.0 us, and 7.8 us for gate and up of 8 experts of 1024 x 2048 at
+// 32 columns; now 6.5 us, and 7.8 us for gate and up of 8 experts of 1024 x 2048 at
 // 4 bits, 18.4 MB).  Bound by launch latency and one round of loads.
 template <int BITS, int MODE, int NG, int WAVES, int U>
 __global__ __launch_bounds__(WAVES * 64) void k_rows_gemv(const RowsArgs a) {
   constexpr int WPB = 2 * BITS;
   constexpr int RW = 64 / NG;                // outputs per work-group
   constexpr int XQ = 8 / NG;                 // 16-byte chunks of x per slice
+  constexpr int XH = kHalves<MODE>;
   constexpr int NM = MODE == kSwiglu ? 2 : 1;
   constexpr int SW = SliceWords<BITS, NG>::n;
   __shared__ float red[NM][WAVES][RW];
@@ -563,7 +584,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_rows_gemv(const RowsArgs a) {
       uint32_t wd[U][NM][SW];
       uint16_t sr[U][NM];
       int zc[U][NM];
-      uint4 xv[U][XQ];
+      uint4 xv[U][XH][XQ];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int j = min(jb + step * u, a.kb - 1);        // past the range: re-read, not used
@@ -575,26 +596,33 @@ __global__ __launch_bounds__(WAVES * 64) void k_rows_gemv(const RowsArgs a) {
           sr[u][i] = *lane_ptr(a.scale[i], mi, r);
           zc[u][i] = *lane_ptr(a.zero[i], mi, r);
         }
-        const uint4* xp = reinterpret_cast<const uint4*>(lane_ptr(xrow, (int64_t)j * kBlock, 8 * XQ * g));
+        const uint4* xp =
+            reinterpret_cast<const uint4*>(lane_ptr(xrow, (int64_t)j * (XH * kBlock), 8 * XQ * g));
 #pragma unroll
-        for (int q = 0; q < XQ; ++q) xv[u][q] = xp[q];
+        for (int x = 0; x < XH; ++x)
+#pragma unroll
+          for (int q = 0; q < XQ; ++q) xv[u][x][q] = xp[8 * x + q];
       }
       loads_issued();
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (jb + step * u >= a.kb) break;
-        f16x2 xs[4 * XQ];
+        f16x2 xs[XH][4 * XQ];
 #pragma unroll
-        for (int q = 0; q < XQ; ++q) {
-          xs[4 * q] = as_h2(xv[u][q].x);
-          xs[4 * q + 1] = as_h2(xv[u][q].y);
-          xs[4 * q + 2] = as_h2(xv[u][q].z);
-          xs[4 * q + 3] = as_h2(xv[u][q].w);
-        }
+        for (int x = 0; x < XH; ++x)
+#pragma unroll
+          for (int q = 0; q < XQ; ++q) {
+            xs[x][4 * q] = as_h2(xv[u][x][q].x);
+            xs[x][4 * q + 1] = as_h2(xv[u][x][q].y);
+            xs[x][4 * q + 2] = as_h2(xv[u][x][q].z);
+            xs[x][4 * q + 3] = as_h2(xv[u][x][q].w);
+          }
 #pragma unroll
         for (int i = 0; i < NM; ++i) {
           const float s = MODE == kToken ? f * h2f(sr[u][i]) : h2f(sr[u][i]);
-          acc[i] = __builtin_fmaf(s, slice_dot<BITS, NG>(wd[u][i], xs, zc[u][i], g, magic), acc[i]);
+          float dot = slice_dot<BITS, NG>(wd[u][i], xs[0], zc[u][i], g, magic);
+          if constexpr (XH == 2) dot += slice_dot<BITS, NG>(wd[u][i], xs[1], zc[u][i], g, magic);
+          acc[i] = __builtin_fmaf(s, dot, acc[i]);
         }
       }
     }
@@ -625,10 +653,11 @@ __global__ __launch_bounds__(WAVES * 64) void k_rows_gemv(const RowsArgs a) {
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) tot[i] += red[i][w][lane];
   }
-  const int64_t o = (int64_t)y * a.ldy + t * kTile + r0 + lane;   // (n % 64 == 0)
+  const int col = t * kTile + r0 + lane;     // (n % 64 == 0)
   if constexpr (MODE == kSwiglu) {
-    a.y16[o] = __builtin_bit_cast(uint16_t, (f16)(silu(tot[0]) * tot[1]));
+    put_halves(a.y16 + (int64_t)y * a.ldy, col, silu(tot[0]) * tot[1]);
   } else {
+    const int64_t o = (int64_t)y * a.ldy + col;
     if (a.y != nullptr) a.y[o] = tot[0];
     if (a.y16 != nullptr) a.y16[o] = __builtin_bit_cast(uint16_t, (f16)tot[0]);
   }
@@ -650,11 +679,15 @@ __device__ __forceinline__ void here(f16x8& v) { asm volatile("" : "+v"(v)); }
 // X by direct-to-LDS loads into four stages, three blocks ahead (and the next
 // block's first operands are read before the barrier), codes two blocks ahead in
 // registers; one barrier per block.
+// Two halves of X (kDown) lie in a stage one behind the other; the low ones of a product
+// are read beside the MFMAs of its high ones into registers of their own (a second set of
+// those spills 12 registers at 4 bits, 22 at 8).
 // Bound by instruction issue: 205 vector instructions beside 16 MFMAs a block, of
-// them 64 the scaling and 72 decoding (4 bits); one issues in 93 % of the cycles of
-// 16384 pairs through 32 experts of 2 x 1408 x 2048 (212 to 264 us over 12 calls, 890 to
-// 720 TFLOP/s; MFMA busy 50 %), in 82 % of their down projections (127 to 160 us; K has
-// 22 blocks only).  2048
+// them 64 the scaling and 72 decoding (4 bits); one issues in 92 % of the cycles of
+// 16384 pairs through 32 experts of 2 x 1408 x 2048 (212 to 273 us over 12 calls, 890 to
+// 690 TFLOP/s; MFMA busy 48 %).  In their down projections, 32 MFMAs a block (191 to 226
+// us), one issues in 70 % and the matrix cores are busy in 58 %: the chains of eight
+// MFMAs on one block of sums, with 22 K-blocks only.  2048
 // rows on 4096 x 4096 without adapters: 78 us, 64 of them in the loop.  128 rows x
 // 128 columns (130 vector instructions a block, twice the operand reads) took 81
 // us there, as this form did then, and 359 for 331 us over 64 experts of 256 rows; two waves a
@@ -703,9 +736,9 @@ __device__ __forceinline__ void load_half(Buffer b, int2 lane, int at, uint32_t*
 // X stages: LDS objects of their own, so that the compiler can tell which
 // direct-to-LDS loads a read depends on.
 constexpr int kXStages = 4;
-template <int I>
+template <int I, int XH>
 __device__ __forceinline__ f16x8* x_stage() {
-  __shared__ f16x8 xs[64 * 8];
+  __shared__ f16x8 xs[XH * 64 * 8];
   return xs;
 }
 
@@ -721,6 +754,7 @@ template <int BITS, int MODE>
 __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
   constexpr int WPB = 2 * BITS;
   constexpr int HW = BITS;
+  constexpr int XH = kHalves<MODE>;
   const RowTile rt = row_tile<MODE>(a, 64);
   if (rt.rows <= 0) return;
   const int gx = rt.col;
@@ -760,11 +794,13 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
   uint16_t sr[2][2];
   int zc[2][2];
   auto request_x = [&](auto T, int j) __attribute__((always_inline)) {
-    f16x8* xs = x_stage<decltype(T)::value>();
+    f16x8* xs = x_stage<decltype(T)::value, XH>();
     const int jj = min(j, a.kb - 1);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      buffer_to_lds(xbuf, xs + 256 * i + 64 * wave, xoff[i], jj * kBlock * 2);
+    for (int x = 0; x < XH; ++x)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        buffer_to_lds(xbuf, xs + 512 * x + 256 * i + 64 * wave, xoff[i], (XH * jj + x) * kBlock * 2);
     __builtin_amdgcn_sched_barrier(0);
   };
   auto request_w = [&](auto S, int j) __attribute__((always_inline)) {
@@ -781,12 +817,21 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
   };
   f32x16 acc[2][2], blk[2];                // [row block][column block]; sums not yet scaled
   f16x8 av[2][4], bv[2][4];                  // [row / column block][K quarter]
+  f16x8 al[4];                               // (two halves) the low ones of the next product
   float scl[2];                              // the scales of bv's operands
   auto read_a = [&](auto R, auto T) __attribute__((always_inline)) {
     constexpr int rb = decltype(R)::value;
-    const f16x8* xs = x_stage<decltype(T)::value>();
+    const f16x8* xs = x_stage<decltype(T)::value, XH>();
 #pragma unroll
     for (int q = 0; q < 4; ++q) av[rb][q] = xs[8 * (32 * rb + c) + xswz(c, 4 * h + q)];
+  };
+  auto read_low = [&](auto R, auto T) __attribute__((always_inline)) {
+    constexpr int rb = decltype(R)::value;
+    if constexpr (XH == 2) {
+      const f16x8* xs = x_stage<decltype(T)::value, XH>() + 512;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) al[q] = xs[8 * (32 * rb + c) + xswz(c, 4 * h + q)];
+    }
   };
   const std::integral_constant<int, 0> I0;
   const std::integral_constant<int, 1> I1;
@@ -809,7 +854,7 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
     asm volatile("" : "+v"(s));
     return s;
   };
-  // four MFMAs of row block R and column block F into blk[R]
+  // the MFMAs (four for each half) of row block R and column block F into blk[R]
   auto product = [&](auto R, auto F) __attribute__((always_inline)) {
     constexpr int rb = decltype(R)::value, f = decltype(F)::value;
     const f32x16 none = {};
@@ -817,6 +862,11 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
     for (int q = 0; q < 4; ++q)
       blk[rb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av[rb][q], bv[f][q], q == 0 ? none : blk[rb],
                                                        0, 0, 0);
+    if constexpr (XH == 2) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        blk[rb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al[q], bv[f][q], blk[rb], 0, 0, 0);
+    }
   };
   // those sums, times s, to the accumulators
   auto scaled = [&](auto R, auto F, float s) __attribute__((always_inline)) {
@@ -839,9 +889,10 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
   scl[0] = scale_of(I0, I0);
   stage_barrier<0>();
   read_a(I0, I0);
+  read_low(I0, I0);
   // loads of a wave and a block behind the one that must be there: X's of the
   // next block and the codes', scales' and zeros' issued after it
-  constexpr int kNewer = 2 + 2 * ((BITS >= 5 ? 2 : 1) + 2);
+  constexpr int kNewer = 2 * XH + 2 * ((BITS >= 5 ? 2 : 1) + 2);
   // Block j, its codes in slot j % 2, its rows in stage j % 4 = T; block j + 3's
   // rows go where block j - 1's were.
   auto step = [&](auto T, int j) __attribute__((always_inline)) {
@@ -857,22 +908,26 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
     scaled(I1, I1, scl[1]);                  // of block j - 1
     decode(U, I1, 0, 2);
     __builtin_amdgcn_sched_barrier(0);
+    read_low(I1, T);
     product(I1, I0);
     decode(U, I1, 2, 4);
     scl[1] = scale_of(U, I1);
     scaled(I0, I0, scl[0]);
     __builtin_amdgcn_sched_barrier(0);
+    read_low(I0, T);
     request_w(U, j + 2);
     product(I0, I1);
     decode(N, I0, 0, 2);
     scaled(I1, I0, scl[0]);
     __builtin_amdgcn_sched_barrier(0);
+    read_low(I1, T);
     read_a(I0, T1);                          // (of block j + 1)
     product(I1, I1);
     decode(N, I0, 2, 4);
     scl[0] = scale_of(N, I0);
     scaled(I0, I1, scl[1]);
     __builtin_amdgcn_sched_barrier(0);
+    read_low(I0, T1);
     stage_barrier<kNewer>();                 // block j + 2's rows are there
   };
   int j0 = 0;
@@ -908,8 +963,8 @@ __global__ __launch_bounds__(256, 2) void k_rows_tiled(const RowsArgs a) {
       for (int r = 0; r < 16; ++r) {
         const int at = 32 * rb + 8 * (r >> 2) + 4 * h + (r & 3);
         if (at >= rt.rows) continue;
-        const float hv = silu(acc[rb][0][r]) * acc[rb][1][r];
-        a.y16[(int64_t)(rt.p0 + at) * a.ldy + col[0]] = __builtin_bit_cast(uint16_t, (f16)hv);
+        put_halves(a.y16 + (int64_t)(rt.p0 + at) * a.ldy, col[0],
+                   silu(acc[rb][0][r]) * acc[rb][1][r]);
       }
   } else {
     // lane c's row c of each row block: its output row and weight, read together

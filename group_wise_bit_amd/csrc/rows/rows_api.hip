@@ -93,16 +93,17 @@ bool stack_overlaps(const qlin_weight* w, int64_t experts, Range r) {
 // two of them share an expert, each pair reads its expert's weights by itself: no
 // plan, and a token's slots are added by the work-group that multiplies them.
 // Alone : grouped, 64 experts of 2048 x 1024 at 4 bits (3.4 MB each) took
-// 13 : 24 us for 8 pairs, 35 : 35 us for 32, 68 : 50 us for 64; 8 of 4096 x 1792
-// at 8 bits (22 MB) 24 : 27 us for 4 pairs, 50 : 43 us for 8, 82 : 48 us for 16.
+// 14 : 20 us for 8 pairs, 38 : 35 us for 32, 70 : 51 us for 64; 8 of 4096 x 1792
+// at 8 bits (22 MB) 25 : 27 us for 4 pairs, 43 : 42 us for 8, 75 : 48 us for 16.
 constexpr int kDirectPairs = 32;
 constexpr int64_t kDirectBytes = 112 << 20;
 
 // From this many rows per expert on 64-row tiles are used, if tiled_form()
-// agrees: 32-row : 64-row tiles, 64 experts of 2048 x 1024 at 4 bits 81 : 81 us at
-// 16 rows each, 105 : 104 us at 32, 131 : 113 us at 48; 16 of 4096 x 1792 at 8
-// bits 100 : 106 us at 16, 128 : 112 us at 32.
-constexpr int kTiledRows = 32;
+// agrees: 32-row : 64-row tiles, 64 experts of 2048 x 1024 at 4 bits 75 : 83 us at
+// 8 rows each, 92 : 85 us at 16, 117 : 114 us at 32, 151 : 118 us at 48; 16 of 4096 x
+// 1792 at 8 bits 93 : 95 us at 8, 104 : 96 us at 16, 142 : 111 us at 32; 128 of 1024 x
+// 512 at 3 bits 50 : 53 us at 8, 61 : 62 us at 16.
+constexpr int kTiledRows = 16;
 
 struct MoePlan {
   int64_t pairs;
@@ -110,7 +111,7 @@ struct MoePlan {
   RowsCfg up, down;    // forms of the two products
   RowPlan rows;
   int32_t* counts;
-  uint16_t* h;
+  uint16_t* h;         // [pairs][inner] in two halves
   float* d;
   int64_t bytes;
 };
@@ -140,7 +141,7 @@ MoePlan moe_plan(const qlin_weight* gate, const qlin_weight* down, int experts, 
     ksplit_form(p.down, tiles_of(model) * used);
   }
   Arena ar{static_cast<char*>(ws)};
-  p.h = ar.take<uint16_t>(p.pairs * inner);
+  p.h = ar.take<uint16_t>(2 * p.pairs * inner);
   if (!p.direct) {
     p.rows = take_plan(ar, p.pairs, experts, 32);    // (enough for 64-row tiles)
     p.counts = take_counts(ar, p.pairs, experts);
@@ -320,12 +321,12 @@ qlin_status qlin_moe_mlp(const qlin_weight* gate, const qlin_weight* up, const q
   a.experts = experts;
   a.ids = ids;
   a.y16 = p.h;
-  a.ldy = inner;
+  a.ldy = 2 * (int64_t)inner;
   run_rows(a, gate->bits, kSwiglu, p.up, stream);
   RowsArgs b{};
   set_weight(b, 0, down);
   b.X = p.h;
-  b.ldx = inner;
+  b.ldx = 2 * (int64_t)inner;
   b.m = m;
   b.top_k = top_k;
   b.plan = p.rows;

@@ -23,7 +23,7 @@ struct RowsCfg {
 // 4096 (192) 20.5 : 21.7, 333 rows on 896 x 4864 (154) 17 : 24, beyond a work-group
 // per CU.  Of 8 against 4 waves 100 rows on 4096 x 4096 (256) took 19.8 :
 // 21.4 us, on 6144 x 4096 (384) 36.1 : 34.9, on 8192 x 512 (512) 15.8 : 12.7; 27 rows
-// through 8 of 128 experts of 512 x 1024 (1024) 47 : 38, and 39 with 2 waves.
+// through 8 of 128 experts of 512 x 1024 (1024) 51 : 37.
 inline void ksplit_form(RowsCfg& c, int64_t groups) {
   c.half = groups <= 128;
   c.waves = groups < 320 ? 8 : 4;
@@ -31,11 +31,11 @@ inline void ksplit_form(RowsCfg& c, int64_t groups) {
 
 // (1 row) The form for `items` K-blocks and `groups` work-groups of 16 columns: 8
 // columns where 16 would not reach every CU, and then 16 waves for a long K.  Of 16
-// against 8 columns a row through 4 of 64 experts of 256 x 512 took 7.4 : 6.7 us, 3 rows
-// through 8 of 64 of 1024 x 2048 27.9 : 28.4; a row through those (first product 512
-// work-groups of 16 columns, second 128, of 128 blocks) 13.3 by this rule, 14.4 with
-// 16 columns and 8 waves in both, 18 with 16 waves in both; of 16 against 8 waves a
-// row through 2 of 8 experts of 512 x 1024 8.0 : 6.8.
+// against 8 columns a row through 4 of 64 experts of 256 x 512 took 7.9 : 6.9 us, 3 rows
+// through 8 of 64 of 1024 x 2048 31.0 : 33.3; a row through those (first product 512
+// work-groups of 16 columns, second 128, of 128 blocks) 14.2 by this rule, 16.7 with
+// 16 columns and 8 waves in both, 18.7 with 16 waves in both; of 16 against 8 waves a
+// row through 2 of 8 experts of 512 x 1024 8.1 : 6.9.
 inline void gemv_form(RowsCfg& c, int items, int64_t groups) {
   c.half = groups < 256;
   c.waves = c.half && items > 32 ? 16 : 8;
@@ -62,8 +62,9 @@ inline bool rows_fits(int n, int mode, RowsCfg c) {
 // however few there are, so it needs a work-group for every other CU: of 32-row
 // against 64-row tiles, adapters on 4096 x 4096 (4 bits) took 58 : 73 us for 512
 // rows (128 work-groups), 82 : 75 us for 768; on 2048 x 2048 40 : 62 us for 512
-// (64), 69 : 63 us for 1024; 8 experts of 1024 x 512 32 : 36 us at 128 rows each
-// (80), 42 : 40 us at 256.  It reads X by 32-bit offsets.
+// (64), 69 : 63 us for 1024; 8 experts of 1024 x 512 33 : 35 us at 64 rows each (48),
+// 45 : 37 us at 128 (80), of 2048 x 1024 44 : 50 us at 64 (96), 67 : 53 us at 128 (160), 4
+// of 2048 x 768 43 : 47 us at 128 (60).  It reads X by 32-bit offsets.
 inline bool tiled_form(int n, int mode, int64_t tiles, int64_t m, int64_t ld, int64_t k) {
   RowsCfg c{};
   c.height = 64;

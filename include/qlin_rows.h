@@ -90,9 +90,8 @@ qlin_status qlin_route(const qlin_router* r, const float* logits, int32_t m, int
  * Outputs, either may be NULL (not both), leading dimension ld_y >= down.n for
  * both: Y fp32, Y16 the same rounded to fp16 (nearest even).
  * Every product x * (q - z) is exact, scales are applied and sums held in fp32;
- * silu(g) * u is rounded once to fp16 (infinite from 65520 on, in steps of 2^-24
- * below 2^-14), the down projection's operand: that is what outputs, fp32 ones
- * too, are off by most (3e-4 of a row's usual size).  Deterministic: each row's result depends on its own
+ * silu(g) * u enters the down projection with 22 bits (in steps of 2^-24 below
+ * 2^-3; it is infinite from 65520 on, and its row then not finite).  Deterministic: each row's result depends on its own
  * inputs and on the call's sizes and strides only.
  * workspace_bytes >= qlin_moe_mlp_workspace_bytes(gate, down, experts, m,
  * top_k), or QLIN_ERR_WORKSPACE (0 is returned there for invalid arguments).

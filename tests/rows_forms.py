@@ -95,7 +95,7 @@ def _plan_bytes(count, buckets, height):
 def moe_workspace(m, top_k, experts, inner, model, bits, dbits):
     """What qlin_moe_mlp_workspace_bytes gives if the form is the one above."""
     pairs = m * top_k
-    b = 65536 + _align(2 * pairs * inner)
+    b = 65536 + _align(4 * pairs * inner)
     if moe(m, top_k, experts, inner, model, bits, dbits)[0] != 1:
         b += _plan_bytes(pairs, experts, 32) + _align(4 * pairs * model)
     return b

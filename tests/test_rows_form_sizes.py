@@ -5,6 +5,7 @@ import ctypes
 import pytest
 
 import rows_forms as rf
+import test_gpu_rows_halves as halves
 import test_gpu_rows_instances as inst
 from group_wise_bit_amd import qlin
 
@@ -42,6 +43,14 @@ def test_sizes_of_the_64_row_form():
     # rows over more than 4 GB take the 32-row form
     assert rf.moe(660, 1, 16, 1088, 128, 4, 4, ld=1 << 22)[0] == 32
     assert rf.lora(660, 4096, 128, 16)[0] == 64 and rf.lora(660, 4096, 128, 16, ld=1 << 22)[0] == 32
+
+
+def test_sizes_of_the_tests_of_halves():
+    forms = [rf.moe(*size, 4, 4) for size in halves.SIZES]
+    assert [f[0] for f in forms] == [1, 1, 1, 32, 32, 32, 64]
+    assert [f[2] for f in forms[:6]] == [(16, 8), (8, 8), (8, 16), (32, 8), (64, 8), (64, 4)]
+    for m, experts, inner, height in ((2, 3, 128, 1), (60, 3, 128, 32), (660, 16, 1088, 64)):
+        assert rf.moe(m, 1, experts, inner, 256, 4, 4)[0] == height
 
 
 def packed(n, k, bits=4):
