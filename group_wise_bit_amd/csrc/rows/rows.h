@@ -83,8 +83,8 @@ enum RowsMode { kSwiglu = 0, kDown = 1, kLora = 2, kToken = 3 };
 // h = silu(g) * u goes to the down product as a high and a low fp16 half: the low one is
 // what rounding to the high one left, so that the two hold 22 bits of it (in steps of
 // 2^-24 below 2^-3; infinite from 65520 on, as fp16 is).  Each half's products with q - z
-// are exact.  One half left outputs off by 2e-4 (rms, relative), fp32 ones too; two cost
-// twice the MFMAs of the down product: 374 : 440 us for 16384 pairs through 32 experts of
+// are exact.  One half left fp32 outputs off by 2.1e-4 (rms, relative), two by 2e-7; two
+// cost twice the MFMAs of the down product: 374 : 440 us for 16384 pairs through 32 experts of
 // 2 x 1408 x 2048, 136 : 149 for 1018 through 16 of 1792 x 4096 at 8 bits, 32.7 : 34.4 for
 // 216 through 128 of 512 x 1024, 12.9 : 13.6 for a row through 8 of 1024 x 2048.
 // A row holds K-block after K-block, 64 high halves and the 64 low ones behind.
