@@ -8,7 +8,7 @@
  * nothing about the ids is read on the host.  All of a call's pointers must
  * belong to the current device.  m = 0 is a no-op in every call (pointers are
  * then not looked at).  A product whose grid would have 2^32 threads is refused
- * with QLIN_ERR_SHAPE (rows, one per token and slot, times columns: none below 2^35).
+ * with QLIN_ERR_SHAPE (rows, one per token and slot, times columns: none below 2^32).
  *
  * Workspaces.  A call's workspace is scratch: nothing in it is kept between
  * calls, and it needs no initialization, with one exception that lets it be
