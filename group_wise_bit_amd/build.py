@@ -29,14 +29,19 @@ INST_SOURCE = os.path.join(CSRC, "inst.hip")
 # row-wise products (include/qlin_rows.h): entry points, and one object per width
 ROWS_API_SOURCE = os.path.join(CSRC, "rows", "rows_api.hip")
 ROWS_INST_SOURCE = os.path.join(CSRC, "rows", "rows_inst.hip")
+# cache of keys and values (include/qlin_kv.h): entry points, and two objects per pair of widths
+KV_API_SOURCE = os.path.join(CSRC, "kv", "kv_api.hip")
+KV_INST_SOURCE = os.path.join(CSRC, "kv", "kv_inst.hip")
 HEADERS = [os.path.join(CSRC, f) for f in ("device_common.h", "codes.h", "kernels.h", "plan.h",
                                            "launch_impl.h", "checks.h", "rows/rows.h", "rows/group.h",
-                                           "rows/route.h", "rows/rows_plan.h")] + [
-    os.path.join(ROOT, "include", f) for f in ("qlin.h", "qlin_rows.h")]
+                                           "rows/route.h", "rows/rows_plan.h", "kv/kv_layout.h",
+                                           "kv/kv_store.h", "kv/attend.h", "kv/kv_plan.h")] + [
+    os.path.join(ROOT, "include", f) for f in ("qlin.h", "qlin_rows.h", "qlin_kv.h")]
 
 GEMV_BITS = (2, 3, 4, 5, 6, 7, 8, 16)   # part 0: GEMV and row gather (16: fp16 control)
 GEMM_BITS = (2, 3, 4, 5, 6, 7, 8)       # part 1: GEMM
 QUANT_BITS = (2, 3, 4, 5, 6, 7, 8)      # part 2: quantizer
+KV_BITS = (4, 8, 16)                    # keys and values, each
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
@@ -73,6 +78,13 @@ def _units():
     units.append(("rows_api", ROWS_API_SOURCE, []))
     for b in GEMM_BITS:
         units.append((f"rows_b{b}", ROWS_INST_SOURCE, [f"-DQLIN_INST_BITS={b}"]))
+    units.append(("kv_api", KV_API_SOURCE, []))
+    for kb in KV_BITS:
+        for vb in KV_BITS:
+            defs = [f"-DQLIN_INST_KB={kb}", f"-DQLIN_INST_VB={vb}"]
+            units.append((f"kv_store_k{kb}_v{vb}", KV_INST_SOURCE,
+                          [*defs, "-DQLIN_INST_PART=0", *QUANT_FLAGS]))
+            units.append((f"kv_attend_k{kb}_v{vb}", KV_INST_SOURCE, [*defs, "-DQLIN_INST_PART=1"]))
     return units
 
 

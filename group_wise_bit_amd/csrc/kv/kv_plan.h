@@ -1,0 +1,20 @@
+// Launchers of the cache's kernels, one object per pair of widths (kv_inst.hip).
+#pragma once
+
+#include "attend.h"
+#include "kv_store.h"
+
+namespace qlin {
+
+// Work-groups of the attention: as many as the chip holds at once, or one for
+// every four tiles if there cannot be that many.
+constexpr int kAttendGroups = 512;
+
+template <int KB, int VB>
+void launch_kv_store(const KvStoreArgs& a, int d, dim3 grid, hipStream_t st);
+template <int KB, int VB>
+void launch_kv_read(const KvReadArgs& a, int d, bool wide, dim3 grid, hipStream_t st);
+template <int KB, int VB>
+void launch_attend(const AttendArgs& a, int d, hipStream_t st);
+
+}  // namespace qlin

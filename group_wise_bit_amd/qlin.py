@@ -44,6 +44,11 @@ ROWS_EXPORTS = (
     "qlin_route", "qlin_moe_mlp_workspace_bytes", "qlin_moe_mlp",
     "qlin_gemm_lora_workspace_bytes", "qlin_gemm_lora",
 )
+# include/qlin_kv.h (the cache of keys and values)
+KV_EXPORTS = (
+    "qlin_kv_page_bytes", "qlin_kv_write", "qlin_kv_read", "qlin_kv_attention_workspace_bytes",
+    "qlin_kv_attention",
+)
 
 
 class QlinError(RuntimeError):
@@ -85,6 +90,21 @@ class QlinAdaptersC(ctypes.Structure):
     _fields_ = [
         ("slots", ctypes.c_int32), ("rank", ctypes.c_int32), ("a", ctypes.c_void_p),
         ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+    ]
+
+
+class QlinKvCacheC(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("page", ctypes.c_int32), ("k_bits", ctypes.c_int32), ("v_bits", ctypes.c_int32),
+        ("data", ctypes.c_void_p),
+    ]
+
+
+class QlinKvSeqsC(ctypes.Structure):
+    _fields_ = [
+        ("seqs", ctypes.c_int32), ("width", ctypes.c_int32), ("table", ctypes.c_void_p),
+        ("ld", ctypes.c_int64), ("lengths", ctypes.c_void_p),
     ]
 
 
@@ -157,6 +177,18 @@ def _lib() -> ctypes.CDLL:
         lib.qlin_gemm_lora_workspace_bytes.restype = i64
         lib.qlin_gemm_lora.argtypes = [wp, ap, vp, i32, i64, vp, vp, vp, i64, vp, i64, vp]
         lib.qlin_gemm_lora.restype = ctypes.c_int
+        kp, sp = ctypes.POINTER(QlinKvCacheC), ctypes.POINTER(QlinKvSeqsC)
+        lib.qlin_kv_page_bytes.argtypes = [i32, i32, i32, i32]
+        lib.qlin_kv_page_bytes.restype = i64
+        lib.qlin_kv_write.argtypes = [kp, vp, i64, vp, i64, i32, sp, vp, vp]
+        lib.qlin_kv_write.restype = ctypes.c_int
+        lib.qlin_kv_read.argtypes = [kp, sp, vp, i32, vp, i64, vp, i64, i32, vp]
+        lib.qlin_kv_read.restype = ctypes.c_int
+        lib.qlin_kv_attention_workspace_bytes.argtypes = [kp, sp, i32]
+        lib.qlin_kv_attention_workspace_bytes.restype = i64
+        lib.qlin_kv_attention.argtypes = [kp, sp, vp, i64, i32, ctypes.c_float, i32, vp, vp, i64, vp,
+                                          vp, i64, vp]
+        lib.qlin_kv_attention.restype = ctypes.c_int
         _LIB = lib
     return _LIB
 
@@ -839,3 +871,175 @@ def gemm_lora(w: QWeight, X: torch.Tensor, adapters: Adapters, ids: torch.Tensor
             c, a, X.data_ptr(), m, _row_pitch(X), ids.data_ptr(), _ptr(Y), _ptr(Y16), ld, wp, wb,
             stream), "qlin_gemm_lora")
     return Y, Y16
+
+
+# ------------------------------------------------ the cache of keys and values
+# (include/qlin_kv.h).  Devices and streams as for the row-wise calls.
+
+def kv_page_bytes(head_dim: int, page_size: int, k_bits: int, v_bits: int) -> int:
+    """Bytes of one page of one head."""
+    return int(_lib().qlin_kv_page_bytes(head_dim, page_size, k_bits, v_bits))
+
+
+@dataclass(eq=False)
+class KVCache(_CStruct):
+    """A layer's cache: pages of `page_size` tokens of keys and values in groups of 64 with
+    k_bits and v_bits (4, 8, or 16: not quantized), each on its own.  data uint8 [pages, kv_heads,
+    kv_page_bytes(...)], contiguous; copying a page copies its tokens."""
+    data: torch.Tensor
+    kv_heads: int
+    head_dim: int
+    page_size: int = 64
+    k_bits: int = 8
+    v_bits: int = 8
+
+    def c_struct(self) -> QlinKvCacheC:
+        return self._cached((self.data,), (self.kv_heads, self.head_dim, self.page_size,
+                                           self.k_bits, self.v_bits), self._build)
+
+    def _build(self) -> QlinKvCacheC:
+        size = kv_page_bytes(self.head_dim, self.page_size, self.k_bits, self.v_bits)
+        if not size:
+            raise ValueError(f"no cache layout for head_dim = {self.head_dim}, page_size = "
+                             f"{self.page_size}, k_bits = {self.k_bits}, v_bits = {self.v_bits}")
+        if self.data.dim() != 3:
+            raise TypeError("data must be a contiguous torch.uint8 [pages, kv_heads, bytes] tensor")
+        _need_flat(self.data, torch.uint8, (self.data.shape[0], self.kv_heads, size), "data")
+        return QlinKvCacheC(self.data.shape[0], self.kv_heads, self.head_dim, self.page_size,
+                            self.k_bits, self.v_bits, self.data.data_ptr())
+
+
+def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, k_bits: int = 8,
+             v_bits: int = 8, device="cuda") -> KVCache:
+    """An empty cache (no page needs initialization: what is not written is not read)."""
+    size = kv_page_bytes(head_dim, page_size, k_bits, v_bits)
+    if not size:
+        raise ValueError(f"no cache layout for head_dim = {head_dim}, page_size = {page_size}, "
+                         f"k_bits = {k_bits}, v_bits = {v_bits}")
+    return KVCache(torch.empty(pages, kv_heads, size, dtype=torch.uint8, device=device), kv_heads,
+                   head_dim, page_size, k_bits, v_bits)
+
+
+def _kv_seqs(cache: KVCache, table: torch.Tensor, lengths: torch.Tensor,
+             starts: Optional[torch.Tensor]) -> QlinKvSeqsC:
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2 or \
+            (table.shape[0] > 0 and table.shape[1] > 1 and table.stride(1) != 1):
+        raise TypeError("table must be an int32 [seqs, pages per sequence] tensor with contiguous "
+                        "rows")
+    seqs = table.shape[0]
+    _need_flat(lengths, torch.int32, (seqs,), "lengths")
+    if starts is not None:
+        _need_flat(starts, torch.int32, (seqs + 1,), "starts")
+    _same_device(cache.data.device, (("table", table), ("lengths", lengths), ("starts", starts)))
+    return QlinKvSeqsC(seqs, table.shape[1], table.data_ptr(), _row_pitch(table),
+                       lengths.data_ptr())
+
+
+def _kv_rows(t: torch.Tensor, dtype: torch.dtype, heads: int, head_dim: int, name: str) -> int:
+    """The pitch of [m, heads, head_dim] rows, whose heads follow one another."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 3 or \
+            t.shape[1:] != (heads, head_dim):
+        raise TypeError(f"{name} must be a {dtype} [rows, {heads}, {head_dim}] tensor")
+    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim)):
+        raise ValueError(f"{name}'s rows must be contiguous, got strides {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else heads * head_dim
+
+
+def kv_write(cache: KVCache, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor,
+             lengths: torch.Tensor, starts: Optional[torch.Tensor] = None) -> None:
+    """qlin_kv_write: rows starts[b] .. starts[b + 1] - 1 of K and V (fp16 [m, kv_heads, head_dim])
+    become the last tokens of sequence b; without starts row b is the last token of sequence b.
+    lengths counts them already."""
+    c = cache.c_struct()
+    s = _kv_seqs(cache, table, lengths, starts)
+    ldk = _kv_rows(K, torch.float16, cache.kv_heads, cache.head_dim, "K")
+    ldv = _kv_rows(V, torch.float16, cache.kv_heads, cache.head_dim, "V")
+    m, dev = K.shape[0], cache.data.device
+    if V.shape[0] != m:
+        raise ValueError(f"K has {m} rows, V {V.shape[0]}")
+    _same_device(dev, (("K", K), ("V", V)))
+    _check(_launch(dev, lambda stream: _lib().qlin_kv_write(
+        ctypes.byref(c), K.data_ptr(), ldk, V.data_ptr(), ldv, m, ctypes.byref(s), _ptr(starts),
+        stream)), "qlin_kv_write")
+
+
+def kv_read(cache: KVCache, table: torch.Tensor, lengths: torch.Tensor,
+            starts: Optional[torch.Tensor] = None, rows: Optional[int] = None,
+            K: Optional[torch.Tensor] = None, V: Optional[torch.Tensor] = None,
+            dtype: torch.dtype = torch.float16) -> Tuple[torch.Tensor, torch.Tensor]:
+    """qlin_kv_read: the last starts[b + 1] - starts[b] tokens of every sequence b as rows
+    starts[b] on of K and V ([rows, kv_heads, head_dim], fp16 or fp32); without starts row b is the
+    last token of sequence b.  rows: how many K and V have where they are not given (default: one
+    per sequence); rows from starts[-1] on are not written."""
+    c = cache.c_struct()
+    s = _kv_seqs(cache, table, lengths, starts)
+    h, d, dev = cache.kv_heads, cache.head_dim, cache.data.device
+    if dtype not in (torch.float16, torch.float32):
+        raise TypeError("dtype must be torch.float16 or torch.float32")
+    if rows is None:
+        given = next((t for t in (K, V) if t is not None), None)
+        if given is None and starts is not None:
+            raise ValueError("rows must be given along with starts, unless K or V is")
+        rows = s.seqs if given is None else given.shape[0]
+    if K is None:
+        K = torch.empty(rows, h, d, dtype=dtype, device=dev)
+    if V is None:
+        V = torch.empty(rows, h, d, dtype=dtype, device=dev)
+    ldk, ldv = _kv_rows(K, dtype, h, d, "K"), _kv_rows(V, dtype, h, d, "V")
+    if K.shape[0] < rows or V.shape[0] < rows:
+        raise ValueError(f"K and V must have {rows} rows")
+    _same_device(dev, (("K", K), ("V", V)))
+    _check(_launch(dev, lambda stream: _lib().qlin_kv_read(
+        ctypes.byref(c), ctypes.byref(s), _ptr(starts), rows, K.data_ptr(), ldk, V.data_ptr(), ldv,
+        int(dtype == torch.float32), stream)), "qlin_kv_read")
+    return K, V
+
+
+def kv_attention(cache: KVCache, Q: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor,
+                 scale: Optional[float] = None, window: int = 0,
+                 O: Optional[torch.Tensor] = None, O16: Optional[torch.Tensor] = None,
+                 lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = "auto",
+                 want_o: bool = True, want_o16: bool = True, want_lse: bool = False
+                 ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """qlin_kv_attention: (O fp32, O16 fp16, lse fp32) of one query row per sequence (Q fp16 [seqs,
+    heads, head_dim]) over its cached tokens, the last `window` of them if that is not 0; scale is
+    1 / sqrt(head_dim) by default."""
+    c = cache.c_struct()
+    s = _kv_seqs(cache, table, lengths, None)
+    d, dev, seqs = cache.head_dim, cache.data.device, s.seqs
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3:
+        raise TypeError(f"Q must be a {torch.float16} [seqs, heads, {d}] tensor")
+    heads = Q.shape[1]
+    ldq = _kv_rows(Q, torch.float16, heads, d, "Q")
+    if Q.shape[0] != seqs:
+        raise ValueError(f"Q has {Q.shape[0]} rows for {seqs} sequences")
+    if O is None and want_o:
+        O = torch.empty(seqs, heads, d, dtype=torch.float32, device=dev)
+    if O16 is None and want_o16:
+        O16 = torch.empty(seqs, heads, d, dtype=torch.float16, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty(seqs, heads, dtype=torch.float32, device=dev)
+    ldo = heads * d
+    pitches = {_kv_rows(t, dtype, heads, d, name)
+               for t, dtype, name in ((O, torch.float32, "O"), (O16, torch.float16, "O16"))
+               if t is not None}
+    for t, name in ((O, "O"), (O16, "O16")):
+        if t is not None and t.shape[0] != seqs:
+            raise ValueError(f"{name} has {t.shape[0]} rows for {seqs} sequences")
+    if len(pitches) > 1:
+        raise ValueError("O and O16 must share one row stride")
+    if pitches:
+        ldo = pitches.pop()
+    if lse is not None:
+        _need_flat(lse, torch.float32, (seqs, heads), "lse")
+    _same_device(dev, (("Q", Q), ("O", O), ("O16", O16), ("lse", lse)))
+    if scale is None:
+        scale = d ** -0.5
+    lib = _lib()
+    cp, sp = ctypes.byref(c), ctypes.byref(s)
+    _with_workspace(
+        ws, dev, lambda: lib.qlin_kv_attention_workspace_bytes(cp, sp, heads),
+        lambda wp, wb, stream: lib.qlin_kv_attention(
+            cp, sp, Q.data_ptr(), ldq, heads, scale, window, _ptr(O), _ptr(O16), ldo, _ptr(lse), wp,
+            wb, stream), "qlin_kv_attention")
+    return O, O16, lse
