@@ -32,11 +32,14 @@ ROWS_INST_SOURCE = os.path.join(CSRC, "rows", "rows_inst.hip")
 # cache of keys and values (include/qlin_kv.h): entry points, and two objects per pair of widths
 KV_API_SOURCE = os.path.join(CSRC, "kv", "kv_api.hip")
 KV_INST_SOURCE = os.path.join(CSRC, "kv", "kv_inst.hip")
+# drawing tokens (include/qlin_sample.h)
+SAMPLE_SOURCE = os.path.join(CSRC, "sample", "sample_api.hip")
 HEADERS = [os.path.join(CSRC, f) for f in ("device_common.h", "codes.h", "kernels.h", "plan.h",
                                            "launch_impl.h", "checks.h", "rows/rows.h", "rows/group.h",
                                            "rows/route.h", "rows/rows_plan.h", "kv/kv_layout.h",
-                                           "kv/kv_store.h", "kv/attend.h", "kv/kv_plan.h")] + [
-    os.path.join(ROOT, "include", f) for f in ("qlin.h", "qlin_rows.h", "qlin_kv.h")]
+                                           "kv/kv_store.h", "kv/attend.h", "kv/kv_plan.h",
+                                           "sample/sample.h")] + [
+    os.path.join(ROOT, "include", f) for f in ("qlin.h", "qlin_rows.h", "qlin_kv.h", "qlin_sample.h")]
 
 GEMV_BITS = (2, 3, 4, 5, 6, 7, 8, 16)   # part 0: GEMV and row gather (16: fp16 control)
 GEMM_BITS = (2, 3, 4, 5, 6, 7, 8)       # part 1: GEMM
@@ -78,6 +81,7 @@ def _units():
     units.append(("rows_api", ROWS_API_SOURCE, []))
     for b in GEMM_BITS:
         units.append((f"rows_b{b}", ROWS_INST_SOURCE, [f"-DQLIN_INST_BITS={b}"]))
+    units.append(("sample", SAMPLE_SOURCE, []))
     units.append(("kv_api", KV_API_SOURCE, []))
     for kb in KV_BITS:
         for vb in KV_BITS:

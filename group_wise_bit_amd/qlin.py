@@ -49,6 +49,8 @@ KV_EXPORTS = (
     "qlin_kv_page_bytes", "qlin_kv_write", "qlin_kv_read", "qlin_kv_attention_workspace_bytes",
     "qlin_kv_attention",
 )
+# include/qlin_sample.h (drawing tokens)
+SAMPLE_EXPORTS = ("qlin_sample_workspace_bytes", "qlin_sample")
 
 
 class QlinError(RuntimeError):
@@ -105,6 +107,13 @@ class QlinKvSeqsC(ctypes.Structure):
     _fields_ = [
         ("seqs", ctypes.c_int32), ("width", ctypes.c_int32), ("table", ctypes.c_void_p),
         ("ld", ctypes.c_int64), ("lengths", ctypes.c_void_p),
+    ]
+
+
+class QlinSamplingC(ctypes.Structure):
+    _fields_ = [
+        ("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+        ("min_p", ctypes.c_void_p),
     ]
 
 
@@ -189,6 +198,11 @@ def _lib() -> ctypes.CDLL:
         lib.qlin_kv_attention.argtypes = [kp, sp, vp, i64, i32, ctypes.c_float, i32, vp, vp, i64, vp,
                                           vp, i64, vp]
         lib.qlin_kv_attention.restype = ctypes.c_int
+        lib.qlin_sample_workspace_bytes.argtypes = [i32, i32]
+        lib.qlin_sample_workspace_bytes.restype = i64
+        lib.qlin_sample.argtypes = [ctypes.POINTER(QlinSamplingC), vp, i32, i32, i64, vp, vp, vp, vp,
+                                    i64, vp]
+        lib.qlin_sample.restype = ctypes.c_int
         _LIB = lib
     return _LIB
 
@@ -1043,3 +1057,64 @@ def kv_attention(cache: KVCache, Q: torch.Tensor, table: torch.Tensor, lengths: 
             cp, sp, Q.data_ptr(), ldq, heads, scale, window, _ptr(O), _ptr(O16), ldo, _ptr(lse), wp,
             wb, stream), "qlin_kv_attention")
     return O, O16, lse
+
+
+# ------------------------------------------------------------- drawing a token
+# (include/qlin_sample.h).  Devices and streams as for the row-wise calls.
+
+@dataclass(eq=False)
+class Sampling(_CStruct):
+    """How sample() draws, one setting per row (None: off for all): temperature fp32 [m] (not above
+    0: the largest logit), top_k int32 [m] (below 1: off), top_p fp32 [m] (not below 1: off) and
+    min_p fp32 [m] (not above 0: off)."""
+    temperature: Optional[torch.Tensor] = None
+    top_k: Optional[torch.Tensor] = None
+    top_p: Optional[torch.Tensor] = None
+    min_p: Optional[torch.Tensor] = None
+
+    def c_struct(self, m: int) -> QlinSamplingC:
+        return self._cached((self.temperature, self.top_k, self.top_p, self.min_p), (m,),
+                            lambda: self._build(m))
+
+    def _build(self, m: int) -> QlinSamplingC:
+        for t, dtype, name in ((self.temperature, torch.float32, "temperature"),
+                               (self.top_k, torch.int32, "top_k"),
+                               (self.top_p, torch.float32, "top_p"),
+                               (self.min_p, torch.float32, "min_p")):
+            if t is not None:
+                _need_flat(t, dtype, (m,), name)
+        return QlinSamplingC(_ptr(self.temperature), _ptr(self.top_k), _ptr(self.top_p),
+                             _ptr(self.min_p))
+
+
+def sample(sampling: Sampling, logits: torch.Tensor, u: torch.Tensor,
+           ids: Optional[torch.Tensor] = None, probs: Optional[torch.Tensor] = None,
+           ws: Optional[torch.Tensor] = "auto") -> Tuple[torch.Tensor, torch.Tensor]:
+    """qlin_sample: (ids int32 [m], probs fp32 [m]) of fp32 logits [m, vocab] and u fp32 [m] in
+    [0, 1): the token that u falls on among the kept ones, and its probability among them."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype != torch.float32 or \
+            logits.dim() != 2 or \
+            (logits.shape[1] > 1 and logits.shape[0] > 0 and logits.stride(1) != 1):
+        raise TypeError("logits must be a float32 [m, vocab] tensor with contiguous rows")
+    m, vocab = logits.shape
+    dev = logits.device
+    c = ctypes.byref(sampling.c_struct(m))
+    _need_flat(u, torch.float32, (m,), "u")
+    if ids is None:
+        ids = torch.empty(m, dtype=torch.int32, device=dev)
+    else:
+        _need_flat(ids, torch.int32, (m,), "ids")
+    if probs is None:
+        probs = torch.empty(m, dtype=torch.float32, device=dev)
+    else:
+        _need_flat(probs, torch.float32, (m,), "probs")
+    _same_device(dev, (("temperature", sampling.temperature), ("top_k", sampling.top_k),
+                       ("top_p", sampling.top_p), ("min_p", sampling.min_p), ("u", u),
+                       ("ids", ids), ("probs", probs)))
+    lib = _lib()
+    _with_workspace(
+        ws, dev, lambda: lib.qlin_sample_workspace_bytes(m, vocab),
+        lambda wp, wb, stream: lib.qlin_sample(
+            c, logits.data_ptr(), m, vocab, _row_pitch(logits), u.data_ptr(), ids.data_ptr(),
+            probs.data_ptr(), wp, wb, stream), "qlin_sample")
+    return ids, probs
