@@ -38,7 +38,7 @@ HEADERS = [os.path.join(CSRC, f) for f in ("device_common.h", "codes.h", "kernel
                                            "launch_impl.h", "checks.h", "rows/rows.h", "rows/group.h",
                                            "rows/route.h", "rows/rows_plan.h", "kv/kv_layout.h",
                                            "kv/kv_store.h", "kv/attend.h", "kv/kv_plan.h",
-                                           "sample/sample.h")] + [
+                                           "sample/sample.h", "sample/split.h")] + [
     os.path.join(ROOT, "include", f) for f in ("qlin.h", "qlin_rows.h", "qlin_kv.h", "qlin_sample.h")]
 
 GEMV_BITS = (2, 3, 4, 5, 6, 7, 8, 16)   # part 0: GEMV and row gather (16: fp16 control)
@@ -58,7 +58,8 @@ HIPCC_FLAGS = [
     "-I", os.path.join(ROOT, "include"),
 ]
 # The quantizer's arithmetic must round every operation on its own (bit-exact
-# codes, scales and zero points): no a*b+c contracted into one fma.
+# codes, scales and zero points): no a*b+c contracted into one fma.  The cache's
+# quantizer and the draw's exponents likewise.
 QUANT_FLAGS = ["-ffp-contract=off"]
 
 
@@ -81,7 +82,7 @@ def _units():
     units.append(("rows_api", ROWS_API_SOURCE, []))
     for b in GEMM_BITS:
         units.append((f"rows_b{b}", ROWS_INST_SOURCE, [f"-DQLIN_INST_BITS={b}"]))
-    units.append(("sample", SAMPLE_SOURCE, []))
+    units.append(("sample", SAMPLE_SOURCE, QUANT_FLAGS))
     units.append(("kv_api", KV_API_SOURCE, []))
     for kb in KV_BITS:
         for vb in KV_BITS:

@@ -88,6 +88,7 @@ struct SampleShared {
   uint32_t digit, above_count;
   uint64_t above_mass;
   int found;
+  float tops[kSampleWaves];
 };
 
 __device__ __forceinline__ uint64_t shfl_up64(uint64_t v, int d) {
@@ -165,13 +166,12 @@ __device__ __forceinline__ void select_byte(SampleShared& sh, const float* x, in
   __syncthreads();
 }
 
-// One work-group per row.  Sums of p are integers (steps of 2^-45), so that they do
-// not depend on their order.  The last kept token is found byte by byte of its
+// A row by one work-group, whatever it holds: sums of p are integers (steps of 2^-45), so that
+// they do not depend on their order; the last kept token is found byte by byte of its
 // logit's bits, over histograms of counts (top_k) and then of masses (top_p).
-__global__ __launch_bounds__(kSampleThreads) void k_sample_row(const SampleArgs a) {
-  __shared__ SampleShared sh;
-  __shared__ float tops[kSampleWaves];
-  const int row = blockIdx.x, n = a.vocab;
+__device__ __forceinline__ void sample_alone(const SampleArgs& a, int row, SampleShared& sh) {
+  float* tops = sh.tops;
+  const int n = a.vocab;
   const float* x = a.logits + row * a.ld;
   SampleRow r = sample_row(a, row);
   float top = -__builtin_inff();

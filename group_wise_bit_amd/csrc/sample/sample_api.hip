@@ -3,7 +3,7 @@
 
 #include "../../../include/qlin_sample.h"
 #include "../checks.h"
-#include "sample.h"
+#include "split.h"
 
 using namespace qlin;
 
@@ -11,7 +11,34 @@ namespace {
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-constexpr int kMaxVocab = 1 << 18;
+constexpr int kMaxVocab = kSlice * kSlices;
+
+int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
+
+// Rows are drawn in batches of this many, so that the workspace is bounded (65 MB
+// for rows of 2^18 tokens): enough of them to fill the chip with slices.
+constexpr int kBatchSlices = 8192;
+constexpr int kBatchRows = 512;
+
+struct SamplePlan {
+  int slices, rows;
+  int64_t mass, count, stat, plan, list, bytes;    // offsets in the workspace, and its size
+};
+
+SamplePlan sample_plan(int m, int vocab) {
+  SamplePlan p{};
+  p.slices = (vocab + kSlice - 1) / kSlice;
+  const int most = kBatchSlices / p.slices < kBatchRows ? kBatchSlices / p.slices : kBatchRows;
+  p.rows = m < most ? m : most;
+  const int64_t items = (int64_t)p.rows * p.slices;
+  p.mass = kCounterBytes;
+  p.count = align256(p.mass + items * kBins * (int64_t)sizeof(double));
+  p.stat = align256(p.count + items * kBins * (int64_t)sizeof(uint32_t));
+  p.plan = align256(p.stat + items * (int64_t)sizeof(SliceStat));
+  p.list = align256(p.plan + p.rows * (int64_t)sizeof(RowPlanS));
+  p.bytes = p.list + p.rows * (int64_t)kListMax * (int64_t)sizeof(uint2);
+  return p;
+}
 
 }  // namespace
 
@@ -19,7 +46,7 @@ extern "C" {
 
 int64_t qlin_sample_workspace_bytes(int32_t m, int32_t vocab) {
   if (m < 1 || m > kMaxM || vocab < 1 || vocab > kMaxVocab) return 0;
-  return kCounterBytes;
+  return sample_plan(m, vocab).bytes;
 }
 
 qlin_status qlin_sample(const qlin_sampling* s, const float* logits, int32_t m, int32_t vocab,
@@ -63,7 +90,25 @@ qlin_status qlin_sample(const qlin_sampling* s, const float* logits, int32_t m, 
   a.probs = probs;
   a.m = m;
   a.vocab = vocab;
-  hipLaunchKernelGGL(k_sample_row, dim3(m), dim3(kSampleThreads), 0, stream, a);
+  const SamplePlan p = sample_plan(m, vocab);
+  char* const base = static_cast<char*>(workspace);
+  SplitArgs b{};
+  b.s = a;
+  b.slices = p.slices;
+  b.cum_mass = reinterpret_cast<double*>(base + p.mass);
+  b.cum_count = reinterpret_cast<uint32_t*>(base + p.count);
+  b.stat = reinterpret_cast<SliceStat*>(base + p.stat);
+  b.plan = reinterpret_cast<RowPlanS*>(base + p.plan);
+  b.list = reinterpret_cast<uint2*>(base + p.list);
+  const bool cuts = a.top_k != nullptr || a.top_p != nullptr || a.min_p != nullptr;
+  for (b.row0 = 0; b.row0 < m; b.row0 += p.rows) {
+    const int rows = m - b.row0 < p.rows ? m - b.row0 : p.rows;
+    hipLaunchKernelGGL(k_sample_bins, dim3(rows * p.slices), dim3(kBinThreads), 0, stream, b);
+    hipLaunchKernelGGL(k_sample_bounds, dim3(rows), dim3(kBins), 0, stream, b);
+    if (cuts)
+      hipLaunchKernelGGL(k_sample_gather, dim3(rows * p.slices), dim3(kBinThreads), 0, stream, b);
+    hipLaunchKernelGGL(k_sample_pick, dim3(rows), dim3(kPickThreads), 0, stream, b);
+  }
   return hip_status(hipGetLastError());
 }
 

@@ -1,0 +1,552 @@
+// Drawing tokens with a row split over work-groups (gfx950, wave64).
+#pragma once
+
+#include "sample.h"
+
+namespace qlin {
+
+// The steps of a draw:
+//   bins    every slice of 4096 logits: counts and masses by bins of the exponent,
+//   bounds  every row: the bins in which the cuts of top_k, top_p and min_p can lie,
+//   gather  every slice: its tokens in these bins, in the order of the vocabulary,
+//   pick    every row: the cut among them, the slice that u falls into, the token.
+// Exponents are t = 12 l / temperature in 64 bits; a bin is floor(t), so that bins of
+// different slices line up whatever their largest logit, and the mass of a
+// token is exp((t - middle of its bin) / 12), a polynomial of degree 7, times a factor per
+// bin.  Bins from 384 below the top one (exp(-32)) on hold no mass.
+constexpr int kSlice = 4096;
+constexpr int kSlices = 64;                  // of a row, at most
+constexpr int kBins = 384;
+constexpr int kBinScale = 12;
+constexpr int kListMax = 8192;               // tokens that are gathered, at most
+constexpr int kBinThreads = 256;
+
+struct SliceStat {
+  double floor_top;                          // floor(t) of its largest logit
+  float top;                                 // -inf: no tokens
+  int pad;
+};
+
+struct RowPlanS {
+  double floor_top;                          // of the row
+  float top;
+  int mode;                                  // 0: no tokens, 1: largest, 2: list, 3: by itself
+  int a, z, e;                               // gathered bins a .. z and e (-1: none)
+  int n, main;                               // gathered tokens, those of bins a .. z
+  int k_main, k_extra;                       // tokens of a .. z / of e among the first top_k
+  double mass_a;                             // of the bins before a
+  double mass_k;                             // of the first top_k without those k_main / k_extra
+  int slice;                                 // mode 1: the first slice with the largest logit
+  int at[kSlices + 1];                       // where a slice's tokens begin in the list
+  double base[kSlices];                      // a slice's mass of the bins before a
+};
+
+struct SplitArgs {
+  SampleArgs s;
+  int row0, slices;
+  double* cum_mass;                          // [rows][slices][kBins]: sums up to a bin
+  uint32_t* cum_count;
+  SliceStat* stat;                           // [rows][slices]
+  RowPlanS* plan;                            // [rows]
+  uint2* list;                               // [rows][kListMax]: index, logit
+};
+
+// 12 / temperature in two parts, and t of a logit: hi rounded, lo what is missing.
+struct BinScale {
+  double hi, lo;
+};
+__device__ __forceinline__ BinScale bin_scale(double t) {
+  BinScale c;
+  c.hi = (double)kBinScale / t;
+  c.lo = __builtin_fma(-c.hi, t, (double)kBinScale) / t;
+  if (!(t < (double)__builtin_inff())) c.lo = 0.;
+  return c;
+}
+// (from |t| = 2^51 on a bin holds one value of l only, and any x will do)
+__device__ __forceinline__ double t_low(double l, double hi, BinScale c) {
+  const double x = __builtin_fma(l, c.lo, __builtin_fma(l, c.hi, -hi));
+  return __builtin_fmin(__builtin_fmax(x, -0.25), 0.25);
+}
+
+// exp(x / 12) - 1 + one for |x| <= 1/2 (and a little beyond): x^8 / (12^8 8!) < 2^-51.
+__device__ __forceinline__ double bin_mass(double x, double one) {
+  const double z = x * (1. / kBinScale);
+  double p = 1. / 5040;
+  p = __builtin_fma(p, z, 1. / 720);
+  p = __builtin_fma(p, z, 1. / 120);
+  p = __builtin_fma(p, z, 1. / 24);
+  p = __builtin_fma(p, z, 1. / 6);
+  p = __builtin_fma(p, z, 0.5);
+  p = __builtin_fma(p, z, 1.);
+  return __builtin_fma(p, z, one);
+}
+// Masses within a bin are whole numbers of 2^-34: sums of 2^18 equal ones are exact, and
+// the sums of histograms and of lists are sums of the same numbers.
+constexpr int kMassStep = 34;
+constexpr double kMassOne = 1. + (double)(1 << (52 - kMassStep));
+
+// Mass of a logit relative to the middle of the bin floor_top.
+__device__ __forceinline__ double list_mass(float l, double floor_top, BinScale c) {
+  const double ld = (double)l, hi = ld * c.hi, f = __builtin_floor(hi);
+  const double p = bin_mass(hi - f - 0.5 + t_low(ld, hi, c), kMassOne) - (kMassOne - 1.);
+  return p * exp((f - floor_top) * (1. / kBinScale));
+}
+__device__ __forceinline__ int bin_of(float l, double floor_top, BinScale c) {
+  const double k = floor_top - __builtin_floor((double)l * c.hi);
+  return k < (double)kBins ? (int)k : kBins;
+}
+
+template <typename T>
+__device__ __forceinline__ T wave_scan(T v) {          // inclusive
+  const int lane = lane_id();
+  for (int d = 1; d < 64; d *= 2) {
+    const T o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// A histogram entry: the count from bit 51 on (4096 at most), the mass in its steps
+// below (4096 exp(1 / 24) 2^34 at most): one LDS atomic per token, and a sum that does
+// not depend on the order.
+constexpr int kCountBit = 51;
+
+__global__ __launch_bounds__(kBinThreads) void k_sample_bins(const SplitArgs a) {
+  __shared__ unsigned long long hist[kBins];
+  __shared__ float tops[4];
+  __shared__ double wave_mass[4];
+  __shared__ uint32_t wave_count[4];
+  const int slice = blockIdx.x % a.slices, r = blockIdx.x / a.slices, row = a.row0 + r;
+  const int64_t at = (int64_t)r * a.slices + slice;
+  const float* x = a.s.logits + row * a.s.ld + slice * kSlice;
+  const int n = min(a.s.vocab - slice * kSlice, kSlice);
+  constexpr int per = kSlice / kBinThreads;
+  float l[per];
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int j = 0; j < per; ++j) {
+    const int i = j * kBinThreads + threadIdx.x;
+    l[j] = i < n ? x[i] : -__builtin_inff();
+  }
+  const SampleRow set = sample_row(a.s, row);
+  for (int i = threadIdx.x; i < kBins; i += kBinThreads) hist[i] = 0;
+#pragma unroll
+  for (int j = 0; j < per; ++j) {
+    l[j] = logit_of(l[j]);
+    top = fmaxf(top, l[j]);
+  }
+  for (int d = 32; d > 0; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
+  if (lane_id() == 0) tops[wave_id()] = top;
+  __syncthreads();
+  for (int w = 0; w < 4; ++w) top = fmaxf(top, tops[w]);
+  const BinScale c = bin_scale(set.t == 0. ? 1. : set.t);
+  const double first = top > -__builtin_inff() ? __builtin_floor((double)top * c.hi) : 0.;
+  if (threadIdx.x == 0) a.stat[at] = SliceStat{first, top, 0};
+  if (set.t == 0. || top == -__builtin_inff()) return;
+#pragma unroll
+  for (int j = 0; j < per; ++j) {
+    if (l[j] == -__builtin_inff()) continue;
+    const double ld = (double)l[j], hi = ld * c.hi, f = __builtin_floor(hi);
+    const double k = first - f;
+    if (k < (double)kBins) {
+      const double p = bin_mass(hi - f - 0.5 + t_low(ld, hi, c), kMassOne);
+      const uint64_t b = __builtin_bit_cast(uint64_t, p);
+      atomicAdd(&hist[(int)k], (unsigned long long)((b & ((1ull << 52) - 1)) | (1ull << kCountBit)));
+    }
+  }
+  __syncthreads();
+  double mass_before = 0.;
+  uint32_t count_before = 0;
+  for (int base = 0; base < kBins; base += kBinThreads) {
+    const int k = base + threadIdx.x;
+    const uint64_t h = k < kBins ? hist[k] : 0;
+    double m = (double)(h & ((1ull << kCountBit) - 1)) * (1. / (double)(1ull << kMassStep)) *
+               exp(-(double)k * (1. / kBinScale));
+    uint32_t q = (uint32_t)(h >> kCountBit);
+    m = wave_scan(m);
+    q = wave_scan(q);
+    if (lane_id() == 63) { wave_mass[wave_id()] = m; wave_count[wave_id()] = q; }
+    __syncthreads();
+    double mb = mass_before;
+    uint32_t cb = count_before;
+    for (int w = 0; w < 4; ++w) {
+      if (w == wave_id()) { m += mb; q += cb; }
+      mb += wave_mass[w];
+      cb += wave_count[w];
+    }
+    mass_before = mb;
+    count_before = cb;
+    if (k < kBins) {
+      a.cum_mass[at * kBins + k] = m;
+      a.cum_count[at * kBins + k] = q;
+    }
+    __syncthreads();
+  }
+}
+
+// One work-group per row, a thread per bin.
+__global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
+  __shared__ double mass[kBins];
+  __shared__ uint32_t count[kBins];
+  __shared__ double factor[kSlices];
+  __shared__ int shift[kSlices];
+  const int r = blockIdx.x, row = a.row0 + r, k = threadIdx.x, lane = lane_id();
+  RowPlanS& p = a.plan[r];
+  const SampleRow set = sample_row(a.s, row);
+  const int64_t at = (int64_t)r * a.slices;
+  // the row's top, and how far below it the slices begin (every wave by itself)
+  const SliceStat st = lane < a.slices ? a.stat[at + lane] : SliceStat{0., -__builtin_inff(), 0};
+  float top = st.top;
+  for (int d = 32; d > 0; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
+  if (top == -__builtin_inff() || set.t == 0.) {
+    if (k == 0) {
+      p.mode = top == -__builtin_inff() ? 0 : 1;
+      p.top = top;
+      p.n = 0;
+    }
+    const uint64_t has = __ballot(st.top == top);
+    if (k == 0) p.slice = __builtin_ctzll(has);
+    return;
+  }
+  const BinScale c = bin_scale(set.t);
+  const double t_top = (double)top * c.hi, f = __builtin_floor(t_top);
+  if (k < kSlices) {
+    const double d = f - st.floor_top;
+    const int s = st.top > -__builtin_inff() && d < (double)kBins ? (int)d : kBins;
+    shift[k] = s;
+    factor[k] = exp(-(double)s * (1. / kBinScale));
+  }
+  __syncthreads();
+  double m = 0.;
+  uint32_t q = 0;
+  for (int s = 0; s < a.slices; ++s) {
+    const int d = k - shift[s];
+    if (d >= 0) {
+      m += a.cum_mass[(at + s) * kBins + d] * factor[s];
+      q += a.cum_count[(at + s) * kBins + d];
+    }
+  }
+  mass[k] = m;
+  count[k] = q;
+  // the first bin with which the count reaches top_k
+  const int bk = set.k != 0 ? __syncthreads_count(q < (uint32_t)set.k) : kBins;
+  __syncthreads();
+  const bool cut_k = bk < kBins;               // (or fewer tokens have any mass)
+  const bool whole = cut_k && count[bk] == (uint32_t)set.k;
+  const double all = mass[kBins - 1];
+  const double high = cut_k ? mass[bk] : all;
+  const double low = !cut_k || whole ? high : bk > 0 ? mass[bk - 1] : 0.;
+  // sums of histograms and lists differ by their roundings to 64 bits only
+  const bool cut_p = set.p < 1.f;
+  const double slack = 1. / (1 << 30);
+  const int p0 = __syncthreads_count(m < (double)set.p * low * (1. - slack));
+  const int p1 = __syncthreads_count(m < (double)set.p * high * (1. + slack));
+  int lo = kBins, hi = kBins;
+  if (cut_k) lo = hi = bk;
+  if (cut_p) {
+    lo = min(lo, min(p0, kBins - 1));
+    hi = min(hi, min(p1, kBins - 1));
+  }
+  if (set.mp > 0.f) {
+    const double edge = t_top + log((double)set.mp) * kBinScale;
+    const double near = fmax(1. / (1 << 20), __builtin_fabs(t_top) * 0x1p-48);
+    const double m0 = f - __builtin_floor(edge + near), m1 = f - __builtin_floor(edge - near);
+    lo = min(lo, m0 < (double)kBins ? max((int)m0, 0) : kBins);
+    hi = min(hi, m1 < (double)kBins ? max((int)m1, 0) : kBins);
+  }
+  // (nothing lies beyond the last bin)
+  const int first = lo, last = min(hi, kBins - 1);
+  const int extra = cut_p && cut_k && !whole && bk > last ? bk : -1;
+  const uint32_t before = first > 0 ? count[first - 1] : 0u;
+  const int main = first < kBins ? (int)(count[last] - before) : 0;
+  const int more = extra >= 0 ? (int)(count[extra] - count[extra - 1]) : 0;
+  if (k < 64) {
+    int size = 0;
+    double base = 0.;
+    if (k < a.slices) {
+      const uint32_t* n = a.cum_count + (at + k) * kBins - shift[k];
+      const int s = shift[k];
+      auto upto = [&](int bin) { return bin >= s ? n[bin] : 0u; };
+      if (first < kBins) size = (int)(upto(last) - upto(first - 1));
+      if (extra >= 0) size += (int)(upto(extra) - upto(extra - 1));
+      if (first > 0 && first - 1 >= s)
+        base = a.cum_mass[(at + k) * kBins + first - 1 - s] * factor[k];
+    }
+    const int end = wave_scan(size);
+    p.at[k + 1] = end;
+    if (k == 0) p.at[0] = 0;
+    p.base[k] = base;
+  }
+  if (k == 0) {
+    p.floor_top = f;
+    p.top = top;
+    p.a = first;
+    p.z = last;
+    p.e = extra;
+    p.n = main + more;
+    p.main = main;
+    p.mode = main + more <= kListMax ? 2 : 3;
+    p.mass_a = first > 0 ? mass[first - 1] : 0.;
+    p.k_main = cut_k && bk <= last ? set.k - (int)before : main;
+    p.k_extra = extra >= 0 ? set.k - (int)count[extra - 1] : 0;
+    // the mass of the first top_k: mass_a and the list's, or what lies before the bin e and that bin's
+    p.mass_k = extra >= 0 ? mass[extra - 1] : cut_k && bk <= last ? -1. : high;
+  }
+}
+
+__global__ __launch_bounds__(kBinThreads) void k_sample_gather(const SplitArgs a) {
+  __shared__ int counts[64];
+  const int slice = blockIdx.x % a.slices, r = blockIdx.x / a.slices, row = a.row0 + r;
+  const RowPlanS& p = a.plan[r];
+  if (p.mode != 2) return;
+  const int from = p.at[slice];
+  if (p.at[slice + 1] == from) return;
+  const float* x = a.s.logits + row * a.s.ld + slice * kSlice;
+  const int n = min(a.s.vocab - slice * kSlice, kSlice);
+  const BinScale c = bin_scale(sample_row(a.s, row).t);
+  const double f = p.floor_top;
+  const int first = p.a, last = p.z, extra = p.e, lane = lane_id(), wave = wave_id();
+  constexpr int per = kSlice / kBinThreads;
+  float l[per];
+  uint32_t in = 0;
+#pragma unroll
+  for (int j = 0; j < per; ++j) {
+    const int i = j * kBinThreads + threadIdx.x;
+    l[j] = i < n ? x[i] : -__builtin_inff();
+  }
+#pragma unroll
+  for (int j = 0; j < per; ++j) {
+    l[j] = logit_of(l[j]);
+    const int k = l[j] > -__builtin_inff() ? bin_of(l[j], f, c) : kBins;
+    const bool mine = (k >= first && k <= last) || k == extra;
+    in |= (uint32_t)mine << j;
+    const uint64_t b = __ballot(mine);
+    if (lane == 0) counts[j * 4 + wave] = __builtin_popcountll(b);
+  }
+  __syncthreads();
+  const int ends = wave_scan(counts[lane]);
+#pragma unroll
+  for (int j = 0; j < per; ++j) {
+    const bool mine = in >> j & 1;
+    const uint64_t b = __ballot(mine);
+    const int end = __shfl(ends, j * 4 + wave);
+    if (mine) {
+      const int pos = from + end - __builtin_popcountll(b) + __builtin_popcountll(b & ((1ull << lane) - 1));
+      a.list[(int64_t)r * kListMax + pos] = make_uint2(
+          slice * kSlice + j * kBinThreads + threadIdx.x, __builtin_bit_cast(uint32_t, l[j]));
+    }
+  }
+}
+
+constexpr int kPickThreads = kSampleThreads;
+constexpr int kPickPer = kListMax / kPickThreads;
+
+// The order of tokens as an ascending integer: by logit, descending, then by index.
+__device__ __forceinline__ uint64_t order_key(float l, uint32_t index) {
+  return (uint64_t)~logit_key(l) << 32 | index;
+}
+__device__ __forceinline__ float key_logit(uint64_t key) {
+  const uint32_t b = ~(uint32_t)(key >> 32);
+  return __builtin_bit_cast(float, b & 0x80000000u ? b & 0x7FFFFFFFu : ~b);
+}
+
+// Sorts keys[0 .. size), size a power of two from 64 on: bitonic, exchanges within a wave's 64 keys
+// through registers.
+__device__ __forceinline__ void sort_keys(uint64_t* keys, int size) {
+  for (int k = 2; k <= size; k *= 2) {
+    int j = k / 2;
+    for (; j >= 64; j /= 2) {
+      for (int i = threadIdx.x; i < size / 2; i += kPickThreads) {
+        const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+        const uint64_t x = keys[lo], y = keys[hi];
+        if ((x > y) == ((lo & k) == 0)) { keys[lo] = y; keys[hi] = x; }
+      }
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < size; i += kPickThreads) {
+      uint64_t x = keys[i];
+      for (int d = j; d > 0; d /= 2) {
+        const uint32_t ol = __shfl_xor((uint32_t)x, d), oh = __shfl_xor((uint32_t)(x >> 32), d);
+        const uint64_t y = (uint64_t)oh << 32 | ol;
+        const bool lower = (i & d) == 0, up = (i & k) == 0;
+        x = (lower == up) == (x < y) ? x : y;
+      }
+      keys[i] = x;
+    }
+    __syncthreads();
+  }
+}
+
+struct PickShared {
+  uint64_t keys[kListMax];
+  double sums[kListMax];
+  SampleShared alone;
+  double wave[kSampleWaves];
+  double before, target, total;
+  int slice, count[3];
+};
+
+// Inclusive sums of v[0 .. n) in place, each thread's kPickPer (or fewer) in a row.
+__device__ __forceinline__ void sum_list(double* v, double* wave, int n) {
+  const int per = (n + kPickThreads - 1) / kPickThreads;
+  const int i0 = threadIdx.x * per;
+  double s = 0.;
+  for (int i = 0; i < per; ++i)
+    if (i0 + i < n) s += v[i0 + i];
+  const double up = wave_scan(s);
+  if (lane_id() == 63) wave[wave_id()] = up;
+  __syncthreads();
+  double run = up - s;
+  for (int w = 0; w < wave_id(); ++w) run += wave[w];
+  for (int i = 0; i < per; ++i)
+    if (i0 + i < n) {
+      run += v[i0 + i];
+      v[i0 + i] = run;
+    }
+  __syncthreads();
+}
+
+__global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a) {
+  __shared__ PickShared sh;
+  const int r = blockIdx.x, row = a.row0 + r, lane = lane_id();
+  const RowPlanS& p = a.plan[r];
+  const float* x = a.s.logits + row * a.s.ld;
+  const int mode = p.mode;
+  if (mode == 3) {
+    sample_alone(a.s, row, sh.alone);
+    return;
+  }
+  if (mode == 0) {
+    if (threadIdx.x == 0) {
+      a.s.ids[row] = -1;
+      if (a.s.probs != nullptr) a.s.probs[row] = 0.f;
+    }
+    return;
+  }
+  if (mode == 1) {
+    if (threadIdx.x == 0) sh.slice = 0x7FFFFFFF;
+    __syncthreads();
+    for (int i = p.slice * kSlice + threadIdx.x; i < min((p.slice + 1) * kSlice, a.s.vocab);
+         i += kPickThreads)
+      if (logit_of(x[i]) == p.top) atomicMin(&sh.slice, i);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      a.s.ids[row] = sh.slice;
+      if (a.s.probs != nullptr) a.s.probs[row] = 1.f;
+    }
+    return;
+  }
+  const SampleRow set = sample_row(a.s, row);
+  const BinScale c = bin_scale(set.t);
+  const double f = p.floor_top;
+  const int n = p.n, main = p.main;
+  const uint2* list = a.list + (int64_t)r * kListMax;
+  uint64_t cut = 0;                            // keys up to it are kept
+  if (n > 0) {
+    int size = 64;
+    while (size < n) size *= 2;
+    for (int i = threadIdx.x; i < size; i += kPickThreads) {
+      const uint2 t = i < n ? list[i] : make_uint2(0, 0);
+      sh.keys[i] = i < n ? order_key(__builtin_bit_cast(float, t.y), t.x) : ~0ull;
+    }
+    if (threadIdx.x < 3) sh.count[threadIdx.x] = 0;
+    __syncthreads();
+    sort_keys(sh.keys, size);
+    for (int i = threadIdx.x; i < n; i += kPickThreads)
+      sh.sums[i] = list_mass(key_logit(sh.keys[i]), f, c);
+    __syncthreads();
+    sum_list(sh.sums, sh.wave, n);
+    int kept = p.k_main;
+    if (set.p < 1.f) {
+      double mass_k = p.mass_k;
+      if (p.e >= 0) mass_k += sh.sums[main + p.k_extra - 1] - (main > 0 ? sh.sums[main - 1] : 0.);
+      else if (mass_k < 0.) mass_k = p.mass_a + sh.sums[p.k_main - 1];
+      const double target = (double)set.p * mass_k;
+      int less = 0;
+      for (int i = threadIdx.x; i < main; i += kPickThreads) less += p.mass_a + sh.sums[i] < target;
+      if (less) atomicAdd(&sh.count[0], less);
+    }
+    if (set.mp > 0.f) {
+      const double top_hi = (double)p.top * c.hi, top_lo = t_low((double)p.top, top_hi, c);
+      int pass = 0;
+      for (int i = threadIdx.x; i < main; i += kPickThreads) {
+        const float l = key_logit(sh.keys[i]);
+        const double hi = (double)l * c.hi;
+        const double e = (hi - top_hi + (t_low((double)l, hi, c) - top_lo)) * (1. / kBinScale);
+        pass += l == p.top || exp(e) >= (double)set.mp;
+      }
+      if (pass) atomicAdd(&sh.count[1], pass);
+    }
+    __syncthreads();
+    if (set.p < 1.f) kept = min(kept, sh.count[0] + 1);
+    if (set.mp > 0.f) kept = min(kept, sh.count[1]);
+    cut = kept > 0 ? sh.keys[kept - 1] : 0;
+    __syncthreads();
+    // the kept ones' masses in the order of the vocabulary
+    for (int i = threadIdx.x; i < n; i += kPickThreads) {
+      const uint2 t = list[i];
+      const float l = __builtin_bit_cast(float, t.y);
+      sh.sums[i] = kept > 0 && order_key(l, t.x) <= cut ? list_mass(l, f, c) : 0.;
+    }
+    __syncthreads();
+    sum_list(sh.sums, sh.wave, n);
+    if (kept == 0) cut = 0;
+  }
+  // the slice that u falls into
+  if (wave_id() == 0) {
+    double w = 0.;
+    if (lane < a.slices) {
+      w = p.base[lane];
+      const int i0 = p.at[lane], i1 = p.at[lane + 1];
+      if (i1 > i0) w += sh.sums[i1 - 1] - (i0 > 0 ? sh.sums[i0 - 1] : 0.);
+    }
+    const double end = wave_scan(w);
+    const double total = __shfl(end, 63), target = (double)set.u * total;
+    const uint64_t past = __ballot(w > 0. && end > target), any = __ballot(w > 0.);
+    const int s = past != 0 ? __builtin_ctzll(past) : 63 - __builtin_clzll(any);
+    if (lane == s) {
+      sh.slice = s;
+      sh.before = end - w;
+      sh.target = target;
+      sh.total = total;
+      sh.count[0] = sh.count[1] = 0x7FFFFFFF;
+      sh.count[2] = -1;
+    }
+  }
+  __syncthreads();
+  // the token in the slice
+  constexpr int per = kSlice / kPickThreads;
+  const int first = sh.slice * kSlice, i0 = first + (int)threadIdx.x * per;
+  double w[per], s = 0.;
+#pragma unroll
+  for (int j = 0; j < per; ++j) {
+    w[j] = 0.;
+    const float l = i0 + j < a.s.vocab ? logit_of(x[i0 + j]) : -__builtin_inff();
+    if (l > -__builtin_inff() && (bin_of(l, f, c) < p.a || order_key(l, i0 + j) <= cut))
+      w[j] = list_mass(l, f, c);
+    s += w[j];
+  }
+  const double up = wave_scan(s);
+  if (lane == 63) sh.wave[wave_id()] = up;
+  __syncthreads();
+  double run = sh.before + (up - s);
+  for (int v = 0; v < wave_id(); ++v) run += sh.wave[v];
+#pragma unroll
+  for (int j = 0; j < per; ++j) {
+    run += w[j];
+    if (w[j] > 0.) {
+      if (run > sh.target) atomicMin(&sh.count[0], i0 + j);
+      atomicMax(&sh.count[2], i0 + j);
+    }
+  }
+  __syncthreads();
+  const int id = sh.count[0] != 0x7FFFFFFF ? sh.count[0] : sh.count[2];
+#pragma unroll
+  for (int j = 0; j < per; ++j)
+    if (i0 + j == id) {
+      a.s.ids[row] = id;
+      if (a.s.probs != nullptr) a.s.probs[row] = (float)(w[j] / sh.total);
+    }
+}
+
+}  // namespace qlin
