@@ -7,6 +7,7 @@ namespace qlin {
 
 constexpr int kAttendWaves = 4;
 constexpr int kAttendRows = 16;        // query heads of a work-group: a column block of an MFMA
+constexpr int kMaxParts = 1024;        // work-groups at most, and parts of a sequence
 
 struct AttendArgs {
   KvSeqs s;
@@ -24,7 +25,9 @@ struct AttendArgs {
   int rows;                  // query heads per work-group, min(ratio, 16)
   int rts;                   // work-groups' row blocks per head of the cache
   int window, groups;
-  float c;                   // scale * log2(e)
+  bool whole;                // a work-group per sequence and row block, nothing to join
+  uint32_t flip;             // sign bits of a negative scale
+  float c;                   // |scale| * log2(e), above 0
 };
 
 // Tokens [lo, hi) that a sequence sees.
@@ -40,23 +43,13 @@ __device__ __forceinline__ int seen_tiles(const AttendArgs& a, int b) {
   return hi > lo ? (hi + kKvTile - 1) / kKvTile - lo / kKvTile : 0;
 }
 
-// Tiles of all sequences before b = `until`, or all.
-__device__ __forceinline__ int64_t tiles_before(const AttendArgs& a, int until) {
-  const int lane = lane_id();
-  int64_t total = 0;
-  for (int base = 0; base < until; base += 64) {
-    const int n = base + lane < until ? seen_tiles(a, base + lane) : 0;
-    total += __builtin_amdgcn_readlane(scan64(n), 63);
-  }
-  return total;
-}
-
 // Every work-group takes `share` tiles of the list [sequence][head][row block][tile].
 __device__ __forceinline__ int64_t tile_share(int64_t all, int groups) {
   const int64_t s = (all + groups - 1) / groups;
   return s < kAttendWaves ? kAttendWaves : s;
 }
 
+// Where a wave has a tile: in registers,
 template <int D, int KB, int VB>
 struct KvRegs {
   static constexpr int G = D / 64;
@@ -64,35 +57,90 @@ struct KvRegs {
   u32x4 ks[G], vs[G];
   uint32_t kz[(G + 1) / 2];
   u32x2 vz[G];
+
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    using T = KvTile<D, KB, VB>;
+    const int lane = lane_id(), g = lane >> 4, r = lane & 15;
+#pragma unroll
+    for (int i = 0; i < KB * G / 4; ++i) k[i] = *(const u32x4*)(p + T::k + (i * 64 + lane) * 16);
+    if constexpr (KB < 16) {
+#pragma unroll
+      for (int c = 0; c < G; ++c) ks[c] = *(const u32x4*)(p + T::ks + c * 64 + g * 16);
+      if constexpr (G == 1) kz[0] = *(const uint16_t*)(p + T::kz + r * 2);
+      if constexpr (G == 2) kz[0] = *(const uint32_t*)(p + T::kz + r * 4);
+      if constexpr (G == 4) {
+        const u32x2 z = *(const u32x2*)(p + T::kz + r * 8);
+        kz[0] = z[0];
+        kz[1] = z[1];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VB * G / 4; ++i) v[i] = *(const u32x4*)(p + T::v + (i * 64 + lane) * 16);
+    if constexpr (VB < 16) {
+#pragma unroll
+      for (int c = 0; c < G; ++c) {
+        vs[c] = *(const u32x4*)(p + T::vs + c * 64 + g * 16);
+        vz[c] = *(const u32x2*)(p + T::vz + (g * G + c) * 8);
+      }
+    }
+  }
+  __device__ __forceinline__ u32x4 k_unit(int i) const { return k[i]; }
+  __device__ __forceinline__ u32x4 v_unit(int i) const { return v[i]; }
+  __device__ __forceinline__ u32x4 k_scales(int c) const { return ks[c]; }
+  __device__ __forceinline__ u32x4 v_scales(int c) const { return vs[c]; }
+  __device__ __forceinline__ uint32_t k_zeros(int i) const { return kz[i]; }
+  __device__ __forceinline__ u32x2 v_zeros(int c) const { return vz[c]; }
 };
 
+// or in LDS, as it lies in memory.
 template <int D, int KB, int VB>
-__device__ __forceinline__ void load_tile(KvRegs<D, KB, VB>& t, const uint8_t* p) {
+struct KvStage {
   using T = KvTile<D, KB, VB>;
-  constexpr int G = D / 64;
-  const int lane = lane_id(), g = lane >> 4, r = lane & 15;
-#pragma unroll
-  for (int i = 0; i < KB * G / 4; ++i) t.k[i] = *(const u32x4*)(p + T::k + (i * 64 + lane) * 16);
-  if constexpr (KB < 16) {
-#pragma unroll
-    for (int c = 0; c < G; ++c) t.ks[c] = *(const u32x4*)(p + T::ks + c * 64 + g * 16);
-    if constexpr (G == 1) t.kz[0] = *(const uint16_t*)(p + T::kz + r * 2);
-    if constexpr (G == 2) t.kz[0] = *(const uint32_t*)(p + T::kz + r * 4);
-    if constexpr (G == 4) {
-      const u32x2 z = *(const u32x2*)(p + T::kz + r * 8);
-      t.kz[0] = z[0];
-      t.kz[1] = z[1];
-    }
+  static constexpr int G = D / 64;
+  const uint8_t* p;
+  int lane, g, r;
+
+  __device__ __forceinline__ explicit KvStage(const uint8_t* at)
+      : p(at), lane(lane_id()), g(lane >> 4), r(lane & 15) {}
+  __device__ __forceinline__ u32x4 k_unit(int i) const { return *(const u32x4*)(p + T::k + (i * 64 + lane) * 16); }
+  __device__ __forceinline__ u32x4 v_unit(int i) const { return *(const u32x4*)(p + T::v + (i * 64 + lane) * 16); }
+  __device__ __forceinline__ u32x4 k_scales(int c) const { return *(const u32x4*)(p + T::ks + c * 64 + g * 16); }
+  __device__ __forceinline__ u32x4 v_scales(int c) const { return *(const u32x4*)(p + T::vs + c * 64 + g * 16); }
+  __device__ __forceinline__ uint32_t k_zeros(int i) const {
+    if constexpr (G == 1) return *(const uint16_t*)(p + T::kz + r * 2);
+    return *(const uint32_t*)(p + T::kz + r * 2 * G + i * 4);
   }
+  __device__ __forceinline__ u32x2 v_zeros(int c) const { return *(const u32x2*)(p + T::vz + (g * G + c) * 8); }
+};
+
+// Direct-to-LDS loads of a tile: 16 bytes of every lane an instruction, the last one of
+// fewer lanes.
+template <int D, int KB, int VB>
+constexpr int kTileLoads = (KvTile<D, KB, VB>::bytes + 1023) / 1024;
+template <int D, int KB, int VB>
+__device__ __forceinline__ void stage_tile(const uint8_t* src, uint8_t* lds) {
+  typedef __attribute__((address_space(3))) void lds_void;
+  constexpr int bytes = KvTile<D, KB, VB>::bytes;
+  const int lane = lane_id();
+  // (what was read from there has arrived)
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < VB * G / 4; ++i) t.v[i] = *(const u32x4*)(p + T::v + (i * 64 + lane) * 16);
-  if constexpr (VB < 16) {
-#pragma unroll
-    for (int c = 0; c < G; ++c) {
-      t.vs[c] = *(const u32x4*)(p + T::vs + c * 64 + g * 16);
-      t.vz[c] = *(const u32x2*)(p + T::vz + (g * G + c) * 8);
-    }
-  }
+  for (int i = 0; i < bytes / 1024; ++i)
+    __builtin_amdgcn_global_load_lds(src + i * 1024 + lane * 16, (lds_void*)(lds + i * 1024), 16, 0, 0);
+  if (bytes % 1024 != 0 && lane < bytes % 1024 / 16)
+    __builtin_amdgcn_global_load_lds(src + bytes / 1024 * 1024 + lane * 16,
+                                     (lds_void*)(lds + bytes / 1024 * 1024), 16, 0, 0);
+}
+// One LDS object per stage, so that the compiler can tell which loads a read waits for.
+template <int D, int KB, int VB, int I>
+__device__ __forceinline__ uint8_t* tile_stage() {
+  __shared__ __attribute__((aligned(16))) uint8_t st[kAttendWaves * KvTile<D, KB, VB>::bytes];
+  return st;
+}
+// s_waitcnt vmcnt(N), expcnt and lgkmcnt not waited on.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
 // Pairs of codes as fp16 numbers q - z, exactly: the code's bits go into the mantissa of
@@ -108,6 +156,17 @@ __device__ __forceinline__ f16x2 code_high(uint32_t w, uint32_t mask, uint32_t m
 template <int B0, int B1>
 __device__ __forceinline__ f16x2 zero_pair(uint32_t w) {
   return as_h2(__builtin_amdgcn_perm(0xE4E4E4E4u, w, 0x04000400u | (B1 << 16) | B0));
+}
+
+// Constants that the compiler does not know: a * x + b of an fp16 number x with these is
+// one v_fma_mix_f32, where a product or a difference would first convert x.
+struct MixConsts {
+  uint32_t magic;
+  float zero, minus;
+};
+__device__ __forceinline__ MixConsts mix_consts() {
+  return MixConsts{vreg_const(kMagic), __builtin_bit_cast(float, vreg_const(0u)),
+                   __builtin_bit_cast(float, vreg_const(0xBF800000u))};
 }
 
 __device__ __forceinline__ float max16x32(float v) {     // over lanes l, l ^ 16, l ^ 32, l ^ 48
@@ -138,17 +197,29 @@ struct AttendState {
 // towards zero, lo the rest: 21 bits).  So that P * s has these bits whatever the
 // size of s, P is taken relative to 2^off, off = max + e - 15, s < 2^e for every scale
 // so far: P s < 2^15.
-template <int D, int KB, int VB>
-__device__ __forceinline__ void attend_tile(AttendState<D>& st, KvRegs<D, KB, VB>& t,
+template <int D, int KB, int VB, typename Tile>
+__device__ __forceinline__ void attend_tile(AttendState<D>& st, const Tile& t,
                                             const f16x8 (&q)[D / 32], float c, bool edge, int first,
-                                            int lo, int hi, uint32_t magic) {
+                                            int lo, int hi, MixConsts mix) {
   constexpr int G = D / 64;
+  const uint32_t magic = mix.magic;
+  constexpr int kUnits = KB * G / 4, kHalf = kUnits >= 2 ? kUnits / 2 : 1;
   const int lane = lane_id(), g = lane >> 4;
   constexpr uint32_t klow = KB == 4 ? 0x000F000Fu : 0x00FF00FFu;
   constexpr uint32_t vlow = VB == 4 ? 0x000F000Fu : 0x00FF00FFu;
   float x[8];
+  u32x4 ks[G];
+  if constexpr (KB < 16) {
+#pragma unroll
+    for (int cg = 0; cg < G; ++cg) ks[cg] = t.k_scales(cg);
+  }
+  u32x4 ku[kHalf];                       // the half tile's units
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    if (h == 0 || kUnits >= 2) {
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) ku[i] = t.k_unit(h * kHalf + i);
+    }
     f32x4 acc[G];
 #pragma unroll
     for (int cg = 0; cg < G; ++cg) {
@@ -156,16 +227,17 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, KvRegs<D, KB, VB
       if constexpr (KB < 16) {
         const int byte = h * G + cg;
         const uint32_t sel = 0x04000400u | ((byte % 4) << 16) | (byte % 4);
-        c1 = as_h2(__builtin_amdgcn_perm(0xE4E4E4E4u, t.kz[byte / 4], sel));
+        c1 = as_h2(__builtin_amdgcn_perm(0xE4E4E4E4u, t.k_zeros(byte / 4), sel));
         if constexpr (KB == 4) c2 = c1 + f16x2{(f16)960.f, (f16)960.f};
       }
       f32x4 s{};
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         union { f16x8 v; f16x2 p[4]; uint32_t w[4]; } f;
-        const int at = (h * G + cg) * (KB / 2) + u * (KB / 4);      // word of the lane's run
+        // word of the lane's run, from its half's first unit on
+        const int at = (h * G + cg) * (KB / 2) + u * (KB / 4) - (kUnits >= 2 ? h * kHalf * 4 : 0);
         if constexpr (KB == 4) {
-          const uint32_t w = t.k[at / 4][at % 4], w8 = w >> 8;
+          const uint32_t w = ku[at / 4][at % 4], w8 = w >> 8;
           f.p[0] = code_low(w, klow, magic, c1);
           f.p[1] = code_high(w, klow << 4, magic, c2);
           f.p[2] = code_low(w8, klow, magic, c1);
@@ -173,12 +245,12 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, KvRegs<D, KB, VB
         } else if constexpr (KB == 8) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t w = t.k[(at + i) / 4][(at + i) % 4];
+            const uint32_t w = ku[(at + i) / 4][(at + i) % 4];
             f.p[2 * i] = code_low(w, klow, magic, c1);
             f.p[2 * i + 1] = code_low(w >> 8, klow, magic, c1);
           }
         } else {
-          f.v = __builtin_bit_cast(f16x8, t.k[at / 4]);
+          f.v = __builtin_bit_cast(f16x8, ku[at / 4]);
         }
         s = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.v, q[cg * 2 + u], s, 0, 0, 0);
       }
@@ -190,14 +262,20 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, KvRegs<D, KB, VB
 #pragma unroll
       for (int cg = 0; cg < G; ++cg) {
         if constexpr (KB < 16) {
-          const f16x2 sc = as_h2(t.ks[cg][h * 2 + i / 2]);
+          const f16x2 sc = as_h2(ks[cg][h * 2 + i / 2]);
           s = __builtin_fmaf(acc[cg][i], (float)sc[i % 2], s);
         } else {
           s += acc[cg][i];
         }
       }
-      x[h * 4 + i] = s * c;
+      x[h * 4 + i] = s;
     }
+  }
+  u32x4 vs[G];
+  u32x4 mask{~0u, ~0u, ~0u, ~0u};        // (16 bits) of the seen tokens' values
+  if constexpr (VB < 16) {
+#pragma unroll
+    for (int cg = 0; cg < G; ++cg) vs[cg] = t.v_scales(cg);
   }
   if (edge) {
 #pragma unroll
@@ -209,10 +287,9 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, KvRegs<D, KB, VB
         // (what lies there may be no number, and 0 times that is none either)
         if constexpr (VB < 16) {
 #pragma unroll
-          for (int cg = 0; cg < G; ++cg) t.vs[cg][i / 2] &= i % 2 ? 0x0000FFFFu : 0xFFFF0000u;
+          for (int cg = 0; cg < G; ++cg) vs[cg][i / 2] &= i % 2 ? 0x0000FFFFu : 0xFFFF0000u;
         } else {
-#pragma unroll
-          for (int b = 0; b < 4 * G; ++b) t.v[b][i / 2] &= i % 2 ? 0x0000FFFFu : 0xFFFF0000u;
+          mask[i / 2] &= i % 2 ? 0x0000FFFFu : 0xFFFF0000u;
         }
       }
     }
@@ -229,7 +306,7 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, KvRegs<D, KB, VB
     for (int cg = 0; cg < G; ++cg)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t pair = t.vs[cg][i];
+        const uint32_t pair = vs[cg][i];
         top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, pair));
       }
     const int one = max((int)top[0], (int)top[1]);
@@ -239,7 +316,7 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, KvRegs<D, KB, VB
     all = max(all, __builtin_amdgcn_readlane(one, 48));
     st.e = max(st.e, (all >> 10) - 14);
   }
-  const float off = st.m + (float)(st.e - 15);
+  const float off = __builtin_fmaf(st.m, c, (float)(st.e - 15));
   if (__ballot(off != st.off) != 0) {
     const float f = __builtin_amdgcn_exp2f(st.off - off);
     st.l *= f;
@@ -252,7 +329,7 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, KvRegs<D, KB, VB
   float p[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    p[i] = __builtin_amdgcn_exp2f(x[i] - off);
+    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -off));
     st.l += p[i];
   }
   union { f16x8 v; f16x2 p[4]; } ph, pl;
@@ -263,39 +340,43 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, KvRegs<D, KB, VB
       for (int i = 0; i < 4; ++i) {
         float w0 = p[2 * i], w1 = p[2 * i + 1];
         if constexpr (VB < 16) {
-          const f16x2 sc = as_h2(t.vs[cg][i]);
-          w0 *= (float)sc[0];
-          w1 *= (float)sc[1];
+          const uint32_t pair = vs[cg][i];
+          w0 = __builtin_fmaf((float)as_h2(pair)[0], w0, mix.zero);
+          w1 = __builtin_fmaf((float)as_h2(pair)[1], w1, mix.zero);
         }
         ph.p[i] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(w0, w1));
         pl.p[i] = __builtin_bit_cast(
-            f16x2, __builtin_amdgcn_cvt_pkrtz(w0 - (float)ph.p[i][0], w1 - (float)ph.p[i][1]));
+            f16x2, __builtin_amdgcn_cvt_pkrtz(__builtin_fmaf((float)ph.p[i][0], mix.minus, w0),
+                                              __builtin_fmaf((float)ph.p[i][1], mix.minus, w1)));
       }
     }
     f16x2 c1[4], c2[4];
     if constexpr (VB < 16) {
-      c1[0] = zero_pair<0, 1>(t.vz[cg][0]);
-      c1[1] = zero_pair<2, 3>(t.vz[cg][0]);
-      c1[2] = zero_pair<0, 1>(t.vz[cg][1]);
-      c1[3] = zero_pair<2, 3>(t.vz[cg][1]);
+      const u32x2 z = t.v_zeros(cg);
+      c1[0] = zero_pair<0, 1>(z[0]);
+      c1[1] = zero_pair<2, 3>(z[0]);
+      c1[2] = zero_pair<0, 1>(z[1]);
+      c1[3] = zero_pair<2, 3>(z[1]);
       if constexpr (VB == 4) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) c2[i] = c1[i] + f16x2{(f16)960.f, (f16)960.f};
       }
     }
+    u32x4 vu{};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       union { f16x8 v; f16x2 p[4]; } f;
+      if (j % (16 / VB) == 0) vu = t.v_unit(cg * (VB / 4) + j / (16 / VB));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (VB == 4) {
-          const uint32_t w = j < 2 ? t.v[cg][i] : t.v[cg][i] >> 8;
+          const uint32_t w = j < 2 ? vu[i] : vu[i] >> 8;
           f.p[i] = j % 2 == 0 ? code_low(w, vlow, magic, c1[i]) : code_high(w, vlow << 4, magic, c2[i]);
         } else if constexpr (VB == 8) {
-          const uint32_t w = t.v[cg * 2 + j / 2][i];
+          const uint32_t w = vu[i];
           f.p[i] = code_low(j % 2 == 0 ? w : w >> 8, vlow, magic, c1[i]);
         } else {
-          f.p[i] = as_h2(t.v[cg * 4 + j][i]);
+          f.p[i] = as_h2(vu[i] & mask[i]);
         }
       }
       st.o[cg][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.v, ph.v, st.o[cg][j], 0, 0, 0);
@@ -304,45 +385,95 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, KvRegs<D, KB, VB
   }
 }
 
+__device__ __forceinline__ f16x8 signed_by(f16x8 v, uint32_t flip) {
+  return __builtin_bit_cast(f16x8, __builtin_bit_cast(u32x4, v) ^ flip);
+}
+
 // The table entries of 64 pages, one per lane.
 struct PageList {
   int base, entry;
 };
 
+// Tiles up to this size go through LDS, in two stages of four waves' tiles: the loads
+// of the next tile run while one is used, without registers.  Larger ones are held in registers.
 template <int D, int KB, int VB>
-__global__ __launch_bounds__(256) void k_attend(const AttendArgs a) {
+constexpr bool kStaged = KvTile<D, KB, VB>::bytes <= 10240;
+template <int D, int KB, int VB>
+constexpr bool kTwoTiles = D <= 128 && (KB + VB) * (D / 64) <= 32;
+// Work-groups per CU that LDS and registers allow.
+constexpr int attend_occupancy(int d, int tile) {
+  return tile > 10240 ? (d == 256 ? 1 : 2) : tile <= 4864 && d <= 128 ? 4 : 2;
+}
+
+template <int D, int KB, int VB>
+__global__ __launch_bounds__(256, attend_occupancy(D, KvTile<D, KB, VB>::bytes)) void k_attend(
+    const AttendArgs a) {
   using T = KvTile<D, KB, VB>;
   constexpr int G = D / 64;
-  constexpr int kPad = 4;                // a row's pitch in LDS is not a multiple of the banks
-  __shared__ float red[kAttendWaves][kAttendRows][D + kPad];
+  constexpr bool staged = kStaged<D, KB, VB>;
+  constexpr int kRow = D + 4;            // a row's pitch in LDS is not a multiple of the banks
   __shared__ float rst[kAttendWaves][kAttendRows][2];
-  const int lane = lane_id(), wave = wave_id(), g = lane >> 4, n = lane & 15;
-  const uint32_t magic = vreg_const(kMagic);
-  const int hgs = a.kv_heads * a.rts;
-  const int64_t all = tiles_before(a, a.s.seqs) * hgs;
-  const int64_t share = tile_share(all, a.groups);
-  const int64_t from = blockIdx.x * share, to = min(from + share, all);
-  if (from >= to) return;
-  // the sequence that tile `from` belongs to
-  int b = 0, tiles = 0;
-  int64_t at = 0;                        // first tile of (b, head 0)
-  for (int base = 0; base < a.s.seqs; base += 64) {
-    const int t = base + lane < a.s.seqs ? seen_tiles(a, base + lane) : 0;
-    const int sum = scan64(t);
-    const uint64_t past = __ballot(at + (int64_t)sum * hgs > from);
-    if (past != 0) {
-      const int l = __builtin_ctzll(past);
-      b = base + l;
-      tiles = __builtin_amdgcn_readlane(t, l);
-      at += (int64_t)(__builtin_amdgcn_readlane(sum, l) - tiles) * hgs;
-      break;
-    }
-    at += (int64_t)__builtin_amdgcn_readlane(sum, 63) * hgs;
+  float* red;                            // [2][16][kRow]: sums of two waves
+  if constexpr (staged) {
+    static_assert(2 * kAttendRows * kRow * 4 <= kAttendWaves * T::bytes, "sums in the first stage");
+    red = reinterpret_cast<float*>(tile_stage<D, KB, VB, 0>());
+  } else {
+    __shared__ float own[2 * kAttendRows * kRow];
+    red = own;
   }
-  int hg = (int)((from - at) / tiles);
-  int64_t begin = at + (int64_t)hg * tiles;      // first tile of (b, hg)
-  int64_t pos = from;
-  while (pos < to) {
+  const int lane = lane_id(), wave = wave_id(), g = lane >> 4, n = lane & 15;
+  const MixConsts mix = mix_consts();
+  const int hgs = a.kv_heads * a.rts;
+  int b = 0, hg = 0, tiles = 0;
+  int64_t begin = 0, pos = 0, to = 0;    // first tile of (b, hg), own tiles
+  if (a.whole) {
+    b = blockIdx.x / hgs;
+    hg = blockIdx.x % hgs;
+    tiles = seen_tiles(a, b);
+    to = tiles;
+    if (tiles == 0) {
+      const int row0 = hg / a.rts * a.ratio + hg % a.rts * kAttendRows;
+      const int rows = min(a.ratio - hg % a.rts * kAttendRows, kAttendRows);
+      for (int i = threadIdx.x; i < rows * D; i += 256) {
+        const int64_t out = b * a.ldo + (int64_t)row0 * D + i;
+        if (a.o != nullptr) a.o[out] = 0.f;
+        if (a.o16 != nullptr) a.o16[out] = (f16)0.f;
+      }
+      if (a.lse != nullptr && threadIdx.x < (unsigned)rows)
+        a.lse[(int64_t)b * a.heads + row0 + threadIdx.x] = -__builtin_inff();
+      return;
+    }
+  } else {
+    // the sequence that this work-group's first tile belongs to
+    const int t0 = lane < a.s.seqs ? seen_tiles(a, lane) : 0;
+    const int sum0 = scan64(t0);
+    int64_t all = __builtin_amdgcn_readlane(sum0, 63);
+    for (int base = 64; base < a.s.seqs; base += 64) {
+      const int t = base + lane < a.s.seqs ? seen_tiles(a, base + lane) : 0;
+      all += __builtin_amdgcn_readlane(scan64(t), 63);
+    }
+    all *= hgs;
+    const int64_t share = tile_share(all, a.groups);
+    pos = blockIdx.x * share;
+    to = min(pos + share, all);
+    if (pos >= to) return;
+    for (int base = 0; base < a.s.seqs; base += 64) {
+      const int t = base == 0 ? t0 : base + lane < a.s.seqs ? seen_tiles(a, base + lane) : 0;
+      const int sum = base == 0 ? sum0 : scan64(t);
+      const uint64_t past = __ballot(begin + (int64_t)sum * hgs > pos);
+      if (past != 0) {
+        const int l = __builtin_ctzll(past);
+        b = base + l;
+        tiles = __builtin_amdgcn_readlane(t, l);
+        begin += (int64_t)(__builtin_amdgcn_readlane(sum, l) - tiles) * hgs;
+        break;
+      }
+      begin += (int64_t)__builtin_amdgcn_readlane(sum, 63) * hgs;
+    }
+    hg = (int)((pos - begin) / tiles);
+    begin += (int64_t)hg * tiles;
+  }
+  for (;;) {
     int lo, hi;
     seen_tokens(a, b, lo, hi);
     const int tile0 = lo / kKvTile;
@@ -350,16 +481,6 @@ __global__ __launch_bounds__(256) void k_attend(const AttendArgs a) {
     const int rows = min(a.ratio - row0, kAttendRows);
     const int first = tile0 + (int)(pos - begin);
     const int last = tile0 + (int)(min(to, begin + tiles) - begin);
-    // ---- this wave's tiles: first + wave, first + wave + 4, ...
-    const int qh = head * a.ratio + row0 + min(n, rows - 1);
-    f16x8 q[D / 32];
-    const f16* qp = a.q + b * a.ldq + (int64_t)qh * D;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const f16x8 z = {};
-      const f16x8 v = *(const f16x8*)(qp + (i / 2) * 64 + g * 16 + (i % 2) * 8);
-      q[i] = n < rows ? v : z;
-    }
     AttendState<D> st;
 #pragma unroll
     for (int c = 0; c < G; ++c)
@@ -369,25 +490,88 @@ __global__ __launch_bounds__(256) void k_attend(const AttendArgs a) {
     st.m = -1e30f;
     st.off = -1e30f;
     st.e = VB < 16 ? -14 : 0;
-    const int32_t* row = a.s.table + b * a.s.ld;
-    PageList pages{-64, 0};
-    for (int t = first + wave; t < last; t += kAttendWaves) {
-      const int pi = t >> a.s.page_log;
-      if (pi - pages.base >= 64) {
-        pages.base = pi;
-        pages.entry = pi + lane < a.s.width ? row[pi + lane] : -1;
+    // ---- this wave's tiles: first + wave, first + wave + 4, ...
+    int t = first + wave;
+    if (t < last) {
+      const int32_t* row = a.s.table + b * a.s.ld;
+      PageList pages{-64, 0};
+      // where tile t lies (somewhere, if its page is not there)
+      bool there[2];
+      auto place = [&](int t, bool& ok) {
+        const int pi = t >> a.s.page_log;
+        if (pi - pages.base >= 64) {
+          pages.base = pi;
+          pages.entry = pi + lane < a.s.width ? row[pi + lane] : -1;
+        }
+        const int page = __builtin_amdgcn_readlane(pages.entry, pi - pages.base);
+        ok = page >= 0 && page < a.s.pages;
+        return a.data + ((int64_t)(ok ? page : 0) * a.kv_heads + head) * a.head_bytes +
+               (t & ((1 << a.s.page_log) - 1)) * T::bytes;
+      };
+      const uint8_t* tp = place(t, there[0]);
+      KvRegs<D, KB, VB> one;
+      if constexpr (staged) stage_tile<D, KB, VB>(tp, tile_stage<D, KB, VB, 0>() + wave * T::bytes);
+      else one.load(tp);
+      f16x8 q[D / 32];
+      const f16* qp = a.q + b * a.ldq + (int64_t)(head * a.ratio + row0 + min(n, rows - 1)) * D;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const f16x8 z = {};
+        const f16x8 v = *(const f16x8*)(qp + (i / 2) * 64 + g * 16 + (i % 2) * 8);
+        q[i] = n < rows ? signed_by(v, a.flip) : z;
       }
-      const int page = __builtin_amdgcn_readlane(pages.entry, pi - pages.base);
-      if (page < 0 || page >= a.s.pages) continue;
-      const uint8_t* tp = a.data + ((int64_t)page * a.kv_heads + head) * a.head_bytes +
-                          (t & ((1 << a.s.page_log) - 1)) * T::bytes;
-      KvRegs<D, KB, VB> regs;
-      load_tile<D, KB, VB>(regs, tp);
-      const int p0 = t * kKvTile;
-      attend_tile<D, KB, VB>(st, regs, q, a.c, p0 < lo || p0 + kKvTile > hi, p0, lo, hi, magic);
+      auto use = [&](const auto& tile, int t) {
+        const int p0 = t * kKvTile;
+        attend_tile<D, KB, VB>(st, tile, q, a.c, p0 < lo || p0 + kKvTile > hi, p0, lo, hi, mix);
+      };
+      if constexpr (staged) {
+        uint8_t* const lds[2] = {tile_stage<D, KB, VB, 0>() + wave * T::bytes,
+                                 tile_stage<D, KB, VB, 1>() + wave * T::bytes};
+        for (;;) {
+          bool more = t + kAttendWaves < last;
+          if (more) {
+            stage_tile<D, KB, VB>(place(t + kAttendWaves, there[1]), lds[1]);
+            wait_loads<kTileLoads<D, KB, VB>>();
+          } else {
+            wait_loads<0>();
+          }
+          if (there[0]) use(KvStage<D, KB, VB>(lds[0]), t);
+          if (!more) break;
+          t += kAttendWaves;
+          more = t + kAttendWaves < last;
+          if (more) {
+            stage_tile<D, KB, VB>(place(t + kAttendWaves, there[0]), lds[0]);
+            wait_loads<kTileLoads<D, KB, VB>>();
+          } else {
+            wait_loads<0>();
+          }
+          if (there[1]) use(KvStage<D, KB, VB>(lds[1]), t);
+          if (!more) break;
+          t += kAttendWaves;
+        }
+      } else if constexpr (kTwoTiles<D, KB, VB>) {
+        KvRegs<D, KB, VB> two;
+        for (;;) {
+          two.load(place(min(t + kAttendWaves, last - 1), there[1]));
+          if (there[0]) use(one, t);
+          t += kAttendWaves;
+          if (t >= last) break;
+          one.load(place(min(t + kAttendWaves, last - 1), there[0]));
+          if (there[1]) use(two, t);
+          t += kAttendWaves;
+          if (t >= last) break;
+        }
+      } else {
+        for (;;) {
+          if (there[0]) use(one, t);
+          t += kAttendWaves;
+          if (t >= last) break;
+          one.load(place(t, there[0]));
+        }
+      }
     }
     st.l = sum16x32(st.l);
-    // ---- the waves' sums together
+    // ---- the waves' sums together: 2 and 3 to 0 and 1, 1 to 0
     if (g == 0) {
       rst[wave][n][0] = st.off;
       rst[wave][n][1] = st.l;
@@ -396,50 +580,81 @@ __global__ __launch_bounds__(256) void k_attend(const AttendArgs a) {
     float off = rst[0][n][0];
 #pragma unroll
     for (int w = 1; w < kAttendWaves; ++w) off = fmaxf(off, rst[w][n][0]);
+    float l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAttendWaves; ++w)
+      l += rst[w][n][1] * __builtin_amdgcn_exp2f(rst[w][n][0] - off);
     const float f = __builtin_amdgcn_exp2f(st.off - off);
+    // a lane's 16 dims of a group: 4 i + j
+    auto put = [&](float* to) {
+#pragma unroll
+      for (int c = 0; c < G; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *(f32x4*)(to + n * kRow + c * 64 + g * 16 + 4 * i) =
+              f32x4{st.o[c][0][i], st.o[c][1][i], st.o[c][2][i], st.o[c][3][i]};
+    };
+    auto add = [&](const float* from) {
+#pragma unroll
+      for (int c = 0; c < G; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 v = *(const f32x4*)(from + n * kRow + c * 64 + g * 16 + 4 * i);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) st.o[c][j][i] += v[j];
+        }
+    };
 #pragma unroll
     for (int c = 0; c < G; ++c)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) red[wave][n][c * 64 + g * 16 + 4 * i + j] = st.o[c][j][i] * f;
+      for (int j = 0; j < 4; ++j) st.o[c][j] *= f;
+    const int parts = min(last - first, kAttendWaves);       // waves that had tiles
+    float* const mine = red + (wave & 1) * kAttendRows * kRow;
+    if (wave >= 2 && wave < parts) put(mine);
     lds_barrier();
-    const bool cut_front = pos > begin, cut_back = to < begin + tiles;
-    const bool cut = cut_front || cut_back;
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (cut_front ? 0 : 1);
-    for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
-      const int r = i / (D / 4), d = i % (D / 4) * 4;
-      float m = rst[0][r][0];
+    if (wave + 2 < parts) add(mine);
+    if (wave == 1 && wave < parts) put(mine);
+    lds_barrier();
+    if (wave == 0) {
+      if (parts > 1) add(red + kAttendRows * kRow);
+      const bool cut_front = pos > begin, cut_back = to < begin + tiles;
+      if (n < rows) {
+        const int h = head * a.ratio + row0 + n;
+        if (cut_front || cut_back) {
+          const int64_t slot = (2 * (int64_t)blockIdx.x + (cut_front ? 0 : 1)) * a.rows + n;
 #pragma unroll
-      for (int w = 1; w < kAttendWaves; ++w) m = fmaxf(m, rst[w][r][0]);
-      float l = 0.f;
-      f32x4 v{};
+          for (int c = 0; c < G; ++c)
 #pragma unroll
-      for (int w = 0; w < kAttendWaves; ++w) {
-        l += rst[w][r][1] * __builtin_amdgcn_exp2f(rst[w][r][0] - m);
-        v += *(const f32x4*)&red[w][r][d];
-      }
-      const int h = head * a.ratio + row0 + r;
-      if (cut) {
-        *(f32x4*)(a.part + (slot * a.rows + r) * D + d) = v;
-        if (d == 0) {
-          a.stat[(slot * a.rows + r) * 2] = m;
-          a.stat[(slot * a.rows + r) * 2 + 1] = l;
+            for (int i = 0; i < 4; ++i)
+              *(f32x4*)(a.part + slot * D + c * 64 + g * 16 + 4 * i) =
+                  f32x4{st.o[c][0][i], st.o[c][1][i], st.o[c][2][i], st.o[c][3][i]};
+          if (g == 0) {
+            a.stat[slot * 2] = off;
+            a.stat[slot * 2 + 1] = l;
+          }
+        } else {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int64_t out = b * a.ldo + (int64_t)h * D + g * 16;
+#pragma unroll
+          for (int c = 0; c < G; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const f32x4 v{st.o[c][0][i] * inv, st.o[c][1][i] * inv, st.o[c][2][i] * inv,
+                            st.o[c][3][i] * inv};
+              if (a.o != nullptr) *(f32x4*)(a.o + out + c * 64 + 4 * i) = v;
+              if (a.o16 != nullptr) {
+                typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+                *(f16x4*)(a.o16 + out + c * 64 + 4 * i) =
+                    f16x4{(f16)v[0], (f16)v[1], (f16)v[2], (f16)v[3]};
+              }
+            }
+          if (a.lse != nullptr && g == 0)
+            a.lse[(int64_t)b * a.heads + h] =
+                l == 0.f ? -__builtin_inff() : (off + __builtin_log2f(l)) * 0.69314718055994531f;
         }
-      } else {
-        v *= l == 0.f ? 0.f : 1.f / l;
-        const int64_t out = b * a.ldo + (int64_t)h * D + d;
-        if (a.o != nullptr) *(f32x4*)(a.o + out) = v;
-        if (a.o16 != nullptr) {
-          typedef f16 f16x4 __attribute__((ext_vector_type(4)));
-          *(f16x4*)(a.o16 + out) = f16x4{(f16)v[0], (f16)v[1], (f16)v[2], (f16)v[3]};
-        }
-        if (a.lse != nullptr && d == 0)
-          a.lse[(int64_t)b * a.heads + h] =
-              l == 0.f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.69314718055994531f;
       }
     }
-    lds_barrier();                       // (the next segment writes red and rst again)
+    lds_barrier();                       // (the next segment writes red, its stage and rst again)
     pos = min(to, begin + tiles);
     if (pos >= to) break;
     begin += tiles;
@@ -451,67 +666,89 @@ __global__ __launch_bounds__(256) void k_attend(const AttendArgs a) {
 }
 
 // The parts of the sequences that more than one work-group dealt with, and rows without
-// tokens.  One work-group per (sequence, query head): its waves take the parts in turn.
+// tokens.  One work-group per (sequence, query head): a thread per part for its weight, then
+// D / 4 threads per part, 1024 / D of them at a time, eight loads of a thread in flight.
 template <int D>
 __global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a) {
-  constexpr int V = D / 64;              // dims per lane
-  __shared__ float red[4][D];
-  __shared__ float rst[4][2];
-  const int lane = lane_id(), wave = wave_id();
+  constexpr int kLanes = D / 4, kSubs = 256 / kLanes;
+  __shared__ float weight[kMaxParts];
+  __shared__ f32x4 red[kSubs][kLanes];
+  __shared__ float tops[4], sums[4];
+  const int lane = lane_id(), wave = wave_id(), tid = threadIdx.x;
   const int b = blockIdx.x, h = blockIdx.y;
   const int hgs = a.kv_heads * a.rts;
-  const int tiles = seen_tiles(a, b);
   const int kvh = h / a.ratio, r16 = h % a.ratio;
   const int hg = kvh * a.rts + r16 / kAttendRows, r = r16 % kAttendRows;
-  float o[V] = {}, l = 0.f, m = -1e30f;
+  int64_t before = 0, all = 0;
+  int tiles = 0;
+  for (int base = 0; base < a.s.seqs; base += 64) {
+    const int t = base + lane < a.s.seqs ? seen_tiles(a, base + lane) : 0;
+    const int sum = scan64(t);
+    if (b >= base && b < base + 64) {
+      tiles = __builtin_amdgcn_readlane(t, b - base);
+      before = all + __builtin_amdgcn_readlane(sum, b - base) - tiles;
+    }
+    all += __builtin_amdgcn_readlane(sum, 63);
+  }
+  f32x4 o{};
+  float l = 0.f, top = -1e30f;
+  const int sub = tid / kLanes, d = tid % kLanes;
   if (tiles > 0) {
-    const int64_t before = tiles_before(a, b), all = tiles_before(a, a.s.seqs) * hgs;
-    const int64_t share = tile_share(all, a.groups);
+    const int64_t share = tile_share(all * hgs, a.groups);
     const int64_t begin = before * hgs + (int64_t)hg * tiles, end = begin + tiles;
     const int64_t w0 = begin / share, w1 = (end - 1) / share;
     if (w0 == w1) return;                // one work-group had all of it
-    for (int64_t w = w0 + wave; w <= w1; w += 4) {
-      const int64_t at = (2 * w + (begin < w * share ? 0 : 1)) * a.rows + r;
-      const float pm = a.stat[at * 2], pl = a.stat[at * 2 + 1];
-      const float nm = fmaxf(m, pm);
-      const float f = __builtin_amdgcn_exp2f(m - nm), pf = __builtin_amdgcn_exp2f(pm - nm);
-      l = l * f + pl * pf;
-      m = nm;
+    const int parts = (int)(w1 - w0) + 1;
+    // (the first work-group's range begins with or before the sequence: its second place)
+    auto place = [&](int i) { return (2 * (w0 + i) + (i == 0)) * a.rows + r; };
+    float pm[kMaxParts / 256], pl[kMaxParts / 256];
 #pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = o[i] * f + a.part[at * D + lane + 64 * i] * pf;
+    for (int j = 0; j < kMaxParts / 256; ++j) {
+      const int i = j * 256 + tid;
+      pm[j] = i < parts ? a.stat[place(i) * 2] : -1e30f;
+      pl[j] = i < parts ? a.stat[place(i) * 2 + 1] : 0.f;
+      top = fmaxf(top, pm[j]);
     }
-    if (lane == 0) {
-      rst[wave][0] = m;
-      rst[wave][1] = l;
+    for (int k = 32; k > 0; k /= 2) top = fmaxf(top, __shfl_xor(top, k));
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, tops[w]);
+#pragma unroll
+    for (int j = 0; j < kMaxParts / 256; ++j) {
+      const int i = j * 256 + tid;
+      const float f = __builtin_amdgcn_exp2f(pm[j] - top);
+      if (i < parts) weight[i] = f;
+      l += pl[j] * f;
     }
+    for (int k = 32; k > 0; k /= 2) l += __shfl_xor(l, k);
+    if (lane == 0) sums[wave] = l;
+    __syncthreads();
+    l = sums[0] + sums[1] + sums[2] + sums[3];
+    int i = sub;
+    for (; i + 7 * kSubs < parts; i += 8 * kSubs) {
+      f32x4 v[8];
 #pragma unroll
-    for (int i = 0; i < V; ++i) red[wave][lane + 64 * i] = o[i];
-  }
-  __syncthreads();
-  if (wave != 0) return;
-  if (tiles > 0) {
-    float top = rst[0][0];
-    for (int w = 1; w < 4; ++w) top = fmaxf(top, rst[w][0]);
-    l = 0.f;
-    for (int i = 0; i < V; ++i) o[i] = 0.f;
-    for (int w = 0; w < 4; ++w) {
-      const float f = __builtin_amdgcn_exp2f(rst[w][0] - top);
-      l += rst[w][1] * f;
+      for (int j = 0; j < 8; ++j) v[j] = *(const f32x4*)(a.part + place(i + j * kSubs) * D + d * 4);
 #pragma unroll
-      for (int i = 0; i < V; ++i) o[i] += red[w][lane + 64 * i] * f;
+      for (int j = 0; j < 8; ++j) o += v[j] * weight[i + j * kSubs];
     }
-    m = top;
+    for (; i < parts; i += kSubs) o += *(const f32x4*)(a.part + place(i) * D + d * 4) * weight[i];
+    red[sub][d] = o;
+    __syncthreads();
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int64_t out = b * a.ldo + (int64_t)h * D + lane + 64 * i;
-    if (a.o != nullptr) a.o[out] = o[i] * inv;
-    if (a.o16 != nullptr) a.o16[out] = (f16)(o[i] * inv);
+  if (sub != 0) return;
+  if (tiles > 0)
+    for (int i = 1; i < kSubs; ++i) o += red[i][d];
+  o *= l == 0.f ? 0.f : 1.f / l;
+  const int64_t out = b * a.ldo + (int64_t)h * D + d * 4;
+  if (a.o != nullptr) *(f32x4*)(a.o + out) = o;
+  if (a.o16 != nullptr) {
+    typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+    *(f16x4*)(a.o16 + out) = f16x4{(f16)o[0], (f16)o[1], (f16)o[2], (f16)o[3]};
   }
-  if (a.lse != nullptr && lane == 0)
+  if (a.lse != nullptr && d == 0)
     a.lse[(int64_t)b * a.heads + h] =
-        l == 0.f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.69314718055994531f;
+        l == 0.f ? -__builtin_inff() : (top + __builtin_log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace qlin

@@ -17,6 +17,7 @@ constexpr int kMaxSeqs = 1 << 16;
 constexpr int kMaxKvHeads = 256;
 constexpr int kMaxHeads = 1024;
 constexpr int64_t kMaxRoom = 1 << 27;      // tokens of a table row
+constexpr float kMaxScale = 1 << 20;
 
 bool kv_dim(int d) { return d == 64 || d == 128 || d == 256; }
 bool kv_page_size(int p) { return p == 32 || p == 64 || p == 128 || p == 256; }
@@ -118,6 +119,10 @@ struct Attend {
   static void run(const AttendArgs& a, int d, hipStream_t st) { launch_attend<KB, VB>(a, d, st); }
 };
 
+// Sequences of tables up to this length are not split: a work-group has all of one, and
+// nothing is joined.
+constexpr int64_t kWholeTokens = 1024;
+
 struct AttendPlan {
   int rows, rts, groups;
   int64_t part, stat, bytes;     // offsets in the workspace, and its size
@@ -131,7 +136,8 @@ AttendPlan attend_plan(const qlin_kv_cache* c, const qlin_kv_seqs* s, int heads)
   const int64_t most = (int64_t)s->seqs * c->kv_heads * p.rts *
                        ((int64_t)s->width * (c->page / kKvTile));
   const int64_t groups = (most + kAttendWaves - 1) / kAttendWaves;
-  p.groups = (int)(groups < kAttendGroups ? groups : kAttendGroups);
+  const int most_groups = attend_groups(c->head_dim, c->k_bits, c->v_bits);
+  p.groups = (int)(groups < most_groups ? groups : most_groups);
   p.part = kCounterBytes;
   p.stat = p.part + 2 * (int64_t)p.groups * p.rows * c->head_dim * 4;
   p.bytes = p.stat + 2 * (int64_t)p.groups * p.rows * 2 * 4;
@@ -244,7 +250,7 @@ qlin_status qlin_kv_attention(const qlin_kv_cache* cache, const qlin_kv_seqs* se
   if (st != QLIN_OK) return st;
   const int64_t row = (int64_t)heads * cache->head_dim;
   if (ld_q < row || ld_o < row || window < 0) return QLIN_ERR_SHAPE;
-  if (!isfinite(scale)) return QLIN_ERR_FORMAT;
+  if (!(fabsf(scale) <= kMaxScale)) return QLIN_ERR_FORMAT;
   if (ld_q % 8 != 0 || ld_o % 8 != 0) return QLIN_ERR_ALIGN;
   if (seqs->seqs == 0) return QLIN_OK;
   st = check_pointers(cache, seqs);
@@ -289,7 +295,10 @@ qlin_status qlin_kv_attention(const qlin_kv_cache* cache, const qlin_kv_seqs* se
   a.rts = p.rts;
   a.window = window;
   a.groups = p.groups;
-  a.c = scale * 1.44269504088896341f;
+  a.whole = (int64_t)seqs->width * cache->page <= kWholeTokens;
+  // (a factor of 0 would make masked scores no numbers: 2^-100 leaves every score 0 as well)
+  a.flip = scale < 0.f ? 0x80008000u : 0u;
+  a.c = fmaxf(fabsf(scale) * 1.44269504088896341f, 0x1p-100f);
   by_bits<Attend>(cache, a, cache->head_dim, stream);
   return hip_status(hipGetLastError());
 }

@@ -32,8 +32,9 @@ template void launch_kv_read<QLIN_INST_KB, QLIN_INST_VB>(const KvReadArgs&, int,
 #else
 template <int D, int KB, int VB>
 void launch_attend_dim(const AttendArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((k_attend<D, KB, VB>), dim3(a.groups), dim3(256), 0, st, a);
-  hipLaunchKernelGGL((k_attend_join<D>), dim3(a.s.seqs, a.heads), dim3(256), 0, st, a);
+  const int groups = a.whole ? a.s.seqs * a.kv_heads * a.rts : a.groups;
+  hipLaunchKernelGGL((k_attend<D, KB, VB>), dim3(groups), dim3(256), 0, st, a);
+  if (!a.whole) hipLaunchKernelGGL((k_attend_join<D>), dim3(a.s.seqs, a.heads), dim3(256), 0, st, a);
 }
 
 template <int KB, int VB>

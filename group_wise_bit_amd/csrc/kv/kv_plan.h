@@ -6,9 +6,11 @@
 
 namespace qlin {
 
-// Work-groups of the attention: as many as the chip holds at once, or one for
-// every four tiles if there cannot be that many.
-constexpr int kAttendGroups = 512;
+// Work-groups of the attention: as many as the chip holds at once (one for every
+// four tiles if there cannot be that many).
+inline int attend_groups(int d, int kb, int vb) {
+  return 256 * attend_occupancy(d, kv_tile_bytes(d, kb, vb));
+}
 
 template <int KB, int VB>
 void launch_kv_store(const KvStoreArgs& a, int d, dim3 grid, hipStream_t st);

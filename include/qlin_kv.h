@@ -126,7 +126,7 @@ qlin_status qlin_kv_read(const qlin_kv_cache* cache, const qlin_kv_seqs* seqs,
  * workspace: scratch of qlin_kv_attention_workspace_bytes (or QLIN_ERR_WORKSPACE; 0
  * is returned there for invalid arguments); its first 65536 bytes are left as they
  * are, so that it may be the buffer of the other calls.  Calls that can run at the same time need
- * workspaces of their own.  heads <= 1024; scale finite.
+ * workspaces of their own.  heads <= 1024; |scale| <= 2^20.
  */
 int64_t qlin_kv_attention_workspace_bytes(const qlin_kv_cache* cache, const qlin_kv_seqs* seqs,
                                           int32_t heads);
