@@ -43,10 +43,16 @@ __device__ __forceinline__ int seen_tiles(const AttendArgs& a, int b) {
   return hi > lo ? (hi + kKvTile - 1) / kKvTile - lo / kKvTile : 0;
 }
 
-// Every work-group takes `share` tiles of the list [sequence][head][row block][tile].
-__device__ __forceinline__ int64_t tile_share(int64_t all, int groups) {
-  const int64_t s = (all + groups - 1) / groups;
-  return s < kAttendWaves ? kAttendWaves : s;
+// Every work-group takes `share` units of the list [sequence][head][row block][units]:
+// kStartUnits for the start of a row block's tiles, then one for each of them.
+constexpr int kStartUnits = 8;
+__device__ __forceinline__ int seen_units(const AttendArgs& a, int b) {
+  const int tiles = seen_tiles(a, b);
+  return tiles > 0 ? tiles + kStartUnits : 0;
+}
+__device__ __forceinline__ int64_t unit_share(int64_t all, int groups) {
+  const int64_t s = (all + groups - 1) / groups, least = kStartUnits + kAttendWaves;
+  return s < least ? least : s;
 }
 
 // Where a wave has a tile: in registers,
@@ -424,14 +430,14 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KvTile<D, KB, VB>::bytes))
   const int lane = lane_id(), wave = wave_id(), g = lane >> 4, n = lane & 15;
   const MixConsts mix = mix_consts();
   const int hgs = a.kv_heads * a.rts;
-  int b = 0, hg = 0, tiles = 0;
-  int64_t begin = 0, pos = 0, to = 0;    // first tile of (b, hg), own tiles
+  int b = 0, hg = 0, units = 0;          // of (b, hg)
+  int64_t begin = 0, pos = 0, to = 0;    // where these begin, and the work-group's own
   if (a.whole) {
     b = blockIdx.x / hgs;
     hg = blockIdx.x % hgs;
-    tiles = seen_tiles(a, b);
-    to = tiles;
-    if (tiles == 0) {
+    units = seen_units(a, b);
+    to = units;
+    if (units == 0) {
       const int row0 = hg / a.rts * a.ratio + hg % a.rts * kAttendRows;
       const int rows = min(a.ratio - hg % a.rts * kAttendRows, kAttendRows);
       for (int i = threadIdx.x; i < rows * D; i += 256) {
@@ -444,34 +450,34 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KvTile<D, KB, VB>::bytes))
       return;
     }
   } else {
-    // the sequence that this work-group's first tile belongs to
-    const int t0 = lane < a.s.seqs ? seen_tiles(a, lane) : 0;
+    // the sequence that this work-group's first unit belongs to
+    const int t0 = lane < a.s.seqs ? seen_units(a, lane) : 0;
     const int sum0 = scan64(t0);
     int64_t all = __builtin_amdgcn_readlane(sum0, 63);
     for (int base = 64; base < a.s.seqs; base += 64) {
-      const int t = base + lane < a.s.seqs ? seen_tiles(a, base + lane) : 0;
+      const int t = base + lane < a.s.seqs ? seen_units(a, base + lane) : 0;
       all += __builtin_amdgcn_readlane(scan64(t), 63);
     }
     all *= hgs;
-    const int64_t share = tile_share(all, a.groups);
+    const int64_t share = unit_share(all, a.groups);
     pos = blockIdx.x * share;
     to = min(pos + share, all);
     if (pos >= to) return;
     for (int base = 0; base < a.s.seqs; base += 64) {
-      const int t = base == 0 ? t0 : base + lane < a.s.seqs ? seen_tiles(a, base + lane) : 0;
+      const int t = base == 0 ? t0 : base + lane < a.s.seqs ? seen_units(a, base + lane) : 0;
       const int sum = base == 0 ? sum0 : scan64(t);
       const uint64_t past = __ballot(begin + (int64_t)sum * hgs > pos);
       if (past != 0) {
         const int l = __builtin_ctzll(past);
         b = base + l;
-        tiles = __builtin_amdgcn_readlane(t, l);
-        begin += (int64_t)(__builtin_amdgcn_readlane(sum, l) - tiles) * hgs;
+        units = __builtin_amdgcn_readlane(t, l);
+        begin += (int64_t)(__builtin_amdgcn_readlane(sum, l) - units) * hgs;
         break;
       }
       begin += (int64_t)__builtin_amdgcn_readlane(sum, 63) * hgs;
     }
-    hg = (int)((pos - begin) / tiles);
-    begin += (int64_t)hg * tiles;
+    hg = (int)((pos - begin) / units);
+    begin += (int64_t)hg * units;
   }
   for (;;) {
     int lo, hi;
@@ -479,8 +485,11 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KvTile<D, KB, VB>::bytes))
     const int tile0 = lo / kKvTile;
     const int head = hg / a.rts, row0 = (hg % a.rts) * kAttendRows;
     const int rows = min(a.ratio - row0, kAttendRows);
-    const int first = tile0 + (int)(pos - begin);
-    const int last = tile0 + (int)(min(to, begin + tiles) - begin);
+    // own tiles of the row block (none, if the range ends with the start's units)
+    const int64_t tiles0 = begin + kStartUnits;
+    const int first = tile0 + (int)(max(pos, tiles0) - tiles0);
+    const int last = tile0 + (int)(min(to, begin + units) - tiles0);
+    if (first >= last) break;
     AttendState<D> st;
 #pragma unroll
     for (int c = 0; c < G; ++c)
@@ -617,7 +626,7 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KvTile<D, KB, VB>::bytes))
     lds_barrier();
     if (wave == 0) {
       if (parts > 1) add(red + kAttendRows * kRow);
-      const bool cut_front = pos > begin, cut_back = to < begin + tiles;
+      const bool cut_front = pos > tiles0, cut_back = to < begin + units;
       if (n < rows) {
         const int h = head * a.ratio + row0 + n;
         if (cut_front || cut_back) {
@@ -655,12 +664,12 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KvTile<D, KB, VB>::bytes))
       }
     }
     lds_barrier();                       // (the next segment writes red, its stage and rst again)
-    pos = min(to, begin + tiles);
+    pos = begin + units;
     if (pos >= to) break;
-    begin += tiles;
+    begin = pos;
     if (++hg == hgs) {
       hg = 0;
-      do { tiles = seen_tiles(a, ++b); } while (tiles == 0);
+      do { units = seen_units(a, ++b); } while (units == 0);
     }
   }
 }
@@ -680,26 +689,26 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a) {
   const int kvh = h / a.ratio, r16 = h % a.ratio;
   const int hg = kvh * a.rts + r16 / kAttendRows, r = r16 % kAttendRows;
   int64_t before = 0, all = 0;
-  int tiles = 0;
+  int units = 0;
   for (int base = 0; base < a.s.seqs; base += 64) {
-    const int t = base + lane < a.s.seqs ? seen_tiles(a, base + lane) : 0;
+    const int t = base + lane < a.s.seqs ? seen_units(a, base + lane) : 0;
     const int sum = scan64(t);
     if (b >= base && b < base + 64) {
-      tiles = __builtin_amdgcn_readlane(t, b - base);
-      before = all + __builtin_amdgcn_readlane(sum, b - base) - tiles;
+      units = __builtin_amdgcn_readlane(t, b - base);
+      before = all + __builtin_amdgcn_readlane(sum, b - base) - units;
     }
     all += __builtin_amdgcn_readlane(sum, 63);
   }
   f32x4 o{};
   float l = 0.f, top = -1e30f;
   const int sub = tid / kLanes, d = tid % kLanes;
-  if (tiles > 0) {
-    const int64_t share = tile_share(all * hgs, a.groups);
-    const int64_t begin = before * hgs + (int64_t)hg * tiles, end = begin + tiles;
-    const int64_t w0 = begin / share, w1 = (end - 1) / share;
+  if (units > 0) {
+    const int64_t share = unit_share(all * hgs, a.groups);
+    const int64_t begin = before * hgs + (int64_t)hg * units, end = begin + units;
+    const int64_t w0 = (begin + kStartUnits) / share, w1 = (end - 1) / share;
     if (w0 == w1) return;                // one work-group had all of it
     const int parts = (int)(w1 - w0) + 1;
-    // (the first work-group's range begins with or before the sequence: its second place)
+    // (the first work-group's range begins before or with the tiles: its second place)
     auto place = [&](int i) { return (2 * (w0 + i) + (i == 0)) * a.rows + r; };
     float pm[kMaxParts / 256], pl[kMaxParts / 256];
 #pragma unroll
@@ -737,7 +746,7 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a) {
     __syncthreads();
   }
   if (sub != 0) return;
-  if (tiles > 0)
+  if (units > 0)
     for (int i = 1; i < kSubs; ++i) o += red[i][d];
   o *= l == 0.f ? 0.f : 1.f / l;
   const int64_t out = b * a.ldo + (int64_t)h * D + d * 4;
