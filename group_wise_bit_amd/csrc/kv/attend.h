@@ -176,8 +176,12 @@ __device__ __forceinline__ MixConsts mix_consts() {
 }
 
 __device__ __forceinline__ float max16x32(float v) {     // over lanes l, l ^ 16, l ^ 32, l ^ 48
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+  const uint32_t x = __builtin_bit_cast(uint32_t, v);
+  const auto a = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  v = fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
+  const uint32_t y = __builtin_bit_cast(uint32_t, v);
+  const auto b = __builtin_amdgcn_permlane16_swap(y, y, false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
 }
 __device__ __forceinline__ float sum16x32(float v) {
   v += __shfl_xor(v, 16);
@@ -300,6 +304,14 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const Tile& t,
       }
     }
   }
+  // values are read from LDS before P is known, where there are registers for them
+  constexpr int kVUnits = VB * G / 4;
+  constexpr bool kEarly = kVUnits <= 4;
+  u32x4 early[kEarly ? kVUnits : 1];
+  if constexpr (kEarly) {
+#pragma unroll
+    for (int i = 0; i < kVUnits; ++i) early[i] = t.v_unit(i);
+  }
   float mx = x[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i]);
@@ -372,7 +384,11 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const Tile& t,
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       union { f16x8 v; f16x2 p[4]; } f;
-      if (j % (16 / VB) == 0) vu = t.v_unit(cg * (VB / 4) + j / (16 / VB));
+      if (j % (16 / VB) == 0) {
+        const int unit = cg * (VB / 4) + j / (16 / VB);
+        if constexpr (kEarly) vu = early[unit];
+        else vu = t.v_unit(unit);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (VB == 4) {

@@ -219,12 +219,22 @@ __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
   __syncthreads();
   double m = 0.;
   uint32_t q = 0;
-  for (int s = 0; s < a.slices; ++s) {
-    const int d = k - shift[s];
-    if (d >= 0) {
-      m += a.cum_mass[(at + s) * kBins + d] * factor[s];
-      q += a.cum_count[(at + s) * kBins + d];
+  for (int s0 = 0; s0 < a.slices; s0 += 8) {
+    double cm[8];
+    uint32_t cq[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int s = min(s0 + j, a.slices - 1), d = max(k - shift[s], 0);
+      cm[j] = a.cum_mass[(at + s) * kBins + d];
+      cq[j] = a.cum_count[(at + s) * kBins + d];
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      // (a slice whose bins all lie below was not written: what is there is not used)
+      if (s0 + j < a.slices && k >= shift[s0 + j]) {
+        m += cm[j] * factor[s0 + j];
+        q += cq[j];
+      }
   }
   mass[k] = m;
   count[k] = q;
@@ -377,33 +387,94 @@ __device__ __forceinline__ void sort_keys(uint64_t* keys, int size) {
   }
 }
 
+// The gathered tokens are sorted into 1024 parts of their range, by t: bins a .. z share kMainParts
+// of them, the bin e has the rest.  Counts and masses of the parts (in steps of 2^-34
+// of bin a's / e's unit, the count from bit 50 on) tell where a cut lies; only the tokens of that part
+// are put in order.
+constexpr int kParts = kPickThreads;
+constexpr int kMainParts = 896;
+constexpr int kPartCount = 50;
+
 struct PickShared {
-  uint64_t keys[kListMax];
-  double sums[kListMax];
-  SampleShared alone;
+  uint64_t keys[kListMax];                   // a part's tokens in order
+  unsigned long long part[kParts];           // sums up to a part
+  unsigned long long slice_mass[kSlices];
   double wave[kSampleWaves];
+  uint64_t scan[kSampleWaves];
   double before, target, total;
-  int slice, count[3];
+  int slice, count[3], size, at, rank;
+  SampleShared alone;
 };
 
-// Inclusive sums of v[0 .. n) in place, each thread's kPickPer (or fewer) in a row.
-__device__ __forceinline__ void sum_list(double* v, double* wave, int n) {
-  const int per = (n + kPickThreads - 1) / kPickThreads;
-  const int i0 = threadIdx.x * per;
+struct PickToken {
+  float l;
+  uint32_t index;
+  int part;                                  // -1: no token
+  uint64_t steps;
+};
+
+// The tokens of a part in order: sh.keys[0 .. sh.size).
+__device__ __forceinline__ void order_part(PickShared& sh, const PickToken (&t)[kPickPer], int part) {
+  if (threadIdx.x == 0) sh.size = 0;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPickPer; ++j)
+    if (t[j].part == part) sh.keys[atomicAdd(&sh.size, 1)] = order_key(t[j].l, t[j].index);
+  __syncthreads();
+  const int n = sh.size;
+  int size = 64;
+  while (size < n) size *= 2;
+  for (int i = n + threadIdx.x; i < size; i += kPickThreads) sh.keys[i] = ~0ull;
+  __syncthreads();
+  sort_keys(sh.keys, size);
+}
+
+// The first part whose sum (counts or masses, from `from` on) reaches `need`; kParts: none.
+template <typename F>
+__device__ __forceinline__ int first_part(PickShared& sh, int from, int to, F reaches) {
+  const int i = threadIdx.x;
+  if (i == 0) sh.at = kParts;
+  __syncthreads();
+  if (i >= from && i < to && reaches(sh.part[i]) && (i == from || !reaches(sh.part[i - 1]))) sh.at = i;
+  __syncthreads();
+  return sh.at;
+}
+
+// Mass of the first `rank` ordered tokens, in the units of list_mass.
+__device__ __forceinline__ double mass_of_first(PickShared& sh, int rank, double f, BinScale c) {
   double s = 0.;
-  for (int i = 0; i < per; ++i)
-    if (i0 + i < n) s += v[i0 + i];
-  const double up = wave_scan(s);
-  if (lane_id() == 63) wave[wave_id()] = up;
+  for (int i = threadIdx.x; i < rank; i += kPickThreads) s += list_mass(key_logit(sh.keys[i]), f, c);
+  for (int d = 32; d > 0; d /= 2) s += __shfl_xor(s, d);
+  if (lane_id() == 0) sh.wave[wave_id()] = s;
   __syncthreads();
-  double run = up - s;
-  for (int w = 0; w < wave_id(); ++w) run += wave[w];
-  for (int i = 0; i < per; ++i)
-    if (i0 + i < n) {
-      run += v[i0 + i];
-      v[i0 + i] = run;
+  s = 0.;
+  for (int w = 0; w < kSampleWaves; ++w) s += sh.wave[w];
+  __syncthreads();
+  return s;
+}
+
+// How many of the ordered tokens it takes until `sum` and their masses reach `target` (all of
+// them if they do not; 1 at least).
+__device__ __forceinline__ int first_to_reach(PickShared& sh, double sum, double target, double f,
+                                              BinScale c) {
+  const int n = sh.size, wave = wave_id();
+  if (threadIdx.x == 0) sh.rank = n > 0 ? n : 1;
+  __syncthreads();
+  for (int base = 0; base < n; base += kPickThreads) {
+    const int i = base + threadIdx.x;
+    const double up = wave_scan(i < n ? list_mass(key_logit(sh.keys[i]), f, c) : 0.);
+    if (lane_id() == 63) sh.wave[wave] = up;
+    __syncthreads();
+    double run = sum + up;
+    for (int w = 0; w < kSampleWaves; ++w) {
+      if (w < wave) run += sh.wave[w];
+      sum += sh.wave[w];
     }
-  __syncthreads();
+    if (i < n && run >= target) atomicMin(&sh.rank, i + 1);
+    __syncthreads();
+    if (sum >= target) break;
+  }
+  return sh.rank;
 }
 
 __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a) {
@@ -442,63 +513,123 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
   const int n = p.n, main = p.main;
   const uint2* list = a.list + (int64_t)r * kListMax;
   uint64_t cut = 0;                            // keys up to it are kept
+  for (int i = threadIdx.x; i < kSlices; i += kPickThreads) sh.slice_mass[i] = 0;
+  constexpr uint64_t kMassMask = (1ull << kPartCount) - 1;
+  const double unit = p.a < kBins ? exp(-(double)p.a * (1. / kBinScale)) : 0.;   // of bin a
+  const double to_mass = unit * (1. / (double)(1ull << kMassStep));
   if (n > 0) {
-    int size = 64;
-    while (size < n) size *= 2;
-    for (int i = threadIdx.x; i < size; i += kPickThreads) {
-      const uint2 t = i < n ? list[i] : make_uint2(0, 0);
-      sh.keys[i] = i < n ? order_key(__builtin_bit_cast(float, t.y), t.x) : ~0ull;
+    PickToken t[kPickPer];
+    sh.part[threadIdx.x] = 0;
+    const double unit_e = p.e >= 0 ? exp(-(double)p.e * (1. / kBinScale)) : 0.;
+#pragma unroll
+    for (int j = 0; j < kPickPer; ++j) {
+      const int i = j * kPickThreads + threadIdx.x;
+      const uint2 w = i < n ? list[i] : make_uint2(0, 0);
+      t[j].l = __builtin_bit_cast(float, w.y);
+      t[j].index = w.x;
+      t[j].part = i < n ? 0 : -1;
     }
-    if (threadIdx.x < 3) sh.count[threadIdx.x] = 0;
     __syncthreads();
-    sort_keys(sh.keys, size);
-    for (int i = threadIdx.x; i < n; i += kPickThreads)
-      sh.sums[i] = list_mass(key_logit(sh.keys[i]), f, c);
+    const double scale = (double)kMainParts / (double)(p.z + 1 - p.a);
+#pragma unroll
+    for (int j = 0; j < kPickPer; ++j) {
+      if (t[j].part < 0) continue;
+      const double ld = (double)t[j].l, hi = ld * c.hi, fl = __builtin_floor(hi);
+      const double x = hi - fl + t_low(ld, hi, c);              // in the bin, about 0 .. 1
+      const int k = (int)(f - fl);
+      const bool extra = k > p.z;
+      const double y = 1. - __builtin_fmin(__builtin_fmax(x, 0.), 1.);
+      t[j].part = extra ? kMainParts + min((int)(y * (kParts - kMainParts)), kParts - kMainParts - 1)
+                        : min((int)(((double)(k - p.a) + y) * scale), kMainParts - 1);
+      const double in_bin = bin_mass(x - 0.5, kMassOne) - (kMassOne - 1.);
+      const double rel = extra || k == p.a ? in_bin : in_bin * exp((double)(p.a - k) * (1. / kBinScale));
+      t[j].steps = (uint64_t)__builtin_rint(rel * (double)(1ull << kMassStep));
+      atomicAdd(&sh.part[t[j].part], (unsigned long long)(t[j].steps | 1ull << kPartCount));
+    }
     __syncthreads();
-    sum_list(sh.sums, sh.wave, n);
+    // sums up to a part; the bin e's begin anew
+    {
+      const int i = threadIdx.x;
+      uint64_t v = sh.part[i];
+      for (int d = 1; d < 64; d *= 2) {
+        const uint64_t o = shfl_up64(v, d);
+        if (lane >= d) v += o;
+      }
+      if (lane == 63) sh.scan[wave_id()] = v;
+      __syncthreads();
+      static_assert(kMainParts % 64 == 0, "whole waves");
+      for (int w = i >= kMainParts ? kMainParts / 64 : 0; w < wave_id(); ++w) v += sh.scan[w];
+      __syncthreads();
+      sh.part[i] = v;
+      __syncthreads();
+    }
+    auto count_to = [&](int part, int from) { return part > from ? (int)(sh.part[part - 1] >> kPartCount) : 0; };
+    auto mass_to = [&](int part, int from) { return part > from ? (double)(sh.part[part - 1] & kMassMask) : 0.; };
+    // tokens of a .. z that are kept: the first `kept` of them in order
     int kept = p.k_main;
+    int held = -1;                             // part of a .. z that sh.keys holds
+    auto rank_of = [&](int want) {             // the want-th token is sh.keys[rank_of(want) - 1]
+      if (held < 0 || want <= count_to(held, 0) || want > count_to(held, 0) + sh.size) {
+        held = first_part(sh, 0, kMainParts, [&](uint64_t v) { return (int)(v >> kPartCount) >= want; });
+        order_part(sh, t, held);
+      }
+      return want - count_to(held, 0);
+    };
     if (set.p < 1.f) {
       double mass_k = p.mass_k;
-      if (p.e >= 0) mass_k += sh.sums[main + p.k_extra - 1] - (main > 0 ? sh.sums[main - 1] : 0.);
-      else if (mass_k < 0.) mass_k = p.mass_a + sh.sums[p.k_main - 1];
+      if (p.e >= 0) {
+        const int pe = first_part(sh, kMainParts, kParts,
+                                  [&](uint64_t v) { return (int)(v >> kPartCount) >= p.k_extra; });
+        order_part(sh, t, pe);
+        mass_k += mass_to(pe, kMainParts) * unit_e * (1. / (double)(1ull << kMassStep)) +
+                  mass_of_first(sh, p.k_extra - count_to(pe, kMainParts), f, c);
+      } else if (mass_k < 0.) {
+        const int rank = rank_of(p.k_main);
+        mass_k = p.mass_a + mass_to(held, 0) * to_mass + mass_of_first(sh, rank, f, c);
+      }
+      // the token with which the sum reaches the target (by rounding there may be none: all)
       const double target = (double)set.p * mass_k;
-      int less = 0;
-      for (int i = threadIdx.x; i < main; i += kPickThreads) less += p.mass_a + sh.sums[i] < target;
-      if (less) atomicAdd(&sh.count[0], less);
+      const int pp = first_part(sh, 0, kMainParts, [&](uint64_t v) {
+        return p.mass_a + (double)(v & kMassMask) * to_mass >= target; });
+      if (pp < kParts && count_to(pp, 0) < kept) {
+        if (held != pp) order_part(sh, t, pp);
+        held = pp;
+        kept = min(kept, count_to(pp, 0) + first_to_reach(sh, p.mass_a + mass_to(pp, 0) * to_mass,
+                                                          target, f, c));
+      }
     }
     if (set.mp > 0.f) {
       const double top_hi = (double)p.top * c.hi, top_lo = t_low((double)p.top, top_hi, c);
       int pass = 0;
-      for (int i = threadIdx.x; i < main; i += kPickThreads) {
-        const float l = key_logit(sh.keys[i]);
-        const double hi = (double)l * c.hi;
-        const double e = (hi - top_hi + (t_low((double)l, hi, c) - top_lo)) * (1. / kBinScale);
-        pass += l == p.top || exp(e) >= (double)set.mp;
+#pragma unroll
+      for (int j = 0; j < kPickPer; ++j) {
+        if (t[j].part < 0 || t[j].part >= kMainParts) continue;
+        const double hi = (double)t[j].l * c.hi;
+        const double e = (hi - top_hi + (t_low((double)t[j].l, hi, c) - top_lo)) * (1. / kBinScale);
+        pass += t[j].l == p.top || exp(e) >= (double)set.mp;
       }
-      if (pass) atomicAdd(&sh.count[1], pass);
+      for (int d = 32; d > 0; d /= 2) pass += __shfl_xor(pass, d);
+      if (threadIdx.x == 0) sh.count[0] = 0;
+      __syncthreads();
+      if (lane == 0 && pass) atomicAdd(&sh.count[0], pass);
+      __syncthreads();
+      kept = min(kept, sh.count[0]);
     }
+    if (kept >= main) cut = ~0ull;             // all of a .. z
+    else if (kept > 0) cut = sh.keys[rank_of(kept) - 1];
     __syncthreads();
-    if (set.p < 1.f) kept = min(kept, sh.count[0] + 1);
-    if (set.mp > 0.f) kept = min(kept, sh.count[1]);
-    cut = kept > 0 ? sh.keys[kept - 1] : 0;
-    __syncthreads();
-    // the kept ones' masses in the order of the vocabulary
-    for (int i = threadIdx.x; i < n; i += kPickThreads) {
-      const uint2 t = list[i];
-      const float l = __builtin_bit_cast(float, t.y);
-      sh.sums[i] = kept > 0 && order_key(l, t.x) <= cut ? list_mass(l, f, c) : 0.;
-    }
-    __syncthreads();
-    sum_list(sh.sums, sh.wave, n);
-    if (kept == 0) cut = 0;
+    // the kept ones' masses, slice by slice
+#pragma unroll
+    for (int j = 0; j < kPickPer; ++j)
+      if (t[j].part >= 0 && t[j].part < kMainParts && order_key(t[j].l, t[j].index) <= cut)
+        atomicAdd(&sh.slice_mass[t[j].index / kSlice], (unsigned long long)t[j].steps);
   }
+  __syncthreads();
   // the slice that u falls into
   if (wave_id() == 0) {
     double w = 0.;
     if (lane < a.slices) {
-      w = p.base[lane];
-      const int i0 = p.at[lane], i1 = p.at[lane + 1];
-      if (i1 > i0) w += sh.sums[i1 - 1] - (i0 > 0 ? sh.sums[i0 - 1] : 0.);
+      w = p.base[lane] + (double)sh.slice_mass[lane] * to_mass;
     }
     const double end = wave_scan(w);
     const double total = __shfl(end, 63), target = (double)set.u * total;
@@ -522,8 +653,10 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
   for (int j = 0; j < per; ++j) {
     w[j] = 0.;
     const float l = i0 + j < a.s.vocab ? logit_of(x[i0 + j]) : -__builtin_inff();
-    if (l > -__builtin_inff() && (bin_of(l, f, c) < p.a || order_key(l, i0 + j) <= cut))
-      w[j] = list_mass(l, f, c);
+    if (l > -__builtin_inff()) {
+      const int k = bin_of(l, f, c);
+      if (k < p.a || (k <= p.z && order_key(l, i0 + j) <= cut)) w[j] = list_mass(l, f, c);
+    }
     s += w[j];
   }
   const double up = wave_scan(s);

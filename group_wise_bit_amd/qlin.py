@@ -936,27 +936,35 @@ def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, k_bi
 
 def _kv_seqs(cache: KVCache, table: torch.Tensor, lengths: torch.Tensor,
              starts: Optional[torch.Tensor]) -> QlinKvSeqsC:
-    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.dim() != 2 or \
-            (table.shape[0] > 0 and table.shape[1] > 1 and table.stride(1) != 1):
+    shape = table.shape if isinstance(table, torch.Tensor) and table.dtype is torch.int32 else ()
+    if len(shape) != 2:
         raise TypeError("table must be an int32 [seqs, pages per sequence] tensor with contiguous "
                         "rows")
-    seqs = table.shape[0]
+    seqs, width = shape
+    ld, step = table.stride()
+    if seqs > 0 and width > 1 and step != 1:
+        raise TypeError("table's rows must be contiguous")
     _need_flat(lengths, torch.int32, (seqs,), "lengths")
+    dev = cache.data.device
     if starts is not None:
         _need_flat(starts, torch.int32, (seqs + 1,), "starts")
-    _same_device(cache.data.device, (("table", table), ("lengths", lengths), ("starts", starts)))
-    return QlinKvSeqsC(seqs, table.shape[1], table.data_ptr(), _row_pitch(table),
-                       lengths.data_ptr())
+    if table.device != dev or lengths.device != dev or \
+            (starts is not None and starts.device != dev):
+        _same_device(dev, (("table", table), ("lengths", lengths), ("starts", starts)))
+    return QlinKvSeqsC(seqs, width, table.data_ptr(), ld if seqs > 1 else width, lengths.data_ptr())
 
 
 def _kv_rows(t: torch.Tensor, dtype: torch.dtype, heads: int, head_dim: int, name: str) -> int:
     """The pitch of [m, heads, head_dim] rows, whose heads follow one another."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 3 or \
-            t.shape[1:] != (heads, head_dim):
+    shape = t.shape if isinstance(t, torch.Tensor) and t.dtype is dtype else ()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
         raise TypeError(f"{name} must be a {dtype} [rows, {heads}, {head_dim}] tensor")
-    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim)):
+    if shape[0] == 0:
+        return heads * head_dim
+    pitch, head, one = t.stride()
+    if one != 1 or (head != head_dim and heads > 1):
         raise ValueError(f"{name}'s rows must be contiguous, got strides {t.stride()}")
-    return t.stride(0) if t.shape[0] > 1 else heads * head_dim
+    return pitch if shape[0] > 1 else heads * head_dim
 
 
 def kv_write(cache: KVCache, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor,
@@ -971,10 +979,10 @@ def kv_write(cache: KVCache, K: torch.Tensor, V: torch.Tensor, table: torch.Tens
     m, dev = K.shape[0], cache.data.device
     if V.shape[0] != m:
         raise ValueError(f"K has {m} rows, V {V.shape[0]}")
-    _same_device(dev, (("K", K), ("V", V)))
+    if K.device != dev or V.device != dev:
+        _same_device(dev, (("K", K), ("V", V)))
     _check(_launch(dev, lambda stream: _lib().qlin_kv_write(
-        ctypes.byref(c), K.data_ptr(), ldk, V.data_ptr(), ldv, m, ctypes.byref(s), _ptr(starts),
-        stream)), "qlin_kv_write")
+        c, K.data_ptr(), ldk, V.data_ptr(), ldv, m, s, _ptr(starts), stream)), "qlin_kv_write")
 
 
 def kv_read(cache: KVCache, table: torch.Tensor, lengths: torch.Tensor,
@@ -1002,10 +1010,11 @@ def kv_read(cache: KVCache, table: torch.Tensor, lengths: torch.Tensor,
     ldk, ldv = _kv_rows(K, dtype, h, d, "K"), _kv_rows(V, dtype, h, d, "V")
     if K.shape[0] < rows or V.shape[0] < rows:
         raise ValueError(f"K and V must have {rows} rows")
-    _same_device(dev, (("K", K), ("V", V)))
+    if K.device != dev or V.device != dev:
+        _same_device(dev, (("K", K), ("V", V)))
     _check(_launch(dev, lambda stream: _lib().qlin_kv_read(
-        ctypes.byref(c), ctypes.byref(s), _ptr(starts), rows, K.data_ptr(), ldk, V.data_ptr(), ldv,
-        int(dtype == torch.float32), stream)), "qlin_kv_read")
+        c, s, _ptr(starts), rows, K.data_ptr(), ldk, V.data_ptr(), ldv, int(dtype is torch.float32),
+        stream)), "qlin_kv_read")
     return K, V
 
 
@@ -1033,28 +1042,31 @@ def kv_attention(cache: KVCache, Q: torch.Tensor, table: torch.Tensor, lengths: 
         O16 = torch.empty(seqs, heads, d, dtype=torch.float16, device=dev)
     if lse is None and want_lse:
         lse = torch.empty(seqs, heads, dtype=torch.float32, device=dev)
-    ldo = heads * d
-    pitches = {_kv_rows(t, dtype, heads, d, name)
-               for t, dtype, name in ((O, torch.float32, "O"), (O16, torch.float16, "O16"))
-               if t is not None}
+    ldo = ldo16 = None
+    if O is not None:
+        ldo = _kv_rows(O, torch.float32, heads, d, "O")
+    if O16 is not None:
+        ldo16 = _kv_rows(O16, torch.float16, heads, d, "O16")
     for t, name in ((O, "O"), (O16, "O16")):
-        if t is not None and t.shape[0] != seqs:
+        if t is not None and (t.shape[0] != seqs or t.device != dev):
+            _same_device(dev, ((name, t),))
             raise ValueError(f"{name} has {t.shape[0]} rows for {seqs} sequences")
-    if len(pitches) > 1:
+    if ldo is None:
+        ldo = heads * d if ldo16 is None else ldo16
+    elif ldo16 is not None and ldo16 != ldo:
         raise ValueError("O and O16 must share one row stride")
-    if pitches:
-        ldo = pitches.pop()
     if lse is not None:
         _need_flat(lse, torch.float32, (seqs, heads), "lse")
-    _same_device(dev, (("Q", Q), ("O", O), ("O16", O16), ("lse", lse)))
+        _same_device(dev, (("lse", lse),))
+    if Q.device != dev:
+        _same_device(dev, (("Q", Q),))
     if scale is None:
         scale = d ** -0.5
     lib = _lib()
-    cp, sp = ctypes.byref(c), ctypes.byref(s)
     _with_workspace(
-        ws, dev, lambda: lib.qlin_kv_attention_workspace_bytes(cp, sp, heads),
+        ws, dev, lambda: lib.qlin_kv_attention_workspace_bytes(c, s, heads),
         lambda wp, wb, stream: lib.qlin_kv_attention(
-            cp, sp, Q.data_ptr(), ldq, heads, scale, window, _ptr(O), _ptr(O16), ldo, _ptr(lse), wp,
+            c, s, Q.data_ptr(), ldq, heads, scale, window, _ptr(O), _ptr(O16), ldo, _ptr(lse), wp,
             wb, stream), "qlin_kv_attention")
     return O, O16, lse
 
