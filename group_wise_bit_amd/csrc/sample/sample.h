@@ -27,19 +27,23 @@ struct SampleRow {
   float p, mp, u;    // p 1, mp 0: off
 };
 
+// (every load is made, of u where a setting is off, so that they are in flight together)
 __device__ __forceinline__ SampleRow sample_row(const SampleArgs& a, int row) {
-  SampleRow r;
-  const float t = a.temperature != nullptr ? a.temperature[row] : 1.f;
-  r.t = t > 0.f ? (double)t : 0.;
-  const int k = a.top_k != nullptr ? a.top_k[row] : 0;
-  r.k = k > 0 && k < a.vocab ? k : 0;
-  const float p = a.top_p != nullptr ? a.top_p[row] : 1.f;
-  r.p = p < 1.f ? fmaxf(p, 0.f) : 1.f;
-  const float mp = a.min_p != nullptr ? a.min_p[row] : 0.f;
-  r.mp = mp > 0.f ? mp : 0.f;
   const float u = a.u[row];
+  const float tv = (a.temperature != nullptr ? a.temperature : a.u)[row];
+  const int kv = (a.top_k != nullptr ? a.top_k : reinterpret_cast<const int32_t*>(a.u))[row];
+  const float pv = (a.top_p != nullptr ? a.top_p : a.u)[row];
+  const float mv = (a.min_p != nullptr ? a.min_p : a.u)[row];
+  const float t = a.temperature != nullptr ? tv : 1.f;
+  const int k = a.top_k != nullptr ? kv : 0;
+  const float p = a.top_p != nullptr ? pv : 1.f;
+  const float mp = a.min_p != nullptr ? mv : 0.f;
+  SampleRow r;
+  r.t = t > 0.f && k != 1 ? (double)t : 0.;
+  r.k = k > 0 && k < a.vocab ? k : 0;
+  r.p = p < 1.f ? fmaxf(p, 0.f) : 1.f;
+  r.mp = mp > 0.f ? mp : 0.f;
   r.u = u > 0.f ? u : 0.f;
-  if (k == 1) r.t = 0.;
   return r;
 }
 
@@ -77,7 +81,7 @@ __device__ __forceinline__ uint64_t scaled(float f, uint64_t v, bool up) {
   return (uint64_t)q + (up && (q << shift) != x);
 }
 
-constexpr int kSampleThreads = 1024;
+constexpr int kSampleThreads = 512;
 constexpr int kSampleWaves = kSampleThreads / 64;
 
 struct SampleShared {

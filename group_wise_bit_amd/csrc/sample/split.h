@@ -27,7 +27,7 @@ struct SliceStat {
   int pad;
 };
 
-struct RowPlanS {
+struct RowHead {
   double floor_top;                          // of the row
   float top;
   int mode;                                  // 0: no tokens, 1: largest, 2: list, 3: by itself
@@ -37,6 +37,9 @@ struct RowPlanS {
   double mass_a;                             // of the bins before a
   double mass_k;                             // of the first top_k without those k_main / k_extra
   int slice;                                 // mode 1: the first slice with the largest logit
+};
+struct RowPlanS {
+  RowHead head;
   int at[kSlices + 1];                       // where a slice's tokens begin in the list
   double base[kSlices];                      // a slice's mass of the bins before a
 };
@@ -200,12 +203,12 @@ __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
   for (int d = 32; d > 0; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
   if (top == -__builtin_inff() || set.t == 0.) {
     if (k == 0) {
-      p.mode = top == -__builtin_inff() ? 0 : 1;
-      p.top = top;
-      p.n = 0;
+      p.head.mode = top == -__builtin_inff() ? 0 : 1;
+      p.head.top = top;
+      p.head.n = 0;
     }
     const uint64_t has = __ballot(st.top == top);
-    if (k == 0) p.slice = __builtin_ctzll(has);
+    if (k == 0) p.head.slice = __builtin_ctzll(has);
     return;
   }
   const BinScale c = bin_scale(set.t);
@@ -219,17 +222,18 @@ __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
   __syncthreads();
   double m = 0.;
   uint32_t q = 0;
-  for (int s0 = 0; s0 < a.slices; s0 += 8) {
-    double cm[8];
-    uint32_t cq[8];
+  constexpr int kFlight = 16;                // slices whose loads are in flight
+  for (int s0 = 0; s0 < a.slices; s0 += kFlight) {
+    double cm[kFlight];
+    uint32_t cq[kFlight];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kFlight; ++j) {
       const int s = min(s0 + j, a.slices - 1), d = max(k - shift[s], 0);
       cm[j] = a.cum_mass[(at + s) * kBins + d];
       cq[j] = a.cum_count[(at + s) * kBins + d];
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < kFlight; ++j)
       // (a slice whose bins all lie below was not written: what is there is not used)
       if (s0 + j < a.slices && k >= shift[s0 + j]) {
         m += cm[j] * factor[s0 + j];
@@ -271,16 +275,19 @@ __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
   const int main = first < kBins ? (int)(count[last] - before) : 0;
   const int more = extra >= 0 ? (int)(count[extra] - count[extra - 1]) : 0;
   if (k < 64) {
+    // (loads of places that hold nothing are made of others, so that all are in flight together)
+    const int slice = min(k, a.slices - 1), s = shift[slice];
+    const uint32_t* n = a.cum_count + (at + slice) * kBins;
+    auto place = [&](int bin) { return min(max(bin - s, 0), kBins - 1); };
+    const uint32_t n0 = n[place(first - 1)], n1 = n[place(last)], n2 = n[place(extra - 1)],
+                   n3 = n[place(extra)];
+    const double before_a = a.cum_mass[(at + slice) * kBins + place(first - 1)];
     int size = 0;
     double base = 0.;
     if (k < a.slices) {
-      const uint32_t* n = a.cum_count + (at + k) * kBins - shift[k];
-      const int s = shift[k];
-      auto upto = [&](int bin) { return bin >= s ? n[bin] : 0u; };
-      if (first < kBins) size = (int)(upto(last) - upto(first - 1));
-      if (extra >= 0) size += (int)(upto(extra) - upto(extra - 1));
-      if (first > 0 && first - 1 >= s)
-        base = a.cum_mass[(at + k) * kBins + first - 1 - s] * factor[k];
+      if (first < kBins) size = (int)((last >= s ? n1 : 0u) - (first - 1 >= s ? n0 : 0u));
+      if (extra >= 0) size += (int)((extra >= s ? n3 : 0u) - (extra - 1 >= s ? n2 : 0u));
+      if (first > 0 && first - 1 >= s) base = before_a * factor[slice];
     }
     const int end = wave_scan(size);
     p.at[k + 1] = end;
@@ -288,32 +295,32 @@ __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
     p.base[k] = base;
   }
   if (k == 0) {
-    p.floor_top = f;
-    p.top = top;
-    p.a = first;
-    p.z = last;
-    p.e = extra;
-    p.n = main + more;
-    p.main = main;
-    p.mode = main + more <= kListMax ? 2 : 3;
-    p.mass_a = first > 0 ? mass[first - 1] : 0.;
-    p.k_main = cut_k && bk <= last ? set.k - (int)before : main;
-    p.k_extra = extra >= 0 ? set.k - (int)count[extra - 1] : 0;
+    p.head.floor_top = f;
+    p.head.top = top;
+    p.head.a = first;
+    p.head.z = last;
+    p.head.e = extra;
+    p.head.n = main + more;
+    p.head.main = main;
+    p.head.mode = main + more <= kListMax ? 2 : 3;
+    p.head.mass_a = first > 0 ? mass[first - 1] : 0.;
+    p.head.k_main = cut_k && bk <= last ? set.k - (int)before : main;
+    p.head.k_extra = extra >= 0 ? set.k - (int)count[extra - 1] : 0;
     // the mass of the first top_k: mass_a and the list's, or what lies before the bin e and that bin's
-    p.mass_k = extra >= 0 ? mass[extra - 1] : cut_k && bk <= last ? -1. : high;
+    p.head.mass_k = extra >= 0 ? mass[extra - 1] : cut_k && bk <= last ? -1. : high;
   }
 }
 
 __global__ __launch_bounds__(kBinThreads) void k_sample_gather(const SplitArgs a) {
   __shared__ int counts[64];
   const int slice = blockIdx.x % a.slices, r = blockIdx.x / a.slices, row = a.row0 + r;
-  const RowPlanS& p = a.plan[r];
-  if (p.mode != 2) return;
-  const int from = p.at[slice];
-  if (p.at[slice + 1] == from) return;
+  const RowPlanS& plan = a.plan[r];
+  const RowHead p = plan.head;
+  const int from = plan.at[slice], to = plan.at[slice + 1];
+  const BinScale c = bin_scale(sample_row(a.s, row).t);
+  if (p.mode != 2 || from == to) return;
   const float* x = a.s.logits + row * a.s.ld + slice * kSlice;
   const int n = min(a.s.vocab - slice * kSlice, kSlice);
-  const BinScale c = bin_scale(sample_row(a.s, row).t);
   const double f = p.floor_top;
   const int first = p.a, last = p.z, extra = p.e, lane = lane_id(), wave = wave_id();
   constexpr int per = kSlice / kBinThreads;
@@ -349,7 +356,6 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_gather(const SplitArgs a
 }
 
 constexpr int kPickThreads = kSampleThreads;
-constexpr int kPickPer = kListMax / kPickThreads;
 
 // The order of tokens as an ascending integer: by logit, descending, then by index.
 __device__ __forceinline__ uint64_t order_key(float l, uint32_t index) {
@@ -391,11 +397,14 @@ __device__ __forceinline__ void sort_keys(uint64_t* keys, int size) {
 // of them, the bin e has the rest.  Counts and masses of the parts (in steps of 2^-34
 // of bin a's / e's unit, the count from bit 50 on) tell where a cut lies; only the tokens of that part
 // are put in order.
-constexpr int kParts = kPickThreads;
+constexpr int kParts = 1024;
 constexpr int kMainParts = 896;
 constexpr int kPartCount = 50;
 
 struct PickShared {
+  float l[kListMax];                         // the gathered tokens
+  uint32_t index[kListMax];
+  uint16_t part_of[kListMax];
   uint64_t keys[kListMax];                   // a part's tokens in order
   unsigned long long part[kParts];           // sums up to a part
   unsigned long long slice_mass[kSlices];
@@ -403,28 +412,33 @@ struct PickShared {
   uint64_t scan[kSampleWaves];
   double before, target, total;
   int slice, count[3], size, at, rank;
-  SampleShared alone;
-};
-
-struct PickToken {
-  float l;
-  uint32_t index;
-  int part;                                  // -1: no token
-  uint64_t steps;
 };
 
 // The tokens of a part in order: sh.keys[0 .. sh.size).
-__device__ __forceinline__ void order_part(PickShared& sh, const PickToken (&t)[kPickPer], int part) {
+__device__ __forceinline__ void order_part(PickShared& sh, int n, int part) {
   if (threadIdx.x == 0) sh.size = 0;
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kPickPer; ++j)
-    if (t[j].part == part) sh.keys[atomicAdd(&sh.size, 1)] = order_key(t[j].l, t[j].index);
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n; i += kPickThreads)
+    if (sh.part_of[i] == part) sh.keys[atomicAdd(&sh.size, 1)] = order_key(sh.l[i], sh.index[i]);
   __syncthreads();
-  const int n = sh.size;
+  const int m = sh.size;
+  if (m <= kPickThreads) {
+    // a token's place is the number of those before it
+    const int i = threadIdx.x;
+    const uint64_t mine = i < m ? sh.keys[i] : 0;
+    int rank = 0;
+    if (wave_id() * 64 < m)
+#pragma unroll 4
+      for (int j = 0; j < m; ++j) rank += sh.keys[j] < mine;
+    __syncthreads();
+    if (i < m) sh.keys[rank] = mine;
+    __syncthreads();
+    return;
+  }
   int size = 64;
-  while (size < n) size *= 2;
-  for (int i = n + threadIdx.x; i < size; i += kPickThreads) sh.keys[i] = ~0ull;
+  while (size < m) size *= 2;
+  for (int i = m + threadIdx.x; i < size; i += kPickThreads) sh.keys[i] = ~0ull;
   __syncthreads();
   sort_keys(sh.keys, size);
 }
@@ -432,10 +446,11 @@ __device__ __forceinline__ void order_part(PickShared& sh, const PickToken (&t)[
 // The first part whose sum (counts or masses, from `from` on) reaches `need`; kParts: none.
 template <typename F>
 __device__ __forceinline__ int first_part(PickShared& sh, int from, int to, F reaches) {
-  const int i = threadIdx.x;
-  if (i == 0) sh.at = kParts;
+  if (threadIdx.x == 0) sh.at = kParts;
   __syncthreads();
-  if (i >= from && i < to && reaches(sh.part[i]) && (i == from || !reaches(sh.part[i - 1]))) sh.at = i;
+#pragma unroll 1
+  for (int i = from + threadIdx.x; i < to; i += kPickThreads)
+    if (reaches(sh.part[i]) && (i == from || !reaches(sh.part[i - 1]))) sh.at = i;
   __syncthreads();
   return sh.at;
 }
@@ -479,88 +494,92 @@ __device__ __forceinline__ int first_to_reach(PickShared& sh, double sum, double
 
 __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a) {
   __shared__ PickShared sh;
-  const int r = blockIdx.x, row = a.row0 + r, lane = lane_id();
-  const RowPlanS& p = a.plan[r];
+  const int r = blockIdx.x, row = a.row0 + r, lane = lane_id(), tid = threadIdx.x;
+  const RowPlanS& plan = a.plan[r];
+  const RowHead p = plan.head;
+  const SampleRow set = sample_row(a.s, row);
   const float* x = a.s.logits + row * a.s.ld;
   const int mode = p.mode;
   if (mode == 3) {
-    sample_alone(a.s, row, sh.alone);
+    sample_alone(a.s, row, reinterpret_cast<SampleShared&>(sh));
     return;
   }
   if (mode == 0) {
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
       a.s.ids[row] = -1;
       if (a.s.probs != nullptr) a.s.probs[row] = 0.f;
     }
     return;
   }
   if (mode == 1) {
-    if (threadIdx.x == 0) sh.slice = 0x7FFFFFFF;
+    if (tid == 0) sh.slice = 0x7FFFFFFF;
     __syncthreads();
-    for (int i = p.slice * kSlice + threadIdx.x; i < min((p.slice + 1) * kSlice, a.s.vocab);
-         i += kPickThreads)
+    for (int i = p.slice * kSlice + tid; i < min((p.slice + 1) * kSlice, a.s.vocab); i += kPickThreads)
       if (logit_of(x[i]) == p.top) atomicMin(&sh.slice, i);
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
       a.s.ids[row] = sh.slice;
       if (a.s.probs != nullptr) a.s.probs[row] = 1.f;
     }
     return;
   }
-  const SampleRow set = sample_row(a.s, row);
+  const double base = lane < a.slices ? plan.base[lane] : 0.;
   const BinScale c = bin_scale(set.t);
   const double f = p.floor_top;
   const int n = p.n, main = p.main;
   const uint2* list = a.list + (int64_t)r * kListMax;
   uint64_t cut = 0;                            // keys up to it are kept
-  for (int i = threadIdx.x; i < kSlices; i += kPickThreads) sh.slice_mass[i] = 0;
+  if (tid < kSlices) sh.slice_mass[tid] = 0;
   constexpr uint64_t kMassMask = (1ull << kPartCount) - 1;
-  const double unit = p.a < kBins ? exp(-(double)p.a * (1. / kBinScale)) : 0.;   // of bin a
-  const double to_mass = unit * (1. / (double)(1ull << kMassStep));
+  constexpr double kStep = 1. / (double)(1ull << kMassStep);
+  const double to_mass = p.a < kBins ? exp(-(double)p.a * (1. / kBinScale)) * kStep : 0.;   // bin a's
   if (n > 0) {
-    PickToken t[kPickPer];
-    sh.part[threadIdx.x] = 0;
-    const double unit_e = p.e >= 0 ? exp(-(double)p.e * (1. / kBinScale)) : 0.;
-#pragma unroll
-    for (int j = 0; j < kPickPer; ++j) {
-      const int i = j * kPickThreads + threadIdx.x;
-      const uint2 w = i < n ? list[i] : make_uint2(0, 0);
-      t[j].l = __builtin_bit_cast(float, w.y);
-      t[j].index = w.x;
-      t[j].part = i < n ? 0 : -1;
-    }
+    for (int i = tid; i < kParts; i += kPickThreads) sh.part[i] = 0;
     __syncthreads();
     const double scale = (double)kMainParts / (double)(p.z + 1 - p.a);
-#pragma unroll
-    for (int j = 0; j < kPickPer; ++j) {
-      if (t[j].part < 0) continue;
-      const double ld = (double)t[j].l, hi = ld * c.hi, fl = __builtin_floor(hi);
+    // part and steps of a token
+    auto place = [&](float l, uint64_t& steps) {
+      const double ld = (double)l, hi = ld * c.hi, fl = __builtin_floor(hi);
       const double x = hi - fl + t_low(ld, hi, c);              // in the bin, about 0 .. 1
       const int k = (int)(f - fl);
       const bool extra = k > p.z;
       const double y = 1. - __builtin_fmin(__builtin_fmax(x, 0.), 1.);
-      t[j].part = extra ? kMainParts + min((int)(y * (kParts - kMainParts)), kParts - kMainParts - 1)
-                        : min((int)(((double)(k - p.a) + y) * scale), kMainParts - 1);
-      const double in_bin = bin_mass(x - 0.5, kMassOne) - (kMassOne - 1.);
-      const double rel = extra || k == p.a ? in_bin : in_bin * exp((double)(p.a - k) * (1. / kBinScale));
-      t[j].steps = (uint64_t)__builtin_rint(rel * (double)(1ull << kMassStep));
-      atomicAdd(&sh.part[t[j].part], (unsigned long long)(t[j].steps | 1ull << kPartCount));
+      double rel = bin_mass(x - 0.5, kMassOne) - (kMassOne - 1.);
+      if (!extra && k != p.a) rel *= exp((double)(p.a - k) * (1. / kBinScale));
+      steps = (uint64_t)__builtin_rint(rel * (double)(1ull << kMassStep));
+      return extra ? kMainParts + min((int)(y * (kParts - kMainParts)), kParts - kMainParts - 1)
+                   : min((int)(((double)(k - p.a) + y) * scale), kMainParts - 1);
+    };
+    // (the next two tokens' loads are in flight while one is placed)
+    uint2 w0 = list[min(tid, n - 1)], w1 = list[min(tid + kPickThreads, n - 1)];
+#pragma unroll 1
+    for (int i = tid; i < n; i += kPickThreads) {
+      const uint2 w2 = list[min(i + 2 * kPickThreads, n - 1)];
+      const float l = __builtin_bit_cast(float, w0.y);
+      uint64_t steps;
+      const int part = place(l, steps);
+      sh.l[i] = l;
+      sh.index[i] = w0.x;
+      sh.part_of[i] = (uint16_t)part;
+      atomicAdd(&sh.part[part], (unsigned long long)(steps | 1ull << kPartCount));
+      w0 = w1;
+      w1 = w2;
     }
     __syncthreads();
     // sums up to a part; the bin e's begin anew
+    static_assert(kParts == 2 * kPickThreads && kMainParts % 128 == 0, "two parts a thread");
     {
-      const int i = threadIdx.x;
-      uint64_t v = sh.part[i];
+      const uint64_t v0 = sh.part[2 * tid], v1 = sh.part[2 * tid + 1];
+      uint64_t v = v0 + v1;
       for (int d = 1; d < 64; d *= 2) {
         const uint64_t o = shfl_up64(v, d);
         if (lane >= d) v += o;
       }
       if (lane == 63) sh.scan[wave_id()] = v;
       __syncthreads();
-      static_assert(kMainParts % 64 == 0, "whole waves");
-      for (int w = i >= kMainParts ? kMainParts / 64 : 0; w < wave_id(); ++w) v += sh.scan[w];
-      __syncthreads();
-      sh.part[i] = v;
+      for (int w = 2 * tid >= kMainParts ? kMainParts / 128 : 0; w < wave_id(); ++w) v += sh.scan[w];
+      sh.part[2 * tid] = v - v1;
+      sh.part[2 * tid + 1] = v;
       __syncthreads();
     }
     auto count_to = [&](int part, int from) { return part > from ? (int)(sh.part[part - 1] >> kPartCount) : 0; };
@@ -571,7 +590,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
     auto rank_of = [&](int want) {             // the want-th token is sh.keys[rank_of(want) - 1]
       if (held < 0 || want <= count_to(held, 0) || want > count_to(held, 0) + sh.size) {
         held = first_part(sh, 0, kMainParts, [&](uint64_t v) { return (int)(v >> kPartCount) >= want; });
-        order_part(sh, t, held);
+        order_part(sh, n, held);
       }
       return want - count_to(held, 0);
     };
@@ -580,8 +599,8 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
       if (p.e >= 0) {
         const int pe = first_part(sh, kMainParts, kParts,
                                   [&](uint64_t v) { return (int)(v >> kPartCount) >= p.k_extra; });
-        order_part(sh, t, pe);
-        mass_k += mass_to(pe, kMainParts) * unit_e * (1. / (double)(1ull << kMassStep)) +
+        order_part(sh, n, pe);
+        mass_k += mass_to(pe, kMainParts) * exp(-(double)p.e * (1. / kBinScale)) * kStep +
                   mass_of_first(sh, p.k_extra - count_to(pe, kMainParts), f, c);
       } else if (mass_k < 0.) {
         const int rank = rank_of(p.k_main);
@@ -592,7 +611,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
       const int pp = first_part(sh, 0, kMainParts, [&](uint64_t v) {
         return p.mass_a + (double)(v & kMassMask) * to_mass >= target; });
       if (pp < kParts && count_to(pp, 0) < kept) {
-        if (held != pp) order_part(sh, t, pp);
+        if (held != pp) order_part(sh, n, pp);
         held = pp;
         kept = min(kept, count_to(pp, 0) + first_to_reach(sh, p.mass_a + mass_to(pp, 0) * to_mass,
                                                           target, f, c));
@@ -601,12 +620,12 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
     if (set.mp > 0.f) {
       const double top_hi = (double)p.top * c.hi, top_lo = t_low((double)p.top, top_hi, c);
       int pass = 0;
-#pragma unroll
-      for (int j = 0; j < kPickPer; ++j) {
-        if (t[j].part < 0 || t[j].part >= kMainParts) continue;
-        const double hi = (double)t[j].l * c.hi;
-        const double e = (hi - top_hi + (t_low((double)t[j].l, hi, c) - top_lo)) * (1. / kBinScale);
-        pass += t[j].l == p.top || exp(e) >= (double)set.mp;
+#pragma unroll 1
+      for (int i = tid; i < n; i += kPickThreads) {
+        if (sh.part_of[i] >= kMainParts) continue;
+        const double l = (double)sh.l[i], hi = l * c.hi;
+        const double e = (hi - top_hi + (t_low(l, hi, c) - top_lo)) * (1. / kBinScale);
+        pass += sh.l[i] == p.top || exp(e) >= (double)set.mp;
       }
       for (int d = 32; d > 0; d /= 2) pass += __shfl_xor(pass, d);
       if (threadIdx.x == 0) sh.count[0] = 0;
@@ -619,17 +638,20 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
     else if (kept > 0) cut = sh.keys[rank_of(kept) - 1];
     __syncthreads();
     // the kept ones' masses, slice by slice
-#pragma unroll
-    for (int j = 0; j < kPickPer; ++j)
-      if (t[j].part >= 0 && t[j].part < kMainParts && order_key(t[j].l, t[j].index) <= cut)
-        atomicAdd(&sh.slice_mass[t[j].index / kSlice], (unsigned long long)t[j].steps);
+#pragma unroll 1
+    for (int i = tid; i < n; i += kPickThreads)
+      if (sh.part_of[i] < kMainParts && order_key(sh.l[i], sh.index[i]) <= cut) {
+        uint64_t steps;
+        place(sh.l[i], steps);
+        atomicAdd(&sh.slice_mass[sh.index[i] / kSlice], (unsigned long long)steps);
+      }
   }
   __syncthreads();
   // the slice that u falls into
   if (wave_id() == 0) {
     double w = 0.;
     if (lane < a.slices) {
-      w = p.base[lane] + (double)sh.slice_mass[lane] * to_mass;
+      w = base + (double)sh.slice_mass[lane] * to_mass;
     }
     const double end = wave_scan(w);
     const double total = __shfl(end, 63), target = (double)set.u * total;
@@ -647,7 +669,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
   __syncthreads();
   // the token in the slice
   constexpr int per = kSlice / kPickThreads;
-  const int first = sh.slice * kSlice, i0 = first + (int)threadIdx.x * per;
+  const int first = sh.slice * kSlice, i0 = first + tid * per;
   double w[per], s = 0.;
 #pragma unroll
   for (int j = 0; j < per; ++j) {
