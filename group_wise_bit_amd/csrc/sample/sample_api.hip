@@ -32,8 +32,8 @@ SamplePlan sample_plan(int m, int vocab) {
   p.rows = m < most ? m : most;
   const int64_t items = (int64_t)p.rows * p.slices;
   p.mass = kCounterBytes;
-  p.count = align256(p.mass + items * kBins * (int64_t)sizeof(double));
-  p.stat = align256(p.count + items * kBins * (int64_t)sizeof(uint32_t));
+  p.count = align256(p.mass + items * kSums * (int64_t)sizeof(double));
+  p.stat = align256(p.count + items * kSums * (int64_t)sizeof(uint32_t));
   p.plan = align256(p.stat + items * (int64_t)sizeof(SliceStat));
   p.list = align256(p.plan + p.rows * (int64_t)sizeof(RowPlanS));
   p.bytes = p.list + p.rows * (int64_t)kListMax * (int64_t)sizeof(uint2);

@@ -20,6 +20,7 @@ constexpr int kBins = 384;
 constexpr int kBinScale = 12;
 constexpr int kListMax = 8192;               // tokens that are gathered, at most
 constexpr int kBinThreads = 256;
+constexpr int kSums = kBins + 1;             // a slice's sums: 0, then up to each bin
 
 struct SliceStat {
   double floor_top;                          // floor(t) of its largest logit
@@ -47,7 +48,7 @@ struct RowPlanS {
 struct SplitArgs {
   SampleArgs s;
   int row0, slices;
-  double* cum_mass;                          // [rows][slices][kBins]: sums up to a bin
+  double* cum_mass;                          // [rows][slices][kSums]
   uint32_t* cum_count;
   SliceStat* stat;                           // [rows][slices]
   RowPlanS* plan;                            // [rows]
@@ -144,7 +145,11 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_bins(const SplitArgs a) 
   for (int w = 0; w < 4; ++w) top = fmaxf(top, tops[w]);
   const BinScale c = bin_scale(set.t == 0. ? 1. : set.t);
   const double first = top > -__builtin_inff() ? __builtin_floor((double)top * c.hi) : 0.;
-  if (threadIdx.x == 0) a.stat[at] = SliceStat{first, top, 0};
+  if (threadIdx.x == 0) {
+    a.stat[at] = SliceStat{first, top, 0};
+    a.cum_mass[at * kSums] = 0.;
+    a.cum_count[at * kSums] = 0;
+  }
   if (set.t == 0. || top == -__builtin_inff()) return;
 #pragma unroll
   for (int j = 0; j < per; ++j) {
@@ -180,8 +185,8 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_bins(const SplitArgs a) 
     mass_before = mb;
     count_before = cb;
     if (k < kBins) {
-      a.cum_mass[at * kBins + k] = m;
-      a.cum_count[at * kBins + k] = q;
+      a.cum_mass[at * kSums + 1 + k] = m;
+      a.cum_count[at * kSums + 1 + k] = q;
     }
     __syncthreads();
   }
@@ -228,17 +233,16 @@ __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
     uint32_t cq[kFlight];
 #pragma unroll
     for (int j = 0; j < kFlight; ++j) {
-      const int s = min(s0 + j, a.slices - 1), d = max(k - shift[s], 0);
-      cm[j] = a.cum_mass[(at + s) * kBins + d];
-      cq[j] = a.cum_count[(at + s) * kBins + d];
+      // (a slice without mass in these bins, and one that is not there: its first sum, 0)
+      const int64_t i = (at + min(s0 + j, a.slices - 1)) * kSums + max(k + 1 - shift[s0 + j], 0);
+      cm[j] = a.cum_mass[i];
+      cq[j] = a.cum_count[i];
     }
 #pragma unroll
-    for (int j = 0; j < kFlight; ++j)
-      // (a slice whose bins all lie below was not written: what is there is not used)
-      if (s0 + j < a.slices && k >= shift[s0 + j]) {
-        m += cm[j] * factor[s0 + j];
-        q += cq[j];
-      }
+    for (int j = 0; j < kFlight; ++j) {
+      m += cm[j] * factor[s0 + j];
+      q += cq[j];
+    }
   }
   mass[k] = m;
   count[k] = q;
@@ -275,20 +279,15 @@ __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
   const int main = first < kBins ? (int)(count[last] - before) : 0;
   const int more = extra >= 0 ? (int)(count[extra] - count[extra - 1]) : 0;
   if (k < 64) {
-    // (loads of places that hold nothing are made of others, so that all are in flight together)
+    // (bins before the slice's first: its first sum, 0)
     const int slice = min(k, a.slices - 1), s = shift[slice];
-    const uint32_t* n = a.cum_count + (at + slice) * kBins;
-    auto place = [&](int bin) { return min(max(bin - s, 0), kBins - 1); };
-    const uint32_t n0 = n[place(first - 1)], n1 = n[place(last)], n2 = n[place(extra - 1)],
-                   n3 = n[place(extra)];
-    const double before_a = a.cum_mass[(at + slice) * kBins + place(first - 1)];
-    int size = 0;
-    double base = 0.;
-    if (k < a.slices) {
-      if (first < kBins) size = (int)((last >= s ? n1 : 0u) - (first - 1 >= s ? n0 : 0u));
-      if (extra >= 0) size += (int)((extra >= s ? n3 : 0u) - (extra - 1 >= s ? n2 : 0u));
-      if (first > 0 && first - 1 >= s) base = before_a * factor[slice];
-    }
+    const uint32_t* n = a.cum_count + (at + slice) * kSums;
+    auto upto = [&](int bin) { return max(bin + 1 - s, 0); };
+    const uint32_t n0 = n[upto(first - 1)], n1 = n[upto(last)], n2 = n[upto(extra - 1)],
+                   n3 = n[upto(extra)];
+    const double before_a = a.cum_mass[(at + slice) * kSums + upto(first - 1)] * factor[slice];
+    const int size = k < a.slices ? (first < kBins ? (int)(n1 - n0) : 0) + (extra >= 0 ? (int)(n3 - n2) : 0) : 0;
+    const double base = k < a.slices ? before_a : 0.;
     const int end = wave_scan(size);
     p.at[k + 1] = end;
     if (k == 0) p.at[0] = 0;
