@@ -3,33 +3,35 @@
 
 #include "sample.h"
 
+#include <type_traits>
+
 namespace qlin {
 
 // The steps of a draw:
-//   bins    every slice of 4096 logits: counts and masses by bins of the exponent,
+//   bins    every slice of 8192 logits: counts and masses by bins of the exponent,
 //   bounds  every row: the bins in which the cuts of top_k, top_p and min_p can lie,
 //   gather  every slice: its tokens in these bins, in the order of the vocabulary,
 //   pick    every row: the cut among them, the slice that u falls into, the token.
-// Exponents are t = 12 l / temperature in 64 bits; a bin is floor(t), so that bins of
+// Exponents are t = 12 l / temperature in 64 bits; a bin is t rounded, so that bins of
 // different slices line up whatever their largest logit, and the mass of a
-// token is exp((t - middle of its bin) / 12), a polynomial of degree 7, times a factor per
-// bin.  Bins from 384 below the top one (exp(-32)) on hold no mass.
-constexpr int kSlice = 4096;
-constexpr int kSlices = 64;                  // of a row, at most
+// token is exp((t - bin) / 12), a polynomial of degree 6, times a factor per bin.
+// Bins from 384 below the top one (exp(-32)) on hold no mass.
+constexpr int kSlice = 8192;
+constexpr int kSlices = 32;                  // of a row, at most
 constexpr int kBins = 384;
 constexpr int kBinScale = 12;
 constexpr int kListMax = 8192;               // tokens that are gathered, at most
-constexpr int kBinThreads = 256;
+constexpr int kBinThreads = 512;
 constexpr int kSums = kBins + 1;             // a slice's sums: 0, then up to each bin
 
 struct SliceStat {
-  double floor_top;                          // floor(t) of its largest logit
+  double top_bin;                          // the bin of its largest logit
   float top;                                 // -inf: no tokens
   int pad;
 };
 
 struct RowHead {
-  double floor_top;                          // of the row
+  double top_bin;                          // of the row
   float top;
   int mode;                                  // 0: no tokens, 1: largest, 2: list, 3: by itself
   int a, z, e;                               // gathered bins a .. z and e (-1: none)
@@ -66,37 +68,42 @@ __device__ __forceinline__ BinScale bin_scale(double t) {
   if (!(t < (double)__builtin_inff())) c.lo = 0.;
   return c;
 }
-// (from |t| = 2^51 on a bin holds one value of l only, and any x will do)
 __device__ __forceinline__ double t_low(double l, double hi, BinScale c) {
-  const double x = __builtin_fma(l, c.lo, __builtin_fma(l, c.hi, -hi));
-  return __builtin_fmin(__builtin_fmax(x, -0.25), 0.25);
+  return __builtin_fma(l, c.lo, __builtin_fma(l, c.hi, -hi));
+}
+// t less its bin.  From |t| = 2^40 on nothing is left of hi, and lo may be anything: there
+// a bin holds one value of l only, and any number will do.
+__device__ __forceinline__ double t_rest(double l, double hi, double bin, BinScale c) {
+  const double x = (hi - bin) + t_low(l, hi, c);
+  return __builtin_fabs(bin) < 0x1p40 ? x : 0.;
 }
 
-// exp(x / 12) - 1 + one for |x| <= 1/2 (and a little beyond): x^8 / (12^8 8!) < 2^-51.
+// exp(x / 12) - 1 + one for |x| <= 1/2 (and a little beyond): x^7 / (12^7 7!) < 2^-44.
 __device__ __forceinline__ double bin_mass(double x, double one) {
-  const double z = x * (1. / kBinScale);
-  double p = 1. / 5040;
-  p = __builtin_fma(p, z, 1. / 720);
-  p = __builtin_fma(p, z, 1. / 120);
-  p = __builtin_fma(p, z, 1. / 24);
-  p = __builtin_fma(p, z, 1. / 6);
-  p = __builtin_fma(p, z, 0.5);
-  p = __builtin_fma(p, z, 1.);
-  return __builtin_fma(p, z, one);
+  constexpr double s = 1. / kBinScale;
+  double p = s * s * s * s * s * s / 720;
+  p = __builtin_fma(p, x, s * s * s * s * s / 120);
+  p = __builtin_fma(p, x, s * s * s * s / 24);
+  p = __builtin_fma(p, x, s * s * s / 6);
+  p = __builtin_fma(p, x, s * s / 2);
+  p = __builtin_fma(p, x, s);
+  return __builtin_fma(p, x, one);
 }
 // Masses within a bin are whole numbers of 2^-34: sums of 2^18 equal ones are exact, and
 // the sums of histograms and of lists are sums of the same numbers.
 constexpr int kMassStep = 34;
 constexpr double kMassOne = 1. + (double)(1 << (52 - kMassStep));
 
-// Mass of a logit relative to the middle of the bin floor_top.
-__device__ __forceinline__ double list_mass(float l, double floor_top, BinScale c) {
-  const double ld = (double)l, hi = ld * c.hi, f = __builtin_floor(hi);
-  const double p = bin_mass(hi - f - 0.5 + t_low(ld, hi, c), kMassOne) - (kMassOne - 1.);
-  return p * exp((f - floor_top) * (1. / kBinScale));
+// Mass of a logit relative to the middle of the bin `top`, with the factors of the bins from
+// there on.
+__device__ __forceinline__ double list_mass(float l, double top, BinScale c, const double* factor) {
+  const double ld = (double)l, hi = ld * c.hi, f = __builtin_rint(hi), k = top - f;
+  const double p = bin_mass(t_rest(ld, hi, f, c), kMassOne) - (kMassOne - 1.);
+  return k < (double)kBins ? p * factor[(int)k] : 0.;
 }
-__device__ __forceinline__ int bin_of(float l, double floor_top, BinScale c) {
-  const double k = floor_top - __builtin_floor((double)l * c.hi);
+__device__ __forceinline__ double bin_factor(int k) { return exp(-(double)k * (1. / kBinScale)); }
+__device__ __forceinline__ int bin_of(float l, double top, BinScale c) {
+  const double k = top - __builtin_rint((double)l * c.hi);
   return k < (double)kBins ? (int)k : kBins;
 }
 
@@ -110,86 +117,81 @@ __device__ __forceinline__ T wave_scan(T v) {          // inclusive
   return v;
 }
 
-// A histogram entry: the count from bit 51 on (4096 at most), the mass in its steps
-// below (4096 exp(1 / 24) 2^34 at most): one LDS atomic per token, and a sum that does
+// A histogram entry: the count from bit 50 on (8192 at most), the mass in its steps
+// below (8192 exp(1 / 24) 2^34 at most): one LDS atomic per token, and a sum that does
 // not depend on the order.
-constexpr int kCountBit = 51;
+constexpr int kCountBit = 50;
 
 __global__ __launch_bounds__(kBinThreads) void k_sample_bins(const SplitArgs a) {
   __shared__ unsigned long long hist[kBins];
-  __shared__ float tops[4];
-  __shared__ double wave_mass[4];
-  __shared__ uint32_t wave_count[4];
+  constexpr int kWaves = kBinThreads / 64;
+  __shared__ float tops[kWaves];
+  __shared__ double wave_mass[kWaves];
+  __shared__ uint32_t wave_count[kWaves];
   const int slice = blockIdx.x % a.slices, r = blockIdx.x / a.slices, row = a.row0 + r;
   const int64_t at = (int64_t)r * a.slices + slice;
   const float* x = a.s.logits + row * a.s.ld + slice * kSlice;
-  const int n = min(a.s.vocab - slice * kSlice, kSlice);
+  const int n = min(a.s.vocab - slice * kSlice, kSlice), tid = threadIdx.x, wave = wave_id();
   constexpr int per = kSlice / kBinThreads;
   float l[per];
   float top = -__builtin_inff();
 #pragma unroll
   for (int j = 0; j < per; ++j) {
-    const int i = j * kBinThreads + threadIdx.x;
+    const int i = j * kBinThreads + tid;
     l[j] = i < n ? x[i] : -__builtin_inff();
   }
   const SampleRow set = sample_row(a.s, row);
-  for (int i = threadIdx.x; i < kBins; i += kBinThreads) hist[i] = 0;
+  if (tid < kBins) hist[tid] = 0;
 #pragma unroll
   for (int j = 0; j < per; ++j) {
     l[j] = logit_of(l[j]);
     top = fmaxf(top, l[j]);
   }
   for (int d = 32; d > 0; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
-  if (lane_id() == 0) tops[wave_id()] = top;
+  if (lane_id() == 0) tops[wave] = top;
   __syncthreads();
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, tops[w]);
+  for (int w = 0; w < kWaves; ++w) top = fmaxf(top, tops[w]);
   const BinScale c = bin_scale(set.t == 0. ? 1. : set.t);
-  const double first = top > -__builtin_inff() ? __builtin_floor((double)top * c.hi) : 0.;
-  if (threadIdx.x == 0) {
+  const double first = top > -__builtin_inff() ? __builtin_rint((double)top * c.hi) : 0.;
+  if (tid == 0) {
     a.stat[at] = SliceStat{first, top, 0};
     a.cum_mass[at * kSums] = 0.;
     a.cum_count[at * kSums] = 0;
   }
   if (set.t == 0. || top == -__builtin_inff()) return;
-#pragma unroll
-  for (int j = 0; j < per; ++j) {
-    if (l[j] == -__builtin_inff()) continue;
-    const double ld = (double)l[j], hi = ld * c.hi, f = __builtin_floor(hi);
-    const double k = first - f;
+  // (a token that is none is infinitely far below)
+  auto add = [&](float v, auto far) {
+    const double ld = (double)v, hi = ld * c.hi, f = __builtin_rint(hi), k = first - f;
     if (k < (double)kBins) {
-      const double p = bin_mass(hi - f - 0.5 + t_low(ld, hi, c), kMassOne);
-      const uint64_t b = __builtin_bit_cast(uint64_t, p);
+      const double t = decltype(far)::value ? t_rest(ld, hi, f, c) : (hi - f) + t_low(ld, hi, c);
+      const uint64_t b = __builtin_bit_cast(uint64_t, bin_mass(t, kMassOne));
       atomicAdd(&hist[(int)k], (unsigned long long)((b & ((1ull << 52) - 1)) | (1ull << kCountBit)));
     }
+  };
+  if (__builtin_fabs(first) < 0x1p39) {        // every bin of the slice is below 2^40
+#pragma unroll
+    for (int j = 0; j < per; ++j) add(l[j], std::false_type{});
+  } else {
+    for (int j = 0; j < per; ++j) add(l[j], std::true_type{});
   }
   __syncthreads();
-  double mass_before = 0.;
-  uint32_t count_before = 0;
-  for (int base = 0; base < kBins; base += kBinThreads) {
-    const int k = base + threadIdx.x;
-    const uint64_t h = k < kBins ? hist[k] : 0;
-    double m = (double)(h & ((1ull << kCountBit) - 1)) * (1. / (double)(1ull << kMassStep)) *
-               exp(-(double)k * (1. / kBinScale));
-    uint32_t q = (uint32_t)(h >> kCountBit);
-    m = wave_scan(m);
-    q = wave_scan(q);
-    if (lane_id() == 63) { wave_mass[wave_id()] = m; wave_count[wave_id()] = q; }
-    __syncthreads();
-    double mb = mass_before;
-    uint32_t cb = count_before;
-    for (int w = 0; w < 4; ++w) {
-      if (w == wave_id()) { m += mb; q += cb; }
-      mb += wave_mass[w];
-      cb += wave_count[w];
-    }
-    mass_before = mb;
-    count_before = cb;
-    if (k < kBins) {
-      a.cum_mass[at * kSums + 1 + k] = m;
-      a.cum_count[at * kSums + 1 + k] = q;
-    }
-    __syncthreads();
+  static_assert(kBins <= kBinThreads && kBins % 64 == 0, "a thread per bin");
+  const uint64_t h = tid < kBins ? hist[tid] : 0;
+  double m = (double)(h & ((1ull << kCountBit) - 1)) * (1. / (double)(1ull << kMassStep)) *
+             bin_factor(tid);
+  uint32_t q = (uint32_t)(h >> kCountBit);
+  m = wave_scan(m);
+  q = wave_scan(q);
+  if (lane_id() == 63) { wave_mass[wave] = m; wave_count[wave] = q; }
+  __syncthreads();
+  if (tid >= kBins) return;
+  double before = 0.;
+  for (int w = 0; w < wave; ++w) {
+    before += wave_mass[w];
+    q += wave_count[w];
   }
+  a.cum_mass[at * kSums + 1 + tid] = before + m;
+  a.cum_count[at * kSums + 1 + tid] = q;
 }
 
 // One work-group per row, a thread per bin.
@@ -217,12 +219,12 @@ __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
     return;
   }
   const BinScale c = bin_scale(set.t);
-  const double t_top = (double)top * c.hi, f = __builtin_floor(t_top);
+  const double t_top = (double)top * c.hi, f = __builtin_rint(t_top);
   if (k < kSlices) {
-    const double d = f - st.floor_top;
+    const double d = f - st.top_bin;
     const int s = st.top > -__builtin_inff() && d < (double)kBins ? (int)d : kBins;
     shift[k] = s;
-    factor[k] = exp(-(double)s * (1. / kBinScale));
+    factor[k] = bin_factor(s);
   }
   __syncthreads();
   double m = 0.;
@@ -268,7 +270,7 @@ __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
   if (set.mp > 0.f) {
     const double edge = t_top + log((double)set.mp) * kBinScale;
     const double near = fmax(1. / (1 << 20), __builtin_fabs(t_top) * 0x1p-48);
-    const double m0 = f - __builtin_floor(edge + near), m1 = f - __builtin_floor(edge - near);
+    const double m0 = f - __builtin_rint(edge + near), m1 = f - __builtin_rint(edge - near);
     lo = min(lo, m0 < (double)kBins ? max((int)m0, 0) : kBins);
     hi = min(hi, m1 < (double)kBins ? max((int)m1, 0) : kBins);
   }
@@ -289,12 +291,14 @@ __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
     const int size = k < a.slices ? (first < kBins ? (int)(n1 - n0) : 0) + (extra >= 0 ? (int)(n3 - n2) : 0) : 0;
     const double base = k < a.slices ? before_a : 0.;
     const int end = wave_scan(size);
-    p.at[k + 1] = end;
+    if (k < kSlices) {
+      p.at[k + 1] = end;
+      p.base[k] = base;
+    }
     if (k == 0) p.at[0] = 0;
-    p.base[k] = base;
   }
   if (k == 0) {
-    p.head.floor_top = f;
+    p.head.top_bin = f;
     p.head.top = top;
     p.head.a = first;
     p.head.z = last;
@@ -311,7 +315,8 @@ __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
 }
 
 __global__ __launch_bounds__(kBinThreads) void k_sample_gather(const SplitArgs a) {
-  __shared__ int counts[64];
+  constexpr int kWaves = kBinThreads / 64;
+  __shared__ int counts[kSlice / 64];          // [step][wave]
   const int slice = blockIdx.x % a.slices, r = blockIdx.x / a.slices, row = a.row0 + r;
   const RowPlanS& plan = a.plan[r];
   const RowHead p = plan.head;
@@ -320,7 +325,7 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_gather(const SplitArgs a
   if (p.mode != 2 || from == to) return;
   const float* x = a.s.logits + row * a.s.ld + slice * kSlice;
   const int n = min(a.s.vocab - slice * kSlice, kSlice);
-  const double f = p.floor_top;
+  const double f = p.top_bin;
   const int first = p.a, last = p.z, extra = p.e, lane = lane_id(), wave = wave_id();
   constexpr int per = kSlice / kBinThreads;
   float l[per];
@@ -337,15 +342,17 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_gather(const SplitArgs a
     const bool mine = (k >= first && k <= last) || k == extra;
     in |= (uint32_t)mine << j;
     const uint64_t b = __ballot(mine);
-    if (lane == 0) counts[j * 4 + wave] = __builtin_popcountll(b);
+    if (lane == 0) counts[j * kWaves + wave] = __builtin_popcountll(b);
   }
   __syncthreads();
-  const int ends = wave_scan(counts[lane]);
+  static_assert(kSlice / 64 == 128, "two counts a lane");
+  const int c1 = counts[2 * lane + 1], both = wave_scan(counts[2 * lane] + c1);
 #pragma unroll
   for (int j = 0; j < per; ++j) {
     const bool mine = in >> j & 1;
     const uint64_t b = __ballot(mine);
-    const int end = __shfl(ends, j * 4 + wave);
+    const int place = j * kWaves + wave, pair = __shfl(both, place / 2), odd = __shfl(c1, place / 2);
+    const int end = place % 2 ? pair : pair - odd;
     if (mine) {
       const int pos = from + end - __builtin_popcountll(b) + __builtin_popcountll(b & ((1ull << lane) - 1));
       a.list[(int64_t)r * kListMax + pos] = make_uint2(
@@ -406,6 +413,7 @@ struct PickShared {
   uint16_t part_of[kListMax];
   uint64_t keys[kListMax];                   // a part's tokens in order
   unsigned long long part[kParts];           // sums up to a part
+  double factor[kBins];
   unsigned long long slice_mass[kSlices];
   double wave[kSampleWaves];
   uint64_t scan[kSampleWaves];
@@ -457,7 +465,7 @@ __device__ __forceinline__ int first_part(PickShared& sh, int from, int to, F re
 // Mass of the first `rank` ordered tokens, in the units of list_mass.
 __device__ __forceinline__ double mass_of_first(PickShared& sh, int rank, double f, BinScale c) {
   double s = 0.;
-  for (int i = threadIdx.x; i < rank; i += kPickThreads) s += list_mass(key_logit(sh.keys[i]), f, c);
+  for (int i = threadIdx.x; i < rank; i += kPickThreads) s += list_mass(key_logit(sh.keys[i]), f, c, sh.factor);
   for (int d = 32; d > 0; d /= 2) s += __shfl_xor(s, d);
   if (lane_id() == 0) sh.wave[wave_id()] = s;
   __syncthreads();
@@ -476,7 +484,7 @@ __device__ __forceinline__ int first_to_reach(PickShared& sh, double sum, double
   __syncthreads();
   for (int base = 0; base < n; base += kPickThreads) {
     const int i = base + threadIdx.x;
-    const double up = wave_scan(i < n ? list_mass(key_logit(sh.keys[i]), f, c) : 0.);
+    const double up = wave_scan(i < n ? list_mass(key_logit(sh.keys[i]), f, c, sh.factor) : 0.);
     if (lane_id() == 63) sh.wave[wave] = up;
     __syncthreads();
     double run = sum + up;
@@ -522,29 +530,31 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
     }
     return;
   }
-  const double base = lane < a.slices ? plan.base[lane] : 0.;
+  const double base = plan.base[min(lane, a.slices - 1)];
   const BinScale c = bin_scale(set.t);
-  const double f = p.floor_top;
+  const double f = p.top_bin;
   const int n = p.n, main = p.main;
   const uint2* list = a.list + (int64_t)r * kListMax;
   uint64_t cut = 0;                            // keys up to it are kept
   if (tid < kSlices) sh.slice_mass[tid] = 0;
+  if (tid < kBins) sh.factor[tid] = bin_factor(tid);
+  __syncthreads();
   constexpr uint64_t kMassMask = (1ull << kPartCount) - 1;
   constexpr double kStep = 1. / (double)(1ull << kMassStep);
-  const double to_mass = p.a < kBins ? exp(-(double)p.a * (1. / kBinScale)) * kStep : 0.;   // bin a's
+  const double to_mass = p.a < kBins ? sh.factor[p.a] * kStep : 0.;   // bin a's
   if (n > 0) {
     for (int i = tid; i < kParts; i += kPickThreads) sh.part[i] = 0;
     __syncthreads();
     const double scale = (double)kMainParts / (double)(p.z + 1 - p.a);
     // part and steps of a token
     auto place = [&](float l, uint64_t& steps) {
-      const double ld = (double)l, hi = ld * c.hi, fl = __builtin_floor(hi);
-      const double x = hi - fl + t_low(ld, hi, c);              // in the bin, about 0 .. 1
-      const int k = (int)(f - fl);
+      const double ld = (double)l, hi = ld * c.hi, bin = __builtin_rint(hi);
+      const double x = t_rest(ld, hi, bin, c);                  // in the bin, about -1/2 .. 1/2
+      const int k = (int)(f - bin);
       const bool extra = k > p.z;
-      const double y = 1. - __builtin_fmin(__builtin_fmax(x, 0.), 1.);
-      double rel = bin_mass(x - 0.5, kMassOne) - (kMassOne - 1.);
-      if (!extra && k != p.a) rel *= exp((double)(p.a - k) * (1. / kBinScale));
+      const double y = __builtin_fmin(__builtin_fmax(0.5 - x, 0.), 1.);
+      double rel = bin_mass(x, kMassOne) - (kMassOne - 1.);
+      if (!extra) rel *= sh.factor[k - p.a];
       steps = (uint64_t)__builtin_rint(rel * (double)(1ull << kMassStep));
       return extra ? kMainParts + min((int)(y * (kParts - kMainParts)), kParts - kMainParts - 1)
                    : min((int)(((double)(k - p.a) + y) * scale), kMainParts - 1);
@@ -599,7 +609,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
         const int pe = first_part(sh, kMainParts, kParts,
                                   [&](uint64_t v) { return (int)(v >> kPartCount) >= p.k_extra; });
         order_part(sh, n, pe);
-        mass_k += mass_to(pe, kMainParts) * exp(-(double)p.e * (1. / kBinScale)) * kStep +
+        mass_k += mass_to(pe, kMainParts) * sh.factor[p.e] * kStep +
                   mass_of_first(sh, p.k_extra - count_to(pe, kMainParts), f, c);
       } else if (mass_k < 0.) {
         const int rank = rank_of(p.k_main);
@@ -666,17 +676,25 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
     }
   }
   __syncthreads();
-  // the token in the slice
+  // the token in the slice: its logits through LDS, a thread's `per` of them in a row
   constexpr int per = kSlice / kPickThreads;
   const int first = sh.slice * kSlice, i0 = first + tid * per;
+  float* const logits = reinterpret_cast<float*>(sh.keys);
+  static_assert((kSlice + kPickThreads) * sizeof(float) <= sizeof(sh.keys), "a slice");
+#pragma unroll
+  for (int j = 0; j < per; ++j) {
+    const int i = j * kPickThreads + tid;
+    logits[i + i / per] = first + i < a.s.vocab ? x[first + i] : -__builtin_inff();
+  }
+  __syncthreads();
   double w[per], s = 0.;
 #pragma unroll
   for (int j = 0; j < per; ++j) {
     w[j] = 0.;
-    const float l = i0 + j < a.s.vocab ? logit_of(x[i0 + j]) : -__builtin_inff();
+    const float l = logit_of(logits[tid * (per + 1) + j]);
     if (l > -__builtin_inff()) {
       const int k = bin_of(l, f, c);
-      if (k < p.a || (k <= p.z && order_key(l, i0 + j) <= cut)) w[j] = list_mass(l, f, c);
+      if (k < p.a || (k <= p.z && order_key(l, i0 + j) <= cut)) w[j] = list_mass(l, f, c, sh.factor);
     }
     s += w[j];
   }
