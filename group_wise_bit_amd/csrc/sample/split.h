@@ -22,6 +22,7 @@ constexpr int kBins = 384;
 constexpr int kBinScale = 12;
 constexpr int kListMax = 8192;               // tokens that are gathered, at most
 constexpr int kBinThreads = 512;
+constexpr int kRankMax = 512;                // tokens whose order is found by comparing all
 constexpr int kSums = kBins + 1;             // a slice's sums: 0, then up to each bin
 
 struct SliceStat {
@@ -141,7 +142,7 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_bins(const SplitArgs a) 
     l[j] = i < n ? x[i] : -__builtin_inff();
   }
   const SampleRow set = sample_row(a.s, row);
-  if (tid < kBins) hist[tid] = 0;
+  for (int i = tid; i < kBins; i += kBinThreads) hist[i] = 0;
 #pragma unroll
   for (int j = 0; j < per; ++j) {
     l[j] = logit_of(l[j]);
@@ -175,23 +176,33 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_bins(const SplitArgs a) 
     for (int j = 0; j < per; ++j) add(l[j], std::true_type{});
   }
   __syncthreads();
-  static_assert(kBins <= kBinThreads && kBins % 64 == 0, "a thread per bin");
-  const uint64_t h = tid < kBins ? hist[tid] : 0;
-  double m = (double)(h & ((1ull << kCountBit) - 1)) * (1. / (double)(1ull << kMassStep)) *
-             bin_factor(tid);
-  uint32_t q = (uint32_t)(h >> kCountBit);
-  m = wave_scan(m);
-  q = wave_scan(q);
-  if (lane_id() == 63) { wave_mass[wave] = m; wave_count[wave] = q; }
-  __syncthreads();
-  if (tid >= kBins) return;
-  double before = 0.;
-  for (int w = 0; w < wave; ++w) {
-    before += wave_mass[w];
-    q += wave_count[w];
+  double mass_before = 0.;
+  uint32_t count_before = 0;
+#pragma unroll
+  for (int base = 0; base < kBins; base += kBinThreads) {
+    const int k = base + tid;
+    const uint64_t h = k < kBins ? hist[k] : 0;
+    double m = wave_scan((double)(h & ((1ull << kCountBit) - 1)) * (1. / (double)(1ull << kMassStep)) *
+                         bin_factor(k));
+    uint32_t q = wave_scan((uint32_t)(h >> kCountBit));
+    if (lane_id() == 63) { wave_mass[wave] = m; wave_count[wave] = q; }
+    __syncthreads();
+    double mb = mass_before;
+    uint32_t cb = count_before;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w == wave) { m += mb; q += cb; }
+      mb += wave_mass[w];
+      cb += wave_count[w];
+    }
+    mass_before = mb;
+    count_before = cb;
+    if (k < kBins) {
+      a.cum_mass[at * kSums + 1 + k] = m;
+      a.cum_count[at * kSums + 1 + k] = q;
+    }
+    __syncthreads();
   }
-  a.cum_mass[at * kSums + 1 + tid] = before + m;
-  a.cum_count[at * kSums + 1 + tid] = q;
 }
 
 // One work-group per row, a thread per bin.
@@ -275,11 +286,13 @@ __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
     hi = min(hi, m1 < (double)kBins ? max((int)m1, 0) : kBins);
   }
   // (nothing lies beyond the last bin)
-  const int first = lo, last = min(hi, kBins - 1);
+  const int last = min(hi, kBins - 1);
   const int extra = cut_p && cut_k && !whole && bk > last ? bk : -1;
+  const int more = extra >= 0 ? (int)(count[extra] - count[extra - 1]) : 0;
+  // few tokens in all: those before the cuts' bins too, and the draw is made from the list
+  const int first = lo < kBins && (int)count[last] + more <= kRankMax ? 0 : lo;
   const uint32_t before = first > 0 ? count[first - 1] : 0u;
   const int main = first < kBins ? (int)(count[last] - before) : 0;
-  const int more = extra >= 0 ? (int)(count[extra] - count[extra - 1]) : 0;
   if (k < 64) {
     // (bins before the slice's first: its first sum, 0)
     const int slice = min(k, a.slices - 1), s = shift[slice];
@@ -418,8 +431,25 @@ struct PickShared {
   double wave[kSampleWaves];
   uint64_t scan[kSampleWaves];
   double before, target, total;
+  uint64_t cut;
   int slice, count[3], size, at, rank;
 };
+
+// Sums of v over the threads up to this one; over all in sh.total.
+__device__ __forceinline__ double sum_before(PickShared& sh, double v) {
+  const int wave = wave_id();
+  double up = wave_scan(v), all = 0.;
+  if (lane_id() == 63) sh.wave[wave] = up;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSampleWaves; ++w) {
+    if (w == wave) up += all;
+    all += sh.wave[w];
+  }
+  if (threadIdx.x == 0) sh.total = all;
+  __syncthreads();
+  return up;
+}
 
 // The tokens of a part in order: sh.keys[0 .. sh.size).
 __device__ __forceinline__ void order_part(PickShared& sh, int n, int part) {
@@ -536,13 +566,81 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
   const int n = p.n, main = p.main;
   const uint2* list = a.list + (int64_t)r * kListMax;
   uint64_t cut = 0;                            // keys up to it are kept
-  if (tid < kSlices) sh.slice_mass[tid] = 0;
-  if (tid < kBins) sh.factor[tid] = bin_factor(tid);
-  __syncthreads();
   constexpr uint64_t kMassMask = (1ull << kPartCount) - 1;
   constexpr double kStep = 1. / (double)(1ull << kMassStep);
+  const double top_hi = (double)p.top * c.hi, top_lo = t_low((double)p.top, top_hi, c);
+  // p of a token relative to the largest one's
+  auto relative = [&](float l) {
+    const double hi = (double)l * c.hi;
+    return exp((hi - top_hi + (t_low((double)l, hi, c) - top_lo)) * (1. / kBinScale));
+  };
+  if (n > 0 && n <= kRankMax) {
+    // a token per thread, and its place in the order
+    const uint2 t = tid < n ? list[tid] : make_uint2(0, 0);
+    const float l = __builtin_bit_cast(float, t.y);
+    const uint64_t key = order_key(l, t.x);
+    if (tid < n) sh.keys[tid] = key;
+    __syncthreads();
+    int rank = 0;
+    double m = 0.;
+    if (wave_id() * 64 < n) {
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) rank += sh.keys[j] < key;
+      const double ld = (double)l, hi = ld * c.hi, bin = __builtin_rint(hi);
+      m = (bin_mass(t_rest(ld, hi, bin, c), kMassOne) - (kMassOne - 1.)) * bin_factor((int)(f - bin));
+    }
+    __syncthreads();
+    double* const sums = reinterpret_cast<double*>(sh.keys);      // of the order's first tokens
+    if (tid < n) sums[rank] = m;
+    __syncthreads();
+    const double up = sum_before(sh, tid < n ? sums[tid] : 0.);
+    if (tid < n) sums[tid] = up;
+    __syncthreads();
+    int kept = p.k_main;
+    if (set.p < 1.f) {
+      const double mass_k = p.e >= 0 ? p.mass_k + sums[main + p.k_extra - 1] - (main > 0 ? sums[main - 1] : 0.)
+                            : p.mass_k < 0. ? p.mass_a + sums[p.k_main - 1] : p.mass_k;
+      const double target = (double)set.p * mass_k;
+      kept = min(kept, 1 + __syncthreads_count(tid < main && p.mass_a + sums[tid] < target));
+    }
+    if (set.mp > 0.f)
+      kept = min(kept, __syncthreads_count(tid < n && rank < main &&
+                                           (l == p.top || relative(l) >= (double)set.mp)));
+    const bool mine = tid < n && rank < kept;
+    if (p.a == 0) {
+      // all kept tokens are here, in the order of the vocabulary
+      const double w = mine ? m : 0., end = sum_before(sh, w), total = sh.total;
+      const bool past = mine && end > (double)set.u * total;
+      if (tid == 0) {
+        sh.count[0] = 0x7FFFFFFF;
+        sh.count[1] = -1;
+      }
+      __syncthreads();
+      const uint64_t hits = __ballot(past), tails = __ballot(mine);
+      if (lane == 0 && hits != 0) atomicMin(&sh.count[0], tid + __builtin_ctzll(hits));
+      if (lane == 0 && tails != 0) atomicMax(&sh.count[1], tid + 63 - __builtin_clzll(tails));
+      __syncthreads();
+      // (every p is above 0 here: the last one is that of a u near 1)
+      if (tid == min(sh.count[0], sh.count[1])) {
+        a.s.ids[row] = t.x;
+        if (a.s.probs != nullptr) a.s.probs[row] = (float)(w / total);
+      }
+      return;
+    }
+    if (tid < kSlices) sh.slice_mass[tid] = 0;
+    if (tid < kBins) sh.factor[tid] = bin_factor(tid);
+    if (mine && rank == kept - 1) sh.cut = key;
+    __syncthreads();
+    if (kept > 0) cut = sh.cut;
+    if (mine) atomicAdd(&sh.slice_mass[t.x / kSlice],
+                        (unsigned long long)__builtin_rint(m / (sh.factor[p.a] * kStep)));
+  } else {
+    if (tid < kSlices) sh.slice_mass[tid] = 0;
+    if (tid < kBins) sh.factor[tid] = bin_factor(tid);
+  }
+  __syncthreads();
   const double to_mass = p.a < kBins ? sh.factor[p.a] * kStep : 0.;   // bin a's
-  if (n > 0) {
+  if (n > kRankMax) {
     for (int i = tid; i < kParts; i += kPickThreads) sh.part[i] = 0;
     __syncthreads();
     const double scale = (double)kMainParts / (double)(p.z + 1 - p.a);
@@ -627,15 +725,11 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
       }
     }
     if (set.mp > 0.f) {
-      const double top_hi = (double)p.top * c.hi, top_lo = t_low((double)p.top, top_hi, c);
       int pass = 0;
 #pragma unroll 1
-      for (int i = tid; i < n; i += kPickThreads) {
-        if (sh.part_of[i] >= kMainParts) continue;
-        const double l = (double)sh.l[i], hi = l * c.hi;
-        const double e = (hi - top_hi + (t_low(l, hi, c) - top_lo)) * (1. / kBinScale);
-        pass += sh.l[i] == p.top || exp(e) >= (double)set.mp;
-      }
+      for (int i = tid; i < n; i += kPickThreads)
+        if (sh.part_of[i] < kMainParts)
+          pass += sh.l[i] == p.top || relative(sh.l[i]) >= (double)set.mp;
       for (int d = 32; d > 0; d /= 2) pass += __shfl_xor(pass, d);
       if (threadIdx.x == 0) sh.count[0] = 0;
       __syncthreads();
@@ -687,15 +781,16 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
     logits[i + i / per] = first + i < a.s.vocab ? x[first + i] : -__builtin_inff();
   }
   __syncthreads();
+  const int limit = cut == 0 ? p.a : p.z + 1;
   double w[per], s = 0.;
 #pragma unroll
   for (int j = 0; j < per; ++j) {
     w[j] = 0.;
     const float l = logit_of(logits[tid * (per + 1) + j]);
-    if (l > -__builtin_inff()) {
-      const int k = bin_of(l, f, c);
-      if (k < p.a || (k <= p.z && order_key(l, i0 + j) <= cut)) w[j] = list_mass(l, f, c, sh.factor);
-    }
+    // (tokens of the bins before a come before any of the list)
+    const bool in = cut != 0 && cut != ~0ull ? order_key(l, i0 + j) <= cut
+                                             : l > -__builtin_inff() && bin_of(l, f, c) < limit;
+    if (in) w[j] = list_mass(l, f, c, sh.factor);
     s += w[j];
   }
   const double up = wave_scan(s);
@@ -703,13 +798,22 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
   __syncthreads();
   double run = sh.before + (up - s);
   for (int v = 0; v < wave_id(); ++v) run += sh.wave[v];
+  int hit = 0x7FFFFFFF, tail = -1;             // the first beyond the target, the last of all
 #pragma unroll
   for (int j = 0; j < per; ++j) {
     run += w[j];
     if (w[j] > 0.) {
-      if (run > sh.target) atomicMin(&sh.count[0], i0 + j);
-      atomicMax(&sh.count[2], i0 + j);
+      if (run > sh.target) hit = min(hit, i0 + j);
+      tail = i0 + j;
     }
+  }
+  for (int d = 32; d > 0; d /= 2) {
+    hit = min(hit, __shfl_xor(hit, d));
+    tail = max(tail, __shfl_xor(tail, d));
+  }
+  if (lane == 0) {
+    atomicMin(&sh.count[0], hit);
+    atomicMax(&sh.count[2], tail);
   }
   __syncthreads();
   const int id = sh.count[0] != 0x7FFFFFFF ? sh.count[0] : sh.count[2];
