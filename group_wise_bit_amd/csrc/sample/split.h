@@ -79,16 +79,24 @@ __device__ __forceinline__ double t_rest(double l, double hi, double bin, BinSca
   return __builtin_fabs(bin) < 0x1p40 ? x : 0.;
 }
 
-// exp(x / 12) - 1 + one for |x| <= 1/2 (and a little beyond): x^7 / (12^7 7!) < 2^-44.
-__device__ __forceinline__ double bin_mass(double x, double one) {
+// exp(x / 12) - 1 + one for |x| <= 1/2 (and a little beyond): x^7 / (12^7 7!) < 2^-44.  The
+// coefficients are kept in registers (as constants each would be moved before its fma).
+struct MassPoly {
+  double c[7];
+};
+__device__ __forceinline__ MassPoly mass_poly(double one) {
   constexpr double s = 1. / kBinScale;
-  double p = s * s * s * s * s * s / 720;
-  p = __builtin_fma(p, x, s * s * s * s * s / 120);
-  p = __builtin_fma(p, x, s * s * s * s / 24);
-  p = __builtin_fma(p, x, s * s * s / 6);
-  p = __builtin_fma(p, x, s * s / 2);
-  p = __builtin_fma(p, x, s);
-  return __builtin_fma(p, x, one);
+  MassPoly p{{one, s, s * s / 2, s * s * s / 6, s * s * s * s / 24, s * s * s * s * s / 120,
+              s * s * s * s * s * s / 720}};
+#pragma unroll
+  for (int i = 0; i < 7; ++i) asm("" : "+v"(p.c[i]));
+  return p;
+}
+__device__ __forceinline__ double bin_mass(double x, const MassPoly& k) {
+  double p = k.c[6];
+#pragma unroll
+  for (int i = 5; i >= 0; --i) p = __builtin_fma(p, x, k.c[i]);
+  return p;
 }
 // Masses within a bin are whole numbers of 2^-34: sums of 2^18 equal ones are exact, and
 // the sums of histograms and of lists are sums of the same numbers.
@@ -97,9 +105,10 @@ constexpr double kMassOne = 1. + (double)(1 << (52 - kMassStep));
 
 // Mass of a logit relative to the middle of the bin `top`, with the factors of the bins from
 // there on.
-__device__ __forceinline__ double list_mass(float l, double top, BinScale c, const double* factor) {
+__device__ __forceinline__ double list_mass(float l, double top, BinScale c, const double* factor,
+                                            const MassPoly& poly) {
   const double ld = (double)l, hi = ld * c.hi, f = __builtin_rint(hi), k = top - f;
-  const double p = bin_mass(t_rest(ld, hi, f, c), kMassOne) - (kMassOne - 1.);
+  const double p = bin_mass(t_rest(ld, hi, f, c), poly) - (kMassOne - 1.);
   return k < (double)kBins ? p * factor[(int)k] : 0.;
 }
 __device__ __forceinline__ double bin_factor(int k) { return exp(-(double)k * (1. / kBinScale)); }
@@ -160,12 +169,13 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_bins(const SplitArgs a) 
     a.cum_count[at * kSums] = 0;
   }
   if (set.t == 0. || top == -__builtin_inff()) return;
+  const MassPoly poly = mass_poly(kMassOne);
   // (a token that is none is infinitely far below)
   auto add = [&](float v, auto far) {
     const double ld = (double)v, hi = ld * c.hi, f = __builtin_rint(hi), k = first - f;
     if (k < (double)kBins) {
       const double t = decltype(far)::value ? t_rest(ld, hi, f, c) : (hi - f) + t_low(ld, hi, c);
-      const uint64_t b = __builtin_bit_cast(uint64_t, bin_mass(t, kMassOne));
+      const uint64_t b = __builtin_bit_cast(uint64_t, bin_mass(t, poly));
       atomicAdd(&hist[(int)k], (unsigned long long)((b & ((1ull << 52) - 1)) | (1ull << kCountBit)));
     }
   };
@@ -173,6 +183,7 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_bins(const SplitArgs a) 
 #pragma unroll
     for (int j = 0; j < per; ++j) add(l[j], std::false_type{});
   } else {
+#pragma unroll
     for (int j = 0; j < per; ++j) add(l[j], std::true_type{});
   }
   __syncthreads();
@@ -493,9 +504,10 @@ __device__ __forceinline__ int first_part(PickShared& sh, int from, int to, F re
 }
 
 // Mass of the first `rank` ordered tokens, in the units of list_mass.
-__device__ __forceinline__ double mass_of_first(PickShared& sh, int rank, double f, BinScale c) {
+__device__ __forceinline__ double mass_of_first(PickShared& sh, int rank, double f, BinScale c,
+                                                const MassPoly& poly) {
   double s = 0.;
-  for (int i = threadIdx.x; i < rank; i += kPickThreads) s += list_mass(key_logit(sh.keys[i]), f, c, sh.factor);
+  for (int i = threadIdx.x; i < rank; i += kPickThreads) s += list_mass(key_logit(sh.keys[i]), f, c, sh.factor, poly);
   for (int d = 32; d > 0; d /= 2) s += __shfl_xor(s, d);
   if (lane_id() == 0) sh.wave[wave_id()] = s;
   __syncthreads();
@@ -508,13 +520,13 @@ __device__ __forceinline__ double mass_of_first(PickShared& sh, int rank, double
 // How many of the ordered tokens it takes until `sum` and their masses reach `target` (all of
 // them if they do not; 1 at least).
 __device__ __forceinline__ int first_to_reach(PickShared& sh, double sum, double target, double f,
-                                              BinScale c) {
+                                              BinScale c, const MassPoly& poly) {
   const int n = sh.size, wave = wave_id();
   if (threadIdx.x == 0) sh.rank = n > 0 ? n : 1;
   __syncthreads();
   for (int base = 0; base < n; base += kPickThreads) {
     const int i = base + threadIdx.x;
-    const double up = wave_scan(i < n ? list_mass(key_logit(sh.keys[i]), f, c, sh.factor) : 0.);
+    const double up = wave_scan(i < n ? list_mass(key_logit(sh.keys[i]), f, c, sh.factor, poly) : 0.);
     if (lane_id() == 63) sh.wave[wave] = up;
     __syncthreads();
     double run = sum + up;
@@ -563,6 +575,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
   const double base = plan.base[min(lane, a.slices - 1)];
   const BinScale c = bin_scale(set.t);
   const double f = p.top_bin;
+  const MassPoly poly = mass_poly(kMassOne);
   const int n = p.n, main = p.main;
   const uint2* list = a.list + (int64_t)r * kListMax;
   uint64_t cut = 0;                            // keys up to it are kept
@@ -587,7 +600,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
 #pragma unroll 8
       for (int j = 0; j < n; ++j) rank += sh.keys[j] < key;
       const double ld = (double)l, hi = ld * c.hi, bin = __builtin_rint(hi);
-      m = (bin_mass(t_rest(ld, hi, bin, c), kMassOne) - (kMassOne - 1.)) * bin_factor((int)(f - bin));
+      m = (bin_mass(t_rest(ld, hi, bin, c), poly) - (kMassOne - 1.)) * bin_factor((int)(f - bin));
     }
     __syncthreads();
     double* const sums = reinterpret_cast<double*>(sh.keys);      // of the order's first tokens
@@ -651,7 +664,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
       const int k = (int)(f - bin);
       const bool extra = k > p.z;
       const double y = __builtin_fmin(__builtin_fmax(0.5 - x, 0.), 1.);
-      double rel = bin_mass(x, kMassOne) - (kMassOne - 1.);
+      double rel = bin_mass(x, poly) - (kMassOne - 1.);
       if (!extra) rel *= sh.factor[k - p.a];
       steps = (uint64_t)__builtin_rint(rel * (double)(1ull << kMassStep));
       return extra ? kMainParts + min((int)(y * (kParts - kMainParts)), kParts - kMainParts - 1)
@@ -708,10 +721,10 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
                                   [&](uint64_t v) { return (int)(v >> kPartCount) >= p.k_extra; });
         order_part(sh, n, pe);
         mass_k += mass_to(pe, kMainParts) * sh.factor[p.e] * kStep +
-                  mass_of_first(sh, p.k_extra - count_to(pe, kMainParts), f, c);
+                  mass_of_first(sh, p.k_extra - count_to(pe, kMainParts), f, c, poly);
       } else if (mass_k < 0.) {
         const int rank = rank_of(p.k_main);
-        mass_k = p.mass_a + mass_to(held, 0) * to_mass + mass_of_first(sh, rank, f, c);
+        mass_k = p.mass_a + mass_to(held, 0) * to_mass + mass_of_first(sh, rank, f, c, poly);
       }
       // the token with which the sum reaches the target (by rounding there may be none: all)
       const double target = (double)set.p * mass_k;
@@ -721,7 +734,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
         if (held != pp) order_part(sh, n, pp);
         held = pp;
         kept = min(kept, count_to(pp, 0) + first_to_reach(sh, p.mass_a + mass_to(pp, 0) * to_mass,
-                                                          target, f, c));
+                                                          target, f, c, poly));
       }
     }
     if (set.mp > 0.f) {
@@ -790,7 +803,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
     // (tokens of the bins before a come before any of the list)
     const bool in = cut != 0 && cut != ~0ull ? order_key(l, i0 + j) <= cut
                                              : l > -__builtin_inff() && bin_of(l, f, c) < limit;
-    if (in) w[j] = list_mass(l, f, c, sh.factor);
+    if (in) w[j] = list_mass(l, f, c, sh.factor, poly);
     s += w[j];
   }
   const double up = wave_scan(s);
