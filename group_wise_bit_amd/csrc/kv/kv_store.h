@@ -93,65 +93,108 @@ __device__ __forceinline__ int kv_page(const KvSeqs& s, const KvSpan& sp) {
   return page >= 0 && page < s.pages ? page : -1;
 }
 
-template <int CTRL>
-__device__ __forceinline__ float mov_dpp(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF,
-                                                            0xF, true));
+// The range of a group: two fp16 numbers min(w, 0) and min(-w, 0) over its values, the first
+// -inf if one of them is not finite.  (v_pk_min_f16 of two numbers; of a NaN the other one.)
+constexpr uint32_t kBadRange = 0x0000FC00u;
+__device__ __forceinline__ uint32_t pk_min(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("v_pk_min_f16 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
 }
-// Minimum over the 16 lanes of a row (pairs, quads, mirrors of 8 and 16), and over
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("v_pk_max_f16 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ uint32_t range_of(const uint32_t (&w)[N]) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  uint32_t lo = 0, hi = 0;
+  u16x2 size{};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    lo = pk_min(lo, w[i]);
+    hi = pk_max(hi, w[i]);
+    const uint32_t m = w[i] & 0x7FFF7FFFu;
+    size = __builtin_elementwise_max(size, __builtin_bit_cast(u16x2, m));
+  }
+  const uint32_t nhi = hi ^ 0x80008000u;
+  // (lo, -hi) of the even values, of the odd ones
+  const uint32_t r = pk_min(__builtin_amdgcn_perm(nhi, lo, 0x05040100u),
+                            __builtin_amdgcn_perm(nhi, lo, 0x07060302u));
+  return max((int)size[0], (int)size[1]) >= 0x7C00 ? kBadRange : r;
+}
+// The least over the 16 lanes of a row (pairs, quads, mirrors of 8 and 16), and over
 // the four lanes l, l ^ 16, l ^ 32, l ^ 48.
-__device__ __forceinline__ float row_min(float v) {
-  v = fminf(v, mov_dpp<0xB1>(v));
-  v = fminf(v, mov_dpp<0x4E>(v));
-  v = fminf(v, mov_dpp<0x141>(v));
-  return fminf(v, mov_dpp<0x140>(v));
+template <int CTRL>
+__device__ __forceinline__ uint32_t mov_dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
 }
-__device__ __forceinline__ float quarter_min(float v) {
-  v = fminf(v, __shfl_xor(v, 16));
-  return fminf(v, __shfl_xor(v, 32));
+__device__ __forceinline__ uint32_t row_min(uint32_t v) {
+  v = pk_min(v, mov_dpp<0xB1>(v));
+  v = pk_min(v, mov_dpp<0x4E>(v));
+  v = pk_min(v, mov_dpp<0x141>(v));
+  return pk_min(v, mov_dpp<0x140>(v));
+}
+__device__ __forceinline__ uint32_t quarter_min(uint32_t v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  v = pk_min((uint32_t)a[0], (uint32_t)a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return pk_min((uint32_t)b[0], (uint32_t)b[1]);
 }
 
-// A group's rounding from lo = min(w, 0), or -inf for a group that is not finite, and nhi =
-// -max(w, 0).
+// A group's rounding from its range.
 struct KvGroup {
   RtnParams p;
   uint16_t scale;
-  int zero;
+  float zero;
 };
+// Quotients correctly rounded by one step from y = 1 / b (Markstein): q = a y, r = a - b q
+// exactly, q + r y is a / b rounded if y is 1 / b rounded; and 1 / b itself from a y within
+// one unit of it, for a b whose fraction is not all ones (15, 255, an fp16 number).
 template <int BITS>
-__device__ __forceinline__ KvGroup kv_group(float lo, float nhi) {
+__device__ __forceinline__ KvGroup kv_group(uint32_t range) {
   constexpr int qmax = (1 << BITS) - 1;
+  const float lo = (float)as_h2(range)[0], nhi = (float)as_h2(range)[1];
   KvGroup g;
-  if (lo < -65504.f) {
-    g.p = rtn_params(0.f, 0, qmax);
-    g.scale = 0x7E00;
-    g.zero = 0;
-    return g;
-  }
-  const f16 s = (f16)__fdiv_rn(-nhi - lo, (float)qmax);
-  g.scale = __builtin_bit_cast(uint16_t, s);
-  g.zero = 0;
-  g.p = rtn_params((float)s, 0, qmax);
-  if ((float)s != 0.f) {
-    // (the quotient of two fp16 numbers, as a weight's: -lo is one of the values)
-    const float z = rtn_fix(-lo, __builtin_rintf(-lo * g.p.r), g.p);
-    g.zero = (int)clampf(z, 0.f, (float)qmax);
-    g.p = rtn_params((float)s, g.zero, qmax);
-  }
+  const bool bad = lo < -65504.f;
+  constexpr float y = 1.f / qmax;
+  const float d = -nhi - lo, q0 = d * y;
+  const f16 s16 = (f16)__builtin_fmaf(__builtin_fmaf(-q0, (float)qmax, d), y, q0);
+  const float s = bad ? 0.f : (float)s16;
+  g.scale = bad ? (uint16_t)0x7E00 : __builtin_bit_cast(uint16_t, s16);
+  const float r0 = __builtin_amdgcn_rcpf(s);
+  const float r = __builtin_fmaf(__builtin_fmaf(-s, r0, 1.f), r0, r0);
+  const bool none = s == 0.f;
+  g.p.s = s;
+  g.p.r = none ? 0.f : r;
+  g.p.hs = none ? -1.f : 0.5f * s;
+  // (the quotient of two fp16 numbers, as a value's: -lo is one of them)
+  const float z = none ? 0.f : rtn_fix(-lo, __builtin_rintf(-lo * g.p.r), g.p);
+  g.zero = clampf(z, 0.f, (float)qmax);
+  g.p.lo = -g.zero;
+  g.p.hi = none ? 0.f : (float)qmax - g.zero;
   return g;
 }
-__device__ __forceinline__ uint32_t kv_code(f16 w, const KvGroup& g) {
-  if (g.p.s == 0.f) return 0;
-  const float q = rtn_fix((float)w, __builtin_rintf((float)w * g.p.r), g.p);
-  return (uint32_t)((int)clampf(q, g.p.lo, g.p.hi) + g.zero);
+// Values of a pair rounded, with whether one of them is a tie (rtn_fix is then due).
+__device__ __forceinline__ bool kv_round(uint32_t pair, const KvGroup& g, float (&q)[2]) {
+  bool tie = false;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    bool t;
+    q[i] = rtn_raw((float)as_h2(pair)[i], g.p, t);
+    tie |= t;
+  }
+  return tie;
 }
-
-// One value's part in its group's (lo, nhi): a value that is not finite makes lo -inf.
-__device__ __forceinline__ void kv_range(f16 w, float& lo, float& nhi) {
-  const float x = (float)w;
-  const bool ok = __builtin_fabsf(x) <= 65504.f;
-  lo = ok ? fminf(lo, x) : -__builtin_inff();
-  nhi = ok ? fminf(nhi, -x) : nhi;
+__device__ __forceinline__ void kv_fix(uint32_t pair, const KvGroup& g, float (&q)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) q[i] = rtn_fix((float)as_h2(pair)[i], q[i], g.p);
+}
+// The code of a rounded value, into byte B of `to`.
+template <int B>
+__device__ __forceinline__ uint32_t kv_byte(float q, const KvGroup& g, uint32_t to) {
+  return __builtin_amdgcn_cvt_pk_u8_f32(clampf(q, g.p.lo, g.p.hi) + g.zero, B, to);
 }
 
 // One wave per (tile, head, keys or values), and per half tile of keys / group of
@@ -180,23 +223,43 @@ __device__ __forceinline__ void kv_store_tile(const KvStoreArgs& a, const KvSpan
         w[1] = *(const f16x8*)(src + 64 * c + 8);
       }
       constexpr int words = BITS / 2;          // of 16 codes
-      uint32_t out[words];
+      uint32_t out[words], pair[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const u32x4 four = __builtin_bit_cast(u32x4, w[i / 4]);
+        pair[i] = four[i % 4];
+      }
       if constexpr (BITS == 16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = __builtin_bit_cast(u32x4, w[i / 4])[i % 4];
+        for (int i = 0; i < 8; ++i) out[i] = pair[i];
       } else {
-        float lo = 0.f, nhi = 0.f;
+        const KvGroup q = kv_group<BITS>(quarter_min(range_of(pair)));
+        float v[8][2];
+        bool tie = false;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) kv_range(w[i / 8][i % 8], lo, nhi);
-        const KvGroup q = kv_group<BITS>(quarter_min(lo), quarter_min(nhi));
-        constexpr int per = 32 / BITS;
+        for (int i = 0; i < 8; ++i) tie |= kv_round(pair[i], q, v[i]);
+        if (__ballot(tie) != 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) kv_fix(pair[i], q, v[i]);
+        }
+        // code i of a word at bit 16 (i % 2) + BITS (i / 2)
 #pragma unroll
         for (int i = 0; i < words; ++i) {
-          out[i] = 0;
-#pragma unroll
-          for (int j = 0; j < per; ++j) {
-            const int e = i * per + j;
-            out[i] |= kv_code(w[e / 8][e % 8], q) << (16 * (j % 2) + BITS * (j / 2));
+          constexpr int per = 16 / BITS;       // pairs of a word
+          uint32_t even = 0, odd = 0;          // (4 bits) bytes of pairs 0 and 2, of 1 and 3
+          even = kv_byte<0>(v[i * per][0], q, even);
+          even = kv_byte<2>(v[i * per][1], q, even);
+          if constexpr (BITS == 8) {
+            even = kv_byte<1>(v[i * per + 1][0], q, even);
+            out[i] = kv_byte<3>(v[i * per + 1][1], q, even);
+          } else {
+            odd = kv_byte<0>(v[i * per + 1][0], q, odd);
+            odd = kv_byte<2>(v[i * per + 1][1], q, odd);
+            even = kv_byte<1>(v[i * per + 2][0], q, even);
+            even = kv_byte<3>(v[i * per + 2][1], q, even);
+            odd = kv_byte<1>(v[i * per + 3][0], q, odd);
+            odd = kv_byte<3>(v[i * per + 3][1], q, odd);
+            out[i] = even | odd << 4;
           }
         }
         if (mine && g == 0) {
@@ -217,39 +280,69 @@ __device__ __forceinline__ void kv_store_tile(const KvStoreArgs& a, const KvSpan
       }
     }
   } else {
-    typedef f16 f16x4 __attribute__((ext_vector_type(4)));
     constexpr int n = 16 / BITS;               // codes of a half-word
     const int g = lane >> 4, y = lane & 15, c = part;
-    f16x4 w[8];
+    u32x2 w[8];
     bool mine[8];
 #pragma unroll
     for (int t = 0; t < 8; ++t) {              // tokens 4 g + t of the first half, then the second
       const int64_t p = p0 + (t >> 2) * 16 + 4 * g + (t & 3);
       mine[t] = p >= sp.first && p < sp.end;
-      w[t] = f16x4{};
-      if (mine[t]) w[t] = *(const f16x4*)(a.x[1] + (sp.row0 + p) * a.ldx[1] + head * D + c * 64 + 4 * y);
+      w[t] = u32x2{0, 0};
+      if (mine[t]) w[t] = *(const u32x2*)(a.x[1] + (sp.row0 + p) * a.ldx[1] + head * D + c * 64 + 4 * y);
     }
-    uint32_t out[4 / n][4] = {};               // [part of 4 dims][pair of tokens]
+    uint32_t out[4 / n][4];                  // [part of 4 dims][pair of tokens]
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      uint32_t code[4];
+    for (int u = 0; u < 4; ++u) {              // tokens 2 u (low halves) and 2 u + 1
+      const uint32_t pair[2][2] = {{w[2 * u][0], w[2 * u][1]}, {w[2 * u + 1][0], w[2 * u + 1][1]}};
       if constexpr (BITS == 16) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) code[j] = __builtin_bit_cast(uint16_t, (f16)w[t][j]);
+        out[0][u] = __builtin_amdgcn_perm(pair[1][0], pair[0][0], 0x05040100u);
+        out[1][u] = __builtin_amdgcn_perm(pair[1][0], pair[0][0], 0x07060302u);
+        out[2][u] = __builtin_amdgcn_perm(pair[1][1], pair[0][1], 0x05040100u);
+        out[3][u] = __builtin_amdgcn_perm(pair[1][1], pair[0][1], 0x07060302u);
       } else {
-        float lo = 0.f, nhi = 0.f;
+        float v[2][2][2];                      // [token][pair][value]
+        KvGroup q[2];
+        bool tie = false;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) kv_range(w[t][j], lo, nhi);
-        const KvGroup q = kv_group<BITS>(row_min(lo), row_min(nhi));
+        for (int k = 0; k < 2; ++k) {
+          q[k] = kv_group<BITS>(row_min(range_of(pair[k])));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) code[j] = kv_code(w[t][j], q);
-        if (mine[t] && y == 0) {
-          scales[c * 32 + g * 8 + t] = q.scale;
-          zeros[(g * G + c) * 8 + t] = (uint8_t)q.zero;
+          for (int i = 0; i < 2; ++i) tie |= kv_round(pair[k][i], q[k], v[k][i]);
         }
-      }
+        if (__ballot(tie) != 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) out[j / n][t / 2] |= code[j] << (16 * (t % 2) + BITS * (j % n));
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) kv_fix(pair[k][i], q[k], v[k][i]);
+        }
+        if constexpr (BITS == 8) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t o = kv_byte<0>(v[0][i][0], q[0], 0);
+            o = kv_byte<1>(v[0][i][1], q[0], o);
+            o = kv_byte<2>(v[1][i][0], q[1], o);
+            out[i][u] = kv_byte<3>(v[1][i][1], q[1], o);
+          }
+        } else {
+          uint32_t even = 0, odd = 0;          // bytes of dims 0 and 2, of 1 and 3
+          even = kv_byte<0>(v[0][0][0], q[0], even);
+          odd = kv_byte<0>(v[0][0][1], q[0], odd);
+          even = kv_byte<1>(v[0][1][0], q[0], even);
+          odd = kv_byte<1>(v[0][1][1], q[0], odd);
+          even = kv_byte<2>(v[1][0][0], q[1], even);
+          odd = kv_byte<2>(v[1][0][1], q[1], odd);
+          even = kv_byte<3>(v[1][1][0], q[1], even);
+          odd = kv_byte<3>(v[1][1][1], q[1], odd);
+          out[0][u] = even | odd << 4;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (mine[2 * u + k] && y == 0) {
+            scales[c * 32 + g * 8 + 2 * u + k] = q[k].scale;
+            zeros[(g * G + c) * 8 + 2 * u + k] = (uint8_t)q[k].zero;
+          }
+      }
     }
     if (whole) {
 #pragma unroll
