@@ -3,6 +3,8 @@
 
 #include "kv_layout.h"
 
+#include <type_traits>
+
 namespace qlin {
 
 struct KvStoreArgs {
@@ -124,18 +126,34 @@ __device__ __forceinline__ uint32_t range_of(const uint32_t (&w)[N]) {
                             __builtin_amdgcn_perm(nhi, lo, 0x07060302u));
   return max((int)size[0], (int)size[1]) >= 0x7C00 ? kBadRange : r;
 }
-// The least over the 16 lanes of a row (pairs, quads, mirrors of 8 and 16), and over
-// the four lanes l, l ^ 16, l ^ 32, l ^ 48.
 template <int CTRL>
 __device__ __forceinline__ uint32_t mov_dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
 }
-__device__ __forceinline__ uint32_t row_min(uint32_t v) {
-  v = pk_min(v, mov_dpp<0xB1>(v));
-  v = pk_min(v, mov_dpp<0x4E>(v));
-  v = pk_min(v, mov_dpp<0x141>(v));
-  return pk_min(v, mov_dpp<0x140>(v));
+// v[t] of eight numbers t over the 16 lanes of a row, in the lanes y % 8 = t: halves of the
+// numbers are exchanged between lanes 4, 2 and 1 apart, so that each step halves them.
+__device__ __forceinline__ uint32_t row_min_of_8(const uint32_t (&v)[8], int y) {
+  uint32_t a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {                // bit 2 of the number, with the lane 4 apart
+    const uint32_t keep = y & 4 ? v[4 + i] : v[i], give = y & 4 ? v[i] : v[4 + i];
+    a[i] = pk_min(keep, (uint32_t)__builtin_amdgcn_ds_swizzle((int)give, 0x101F));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {                // bit 1, with the lane 2 apart
+    const uint32_t keep = y & 2 ? a[2 + i] : a[i], give = y & 2 ? a[i] : a[2 + i];
+    b[i] = pk_min(keep, mov_dpp<0x4E>(give));
+  }
+  const uint32_t keep = y & 1 ? b[1] : b[0], give = y & 1 ? b[0] : b[1];
+  const uint32_t c = pk_min(keep, mov_dpp<0xB1>(give));
+  return pk_min(c, mov_dpp<0x128>(c));         // the other eight lanes (rotated by 8)
 }
+// A number of lane T of the row.
+template <int T>
+__device__ __forceinline__ float from_lane(float v) {
+  return __builtin_bit_cast(float, mov_dpp<0x150 + T>(__builtin_bit_cast(uint32_t, v)));
+}
+// The least over the four lanes l, l ^ 16, l ^ 32, l ^ 48.
 __device__ __forceinline__ uint32_t quarter_min(uint32_t v) {
   const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   v = pk_min((uint32_t)a[0], (uint32_t)a[1]);
@@ -291,9 +309,36 @@ __device__ __forceinline__ void kv_store_tile(const KvStoreArgs& a, const KvSpan
       w[t] = u32x2{0, 0};
       if (mine[t]) w[t] = *(const u32x2*)(a.x[1] + (sp.row0 + p) * a.ldx[1] + head * D + c * 64 + 4 * y);
     }
-    uint32_t out[4 / n][4];                  // [part of 4 dims][pair of tokens]
+    uint32_t out[4 / n][4];                    // [part of 4 dims][pair of tokens]
+    KvGroup own;                               // of token y % 8
+    if constexpr (BITS < 16) {
+      uint32_t range[8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {              // tokens 2 u (low halves) and 2 u + 1
+      for (int t = 0; t < 8; ++t) {
+        const uint32_t pair[2] = {w[t][0], w[t][1]};
+        range[t] = range_of(pair);
+      }
+      own = kv_group<BITS>(row_min_of_8(range, y));
+      if (y < 8 && (p0 + (y >> 2) * 16 + 4 * g + (y & 3)) >= sp.first &&
+          (p0 + (y >> 2) * 16 + 4 * g + (y & 3)) < sp.end) {
+        scales[c * 32 + g * 8 + y] = own.scale;
+        zeros[(g * G + c) * 8 + y] = (uint8_t)own.zero;
+      }
+    }
+    auto token = [&](auto T) {                 // a token's rounding, from the lane that has it
+      constexpr int t = decltype(T)::value;
+      KvGroup q;
+      q.p.s = from_lane<t>(own.p.s);
+      q.p.r = from_lane<t>(own.p.r);
+      q.p.hs = from_lane<t>(own.p.hs);
+      q.p.hi = from_lane<t>(own.p.hi);
+      q.zero = from_lane<t>(own.zero);
+      q.p.lo = -q.zero;
+      q.scale = 0;
+      return q;
+    };
+    auto two = [&](auto U) {                   // tokens 2 u (low halves) and 2 u + 1
+      constexpr int u = decltype(U)::value;
       const uint32_t pair[2][2] = {{w[2 * u][0], w[2 * u][1]}, {w[2 * u + 1][0], w[2 * u + 1][1]}};
       if constexpr (BITS == 16) {
         out[0][u] = __builtin_amdgcn_perm(pair[1][0], pair[0][0], 0x05040100u);
@@ -302,14 +347,13 @@ __device__ __forceinline__ void kv_store_tile(const KvStoreArgs& a, const KvSpan
         out[3][u] = __builtin_amdgcn_perm(pair[1][1], pair[0][1], 0x07060302u);
       } else {
         float v[2][2][2];                      // [token][pair][value]
-        KvGroup q[2];
+        const KvGroup q[2] = {token(std::integral_constant<int, 2 * u>{}),
+                              token(std::integral_constant<int, 2 * u + 1>{})};
         bool tie = false;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          q[k] = kv_group<BITS>(row_min(range_of(pair[k])));
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i) tie |= kv_round(pair[k][i], q[k], v[k][i]);
-        }
         if (__ballot(tie) != 0) {
 #pragma unroll
           for (int k = 0; k < 2; ++k)
@@ -336,14 +380,12 @@ __device__ __forceinline__ void kv_store_tile(const KvStoreArgs& a, const KvSpan
           odd = kv_byte<3>(v[1][1][1], q[1], odd);
           out[0][u] = even | odd << 4;
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (mine[2 * u + k] && y == 0) {
-            scales[c * 32 + g * 8 + 2 * u + k] = q[k].scale;
-            zeros[(g * G + c) * 8 + 2 * u + k] = (uint8_t)q[k].zero;
-          }
       }
-    }
+    };
+    two(std::integral_constant<int, 0>{});
+    two(std::integral_constant<int, 1>{});
+    two(std::integral_constant<int, 2>{});
+    two(std::integral_constant<int, 3>{});
     if (whole) {
 #pragma unroll
       for (int i = 0; i < 4 / n; ++i)
