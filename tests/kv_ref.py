@@ -144,9 +144,10 @@ def attention(cache, q, table, lengths, scale, window):
     """(O, lse, bound of O's error in fp32, bound of lse's): q [seqs, heads, d] fp16.
 
     A score is a sum of d exact products in fp32 (d + 8 roundings of sum |q k|, scales
-    included) times scale, and its exponent is rounded four times more, each relative to a
-    value below |S| + |max S| + 40; exp is correct to 2 u.  P enters with 21 bits and a step of
-    2^-39 of the largest P s, sums over n tokens add n + 64 roundings."""
+    included) times scale, whose sign changes no size, and its exponent is rounded four times
+    more, each relative to a value below |S| + |max S| + 40; exp is correct to 2 u.  P enters
+    with 21 bits and a step of 2^-39 of the largest P s, sums over n tokens add n + 64
+    roundings."""
     seqs, heads, d = q.shape
     o, lse = np.zeros((seqs, heads, d)), np.full((seqs, heads), -np.inf)
     eo, el = np.zeros((seqs, heads, d)), np.zeros((seqs, heads))
@@ -159,7 +160,7 @@ def attention(cache, q, table, lengths, scale, window):
         for h in range(heads):
             kh, vh = k[:, h // ratio], v[:, h // ratio]
             x = q[b, h].astype(np.float64)
-            s, size = scale * (kh @ x), scale * (np.abs(kh) @ np.abs(x)).max()
+            s, size = scale * (kh @ x), abs(scale) * (np.abs(kh) @ np.abs(x)).max()
             top = s.max()
             p = np.exp(s - top)
             total = p.sum()
