@@ -22,7 +22,7 @@ struct SampleArgs {
 
 // A row's settings, with what is off or out of range put in order.
 struct SampleRow {
-  double t;          // temperature; 0: the largest logit is taken
+  double t;          // temperature; 0: the first of the largest logits is taken
   int k;             // 0: off
   float p, mp, u;    // p 1, mp 0: off
 };
@@ -39,7 +39,8 @@ __device__ __forceinline__ SampleRow sample_row(const SampleArgs& a, int row) {
   const float p = a.top_p != nullptr ? pv : 1.f;
   const float mp = a.min_p != nullptr ? mv : 0.f;
   SampleRow r;
-  r.t = t > 0.f && k != 1 ? (double)t : 0.;
+  // (with min_p above 1 no p reaches it: the first token alone, as with top_k 1)
+  r.t = t > 0.f && k != 1 && !(mp > 1.f) ? (double)t : 0.;
   r.k = k > 0 && k < a.vocab ? k : 0;
   r.p = p < 1.f ? fmaxf(p, 0.f) : 1.f;
   r.mp = mp > 0.f ? mp : 0.f;

@@ -17,29 +17,29 @@ extern "C" {
 
 /* The settings of the rows: device arrays [m], each NULL where it is off for all. */
 typedef struct qlin_sampling {
-  const float* temperature; /* NULL: 1.  Not above 0: the largest logit is taken     */
+  const float* temperature; /* NULL: 1.  Not above 0: the first of the largest    */
   const int32_t* top_k;     /* below 1: off                                       */
   const float* top_p;       /* not below 1: off;  0 or less: one token            */
-  const float* min_p;       /* not above 0: off                                   */
+  const float* min_p;       /* not above 0: off;  above 1: one token              */
 } qlin_sampling;
 
 /*
  * Row i of logits, fp32 [m, ld], ld >= vocab, and u[i] in [0, 1):
  *     p[j] = exp( (l[j] - max l) / temperature ),
  *     order: by logit, descending, equal logits by index, ascending;
- *     kept: the longest beginning of the order with at most top_k tokens, none behind the first that
- *       brings the sum of p to top_p times that of the first top_k, and p[j] >= min_p
- *       (the first token is always kept);
+ *     kept: the longest beginning of the order with at most top_k tokens, none behind
+ *       the first that brings the sum of p to top_p times that of the first top_k, and
+ *       p[j] >= min_p (the first token is always kept);
  *     ids[i] = the lowest j for which the sum of p over the kept tokens 0 .. j
  *       exceeds u[i] times that over all kept ones;
  *     probs[i] = p[ids[i]] over that sum.
  * Tokens whose logit is -inf or NaN are not there; +inf counts as the largest
  * finite logit.  A row without tokens has id -1 and probability 0.  u below 0
  * (or NaN) counts as 0, and from 1 on takes the last kept token.
- * p is formed in 64 bits; tokens below exp(-40) of the largest may count as 0.  The
- * choice is that of 64-bit arithmetic; a token can differ from the exact one only where a
- * border lies within 2^-35 of it (relative to the sum).  Deterministic: a row's
- * result depends on its own logits, settings and u only.
+ * p is formed in 64 bits; tokens below exp(-31.5) of the largest may count as 0.  The
+ * choice is that of exact arithmetic but where a border (of top_p, min_p or u) lies
+ * within 2^-34 + vocab * 2^-45 of it, relative to the sum.  Deterministic: a row's result
+ * depends on its own logits, settings and u only.
  * ids int32 [m]; probs fp32 [m] or NULL.  1 <= vocab <= 2^18, m <= 2^20; m = 0 is a no-op.
  * workspace: scratch of qlin_sample_workspace_bytes (or QLIN_ERR_WORKSPACE; 0 is
  * returned there for invalid arguments), 16-byte aligned; its first 65536 bytes are left
