@@ -55,7 +55,7 @@ __device__ __forceinline__ int64_t unit_share(int64_t all, int groups) {
   return s < least ? least : s;
 }
 
-// Where a wave has a tile: in registers,
+// A tile in registers, as it lies in memory: a wave's loads are whole 16-byte units.
 template <int D, int KB, int VB>
 struct KvRegs {
   static constexpr int G = D / 64;
@@ -90,64 +90,7 @@ struct KvRegs {
       }
     }
   }
-  __device__ __forceinline__ u32x4 k_unit(int i) const { return k[i]; }
-  __device__ __forceinline__ u32x4 v_unit(int i) const { return v[i]; }
-  __device__ __forceinline__ u32x4 k_scales(int c) const { return ks[c]; }
-  __device__ __forceinline__ u32x4 v_scales(int c) const { return vs[c]; }
-  __device__ __forceinline__ uint32_t k_zeros(int i) const { return kz[i]; }
-  __device__ __forceinline__ u32x2 v_zeros(int c) const { return vz[c]; }
 };
-
-// or in LDS, as it lies in memory.
-template <int D, int KB, int VB>
-struct KvStage {
-  using T = KvTile<D, KB, VB>;
-  static constexpr int G = D / 64;
-  const uint8_t* p;
-  int lane, g, r;
-
-  __device__ __forceinline__ explicit KvStage(const uint8_t* at)
-      : p(at), lane(lane_id()), g(lane >> 4), r(lane & 15) {}
-  __device__ __forceinline__ u32x4 k_unit(int i) const { return *(const u32x4*)(p + T::k + (i * 64 + lane) * 16); }
-  __device__ __forceinline__ u32x4 v_unit(int i) const { return *(const u32x4*)(p + T::v + (i * 64 + lane) * 16); }
-  __device__ __forceinline__ u32x4 k_scales(int c) const { return *(const u32x4*)(p + T::ks + c * 64 + g * 16); }
-  __device__ __forceinline__ u32x4 v_scales(int c) const { return *(const u32x4*)(p + T::vs + c * 64 + g * 16); }
-  __device__ __forceinline__ uint32_t k_zeros(int i) const {
-    if constexpr (G == 1) return *(const uint16_t*)(p + T::kz + r * 2);
-    return *(const uint32_t*)(p + T::kz + r * 2 * G + i * 4);
-  }
-  __device__ __forceinline__ u32x2 v_zeros(int c) const { return *(const u32x2*)(p + T::vz + (g * G + c) * 8); }
-};
-
-// Direct-to-LDS loads of a tile: 16 bytes of every lane an instruction, the last one of
-// fewer lanes.
-template <int D, int KB, int VB>
-constexpr int kTileLoads = (KvTile<D, KB, VB>::bytes + 1023) / 1024;
-template <int D, int KB, int VB>
-__device__ __forceinline__ void stage_tile(const uint8_t* src, uint8_t* lds) {
-  typedef __attribute__((address_space(3))) void lds_void;
-  constexpr int bytes = KvTile<D, KB, VB>::bytes;
-  const int lane = lane_id();
-  // (what was read from there has arrived)
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < bytes / 1024; ++i)
-    __builtin_amdgcn_global_load_lds(src + i * 1024 + lane * 16, (lds_void*)(lds + i * 1024), 16, 0, 0);
-  if (bytes % 1024 != 0 && lane < bytes % 1024 / 16)
-    __builtin_amdgcn_global_load_lds(src + bytes / 1024 * 1024 + lane * 16,
-                                     (lds_void*)(lds + bytes / 1024 * 1024), 16, 0, 0);
-}
-// One LDS object per stage, so that the compiler can tell which loads a read waits for.
-template <int D, int KB, int VB, int I>
-__device__ __forceinline__ uint8_t* tile_stage() {
-  __shared__ __attribute__((aligned(16))) uint8_t st[kAttendWaves * KvTile<D, KB, VB>::bytes];
-  return st;
-}
-// s_waitcnt vmcnt(N), expcnt and lgkmcnt not waited on.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
 
 // Pairs of codes as fp16 numbers q - z, exactly: the code's bits go into the mantissa of
 // 1024 (bits 0..3 or 0..7) or, 16 times larger, of 1024 with a factor 1/16.
@@ -207,8 +150,8 @@ struct AttendState {
 // towards zero, lo the rest: 21 bits).  So that P * s has these bits whatever the
 // size of s, P is taken relative to 2^off, off = max + e - 15, s < 2^e for every scale
 // so far: P s < 2^15.
-template <int D, int KB, int VB, typename Tile>
-__device__ __forceinline__ void attend_tile(AttendState<D>& st, const Tile& t,
+template <int D, int KB, int VB>
+__device__ __forceinline__ void attend_tile(AttendState<D>& st, const KvRegs<D, KB, VB>& t,
                                             const f16x8 (&q)[D / 32], float c, bool edge, int first,
                                             int lo, int hi, MixConsts mix) {
   constexpr int G = D / 64;
@@ -221,14 +164,14 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const Tile& t,
   u32x4 ks[G];
   if constexpr (KB < 16) {
 #pragma unroll
-    for (int cg = 0; cg < G; ++cg) ks[cg] = t.k_scales(cg);
+    for (int cg = 0; cg < G; ++cg) ks[cg] = t.ks[cg];
   }
   u32x4 ku[kHalf];                       // the half tile's units
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (h == 0 || kUnits >= 2) {
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i) ku[i] = t.k_unit(h * kHalf + i);
+      for (int i = 0; i < kHalf; ++i) ku[i] = t.k[h * kHalf + i];
     }
     f32x4 acc[G];
 #pragma unroll
@@ -237,7 +180,7 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const Tile& t,
       if constexpr (KB < 16) {
         const int byte = h * G + cg;
         const uint32_t sel = 0x04000400u | ((byte % 4) << 16) | (byte % 4);
-        c1 = as_h2(__builtin_amdgcn_perm(0xE4E4E4E4u, t.k_zeros(byte / 4), sel));
+        c1 = as_h2(__builtin_amdgcn_perm(0xE4E4E4E4u, t.kz[byte / 4], sel));
         if constexpr (KB == 4) c2 = c1 + f16x2{(f16)960.f, (f16)960.f};
       }
       f32x4 s{};
@@ -285,7 +228,7 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const Tile& t,
   u32x4 mask{~0u, ~0u, ~0u, ~0u};        // (16 bits) of the seen tokens' values
   if constexpr (VB < 16) {
 #pragma unroll
-    for (int cg = 0; cg < G; ++cg) vs[cg] = t.v_scales(cg);
+    for (int cg = 0; cg < G; ++cg) vs[cg] = t.vs[cg];
   }
   if (edge) {
 #pragma unroll
@@ -303,14 +246,6 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const Tile& t,
         }
       }
     }
-  }
-  // values are read from LDS before P is known, where there are registers for them
-  constexpr int kVUnits = VB * G / 4;
-  constexpr bool kEarly = kVUnits <= 4;
-  u32x4 early[kEarly ? kVUnits : 1];
-  if constexpr (kEarly) {
-#pragma unroll
-    for (int i = 0; i < kVUnits; ++i) early[i] = t.v_unit(i);
   }
   float mx = x[0];
 #pragma unroll
@@ -370,7 +305,7 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const Tile& t,
     }
     f16x2 c1[4], c2[4];
     if constexpr (VB < 16) {
-      const u32x2 z = t.v_zeros(cg);
+      const u32x2 z = t.vz[cg];
       c1[0] = zero_pair<0, 1>(z[0]);
       c1[1] = zero_pair<2, 3>(z[0]);
       c1[2] = zero_pair<0, 1>(z[1]);
@@ -386,8 +321,7 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const Tile& t,
       union { f16x8 v; f16x2 p[4]; } f;
       if (j % (16 / VB) == 0) {
         const int unit = cg * (VB / 4) + j / (16 / VB);
-        if constexpr (kEarly) vu = early[unit];
-        else vu = t.v_unit(unit);
+        vu = t.v[unit];
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -416,33 +350,21 @@ struct PageList {
   int base, entry;
 };
 
-// Tiles up to this size go through LDS, in two stages of four waves' tiles: the loads
-// of the next tile run while one is used, without registers.  Larger ones are held in registers.
-template <int D, int KB, int VB>
-constexpr bool kStaged = KvTile<D, KB, VB>::bytes <= 10240;
-template <int D, int KB, int VB>
-constexpr bool kTwoTiles = D <= 128 && (KB + VB) * (D / 64) <= 32;
-// Work-groups per CU that LDS and registers allow.
-constexpr int attend_occupancy(int d, int tile) {
-  return tile > 10240 ? (d == 256 ? 1 : 2) : tile <= 4864 && d <= 128 ? 4 : 2;
+// Two tiles of a wave in registers, or one.
+constexpr bool attend_two(int d, int kb, int vb) { return d <= 128 && (kb + vb) * (d / 64) <= 32; }
+// Work-groups per CU that registers allow.
+constexpr int attend_occupancy(int d, int kb, int vb) {
+  return d == 256 ? (kb + vb <= 16 ? 2 : 1) : (kb + vb) * (d / 64) <= 16 ? 3 : 2;
 }
 
 template <int D, int KB, int VB>
-__global__ __launch_bounds__(256, attend_occupancy(D, KvTile<D, KB, VB>::bytes)) void k_attend(
+__global__ __launch_bounds__(256, attend_occupancy(D, KB, VB)) void k_attend(
     const AttendArgs a) {
   using T = KvTile<D, KB, VB>;
   constexpr int G = D / 64;
-  constexpr bool staged = kStaged<D, KB, VB>;
   constexpr int kRow = D + 4;            // a row's pitch in LDS is not a multiple of the banks
   __shared__ float rst[kAttendWaves][kAttendRows][2];
-  float* red;                            // [2][16][kRow]: sums of two waves
-  if constexpr (staged) {
-    static_assert(2 * kAttendRows * kRow * 4 <= kAttendWaves * T::bytes, "sums in the first stage");
-    red = reinterpret_cast<float*>(tile_stage<D, KB, VB, 0>());
-  } else {
-    __shared__ float own[2 * kAttendRows * kRow];
-    red = own;
-  }
+  __shared__ float red[2 * kAttendRows * kRow];      // sums of two waves
   const int lane = lane_id(), wave = wave_id(), g = lane >> 4, n = lane & 15;
   const MixConsts mix = mix_consts();
   const int hgs = a.kv_heads * a.rts;
@@ -535,8 +457,7 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KvTile<D, KB, VB>::bytes))
       };
       const uint8_t* tp = place(t, there[0]);
       KvRegs<D, KB, VB> one;
-      if constexpr (staged) stage_tile<D, KB, VB>(tp, tile_stage<D, KB, VB, 0>() + wave * T::bytes);
-      else one.load(tp);
+      one.load(tp);
       f16x8 q[D / 32];
       const f16* qp = a.q + b * a.ldq + (int64_t)(head * a.ratio + row0 + min(n, rows - 1)) * D;
 #pragma unroll
@@ -549,32 +470,7 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KvTile<D, KB, VB>::bytes))
         const int p0 = t * kKvTile;
         attend_tile<D, KB, VB>(st, tile, q, a.c, p0 < lo || p0 + kKvTile > hi, p0, lo, hi, mix);
       };
-      if constexpr (staged) {
-        uint8_t* const lds[2] = {tile_stage<D, KB, VB, 0>() + wave * T::bytes,
-                                 tile_stage<D, KB, VB, 1>() + wave * T::bytes};
-        for (;;) {
-          bool more = t + kAttendWaves < last;
-          if (more) {
-            stage_tile<D, KB, VB>(place(t + kAttendWaves, there[1]), lds[1]);
-            wait_loads<kTileLoads<D, KB, VB>>();
-          } else {
-            wait_loads<0>();
-          }
-          if (there[0]) use(KvStage<D, KB, VB>(lds[0]), t);
-          if (!more) break;
-          t += kAttendWaves;
-          more = t + kAttendWaves < last;
-          if (more) {
-            stage_tile<D, KB, VB>(place(t + kAttendWaves, there[0]), lds[0]);
-            wait_loads<kTileLoads<D, KB, VB>>();
-          } else {
-            wait_loads<0>();
-          }
-          if (there[1]) use(KvStage<D, KB, VB>(lds[1]), t);
-          if (!more) break;
-          t += kAttendWaves;
-        }
-      } else if constexpr (kTwoTiles<D, KB, VB>) {
+      if constexpr (attend_two(D, KB, VB)) {
         KvRegs<D, KB, VB> two;
         for (;;) {
           two.load(place(min(t + kAttendWaves, last - 1), there[1]));
@@ -679,7 +575,7 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KvTile<D, KB, VB>::bytes))
         }
       }
     }
-    lds_barrier();                       // (the next segment writes red, its stage and rst again)
+    lds_barrier();                       // (the next segment writes red and rst again)
     pos = begin + units;
     if (pos >= to) break;
     begin = pos;

@@ -9,7 +9,7 @@ namespace qlin {
 // Work-groups of the attention: as many as the chip holds at once (one for every
 // four tiles if there cannot be that many).
 inline int attend_groups(int d, int kb, int vb) {
-  return 256 * attend_occupancy(d, kv_tile_bytes(d, kb, vb));
+  return 256 * attend_occupancy(d, kb, vb);
 }
 
 template <int KB, int VB>
