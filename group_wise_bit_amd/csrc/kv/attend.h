@@ -1,4 +1,20 @@
-// Attention of one new token per sequence over the cache (gfx950, wave64).
+// Attention of one new token per sequence over the cache (gfx950, wave64):
+//     S[p] = scale q . k_p,   P = exp(S - max),   O = sum P v_p / sum P,
+// in one pass over the cached tokens with a running maximum and sum; k = s (code - z).
+//
+// What bounds it.  Every code is read once and takes part in 4 ratio operations, far below
+// what the matrix cores do, so that the bytes of the cache are the floor.  With 8 bits and more they
+// are reached (64 sequences of 8192 tokens, 8 heads of 128: 194 us for 1.13 GB, 5.8 TB/s).  With
+// 4 bits the instructions that unpack are as long: a tile of 32 tokens and 128 dims takes 286
+// vector instructions and 24 MFMAs of a wave, 36 us of the 37 us that 131071 tokens of 8 heads
+// take (the loads alone 30, 4.0 TB/s with them).
+//
+// Why this split.  One query head per sequence and head of the cache is no matrix product:
+// the heads that share a head of the cache (ratio, up to 16 at a time) are one MFMA operand, tokens
+// are the other.  A wave takes every fourth tile of its work-group's range, so that no barrier
+// is in the loop.  The tiles of all sequences are one list, cut into equal ranges for as many
+// work-groups as the chip holds: a batch of 48 lengths from 1 to 4096 and one sequence of
+// 131071 tokens both fill it.
 #pragma once
 
 #include "kv_layout.h"
@@ -44,7 +60,9 @@ __device__ __forceinline__ int seen_tiles(const AttendArgs& a, int b) {
 }
 
 // Every work-group takes `share` units of the list [sequence][head][row block][units]:
-// kStartUnits for the start of a row block's tiles, then one for each of them.
+// kStartUnits for the start of a row block's tiles, then one for each of them.  (A start costs
+// a page list, the queries, the sums of four waves and a store.  48 sequences of 1 to 4096 tokens:
+// 51 us without, 30.4 with 4 units, 29.2 with 8, 30.1 with 16.)
 constexpr int kStartUnits = 8;
 __device__ __forceinline__ int seen_units(const AttendArgs& a, int b) {
   const int tiles = seen_tiles(a, b);
@@ -55,7 +73,10 @@ __device__ __forceinline__ int64_t unit_share(int64_t all, int groups) {
   return s < least ? least : s;
 }
 
-// A tile in registers, as it lies in memory: a wave's loads are whole 16-byte units.
+// A tile in registers, as it lies in memory: a wave's loads are whole 16-byte units.  (Through
+// LDS, with direct-to-LDS loads in two stages, four work-groups per CU instead of three: the same
+// on 48 sequences of 4096 tokens and 4 bits, 33.2 us with the join; slower on one of 131071,
+// 44.5 : 42.5, and on 64 of 8192 with 8 bits, 203 : 198.  With three stages 35 us for 29 of the first.)
 template <int D, int KB, int VB>
 struct KvRegs {
   static constexpr int G = D / 64;
@@ -350,9 +371,14 @@ struct PageList {
   int base, entry;
 };
 
-// Two tiles of a wave in registers, or one.
+// Two tiles of a wave in registers, one loading while the other is used; or one, where
+// two gain nothing: 128 dims of 16 bits 47.8 us : 48.2 with one, 256 dims of 8 bits 43.3 : 40.1, of
+// 16 bits 50.1 : 48.2 (48 sequences of 1 to 4096 tokens; the other waves' loads are enough there).
 constexpr bool attend_two(int d, int kb, int vb) { return d <= 128 && (kb + vb) * (d / 64) <= 32; }
-// Work-groups per CU that registers allow.
+// Work-groups per CU that registers allow (four waves each, one per SIMD).  Small tiles three: 168
+// registers; two take 30.3 us for 27.8 (48 sequences, 128 dims, 4 bits), four with one tile 29.2;
+// 64 dims 12.2 (three) : 13.0 (four).  256 dims with up to 16 bits together two: 4 bits 28.8
+// for 37.3 with one, 8 bits 36.0 for 40.1 (more bits do not fit).
 constexpr int attend_occupancy(int d, int kb, int vb) {
   return d == 256 ? (kb + vb <= 16 ? 2 : 1) : (kb + vb) * (d / 64) <= 16 ? 3 : 2;
 }
@@ -587,8 +613,10 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KB, VB)) void k_attend(
 }
 
 // The parts of the sequences that more than one work-group dealt with, and rows without
-// tokens.  One work-group per (sequence, query head): a thread per part for its weight, then
-// D / 4 threads per part, 1024 / D of them at a time, eight loads of a thread in flight.
+// tokens: O = sum of 2^(off_i - max) O_i over the same of l_i.  One work-group per (sequence, query
+// head): a thread per part for its weight, then D / 4 threads per part, 1024 / D of them at
+// a time, eight loads of a thread in flight.  Bound by two rounds of loads, one behind the other:
+// 4.0 to 5.5 us, of 1 to 1024 parts.
 template <int D>
 __global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a) {
   constexpr int kLanes = D / 4, kSubs = 256 / kLanes;

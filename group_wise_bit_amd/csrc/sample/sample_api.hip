@@ -15,8 +15,8 @@ constexpr int kMaxVocab = kSlice * kSlices;
 
 int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
 
-// Rows are drawn in batches of this many, so that the workspace is bounded (65 MB
-// for rows of 2^18 tokens): enough of them to fill the chip with slices.
+// Rows are drawn in batches of at most kBatchRows rows and kBatchSlices slices, so that the
+// workspace is bounded (below 72 MB): enough of them to fill the chip several times over.
 constexpr int kBatchSlices = 8192;
 constexpr int kBatchRows = 512;
 

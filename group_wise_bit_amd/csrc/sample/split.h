@@ -16,13 +16,21 @@ namespace qlin {
 // different slices line up whatever their largest logit, and the mass of a
 // token is exp((t - bin) / 12), a polynomial of degree 6, times a factor per bin.
 // Bins from 384 below the top one (exp(-32)) on hold no mass.
-constexpr int kSlice = 8192;
+//
+// What bounds it.  A logit is read two or three times (the rows of a batch stay in the last
+// cache): the floor of 64 rows of 151936 is 7.5 us, of one row nothing.  One row takes four launches
+// of 5 to 6 us, each a chain of dependent loads and sums; 64 rows take 18 + 7 + 11 + 20 us: the bins
+// are bound by 64-bit arithmetic and an LDS atomic per token, the pick by its chain of
+// barriers on 64 CUs.  A row in one work-group (sample_alone) takes 860 us.
+constexpr int kSlice = 8192;                 // (4096: 21 us of the bins for 18 at 64 rows)
 constexpr int kSlices = 32;                  // of a row, at most
 constexpr int kBins = 384;
 constexpr int kBinScale = 12;
-constexpr int kListMax = 8192;               // tokens that are gathered, at most
+constexpr int kListMax = 8192;               // tokens that are gathered, at most (what LDS holds)
 constexpr int kBinThreads = 512;
-constexpr int kRankMax = 512;                // tokens whose order is found by comparing all
+// Tokens whose order is found by comparing all, a thread each (one row with top_k 50: 5.5 us of
+// the pick, 11.1 through parts).
+constexpr int kRankMax = 512;
 constexpr int kSums = kBins + 1;             // a slice's sums: 0, then up to each bin
 
 struct SliceStat {
@@ -132,6 +140,8 @@ __device__ __forceinline__ T wave_scan(T v) {          // inclusive
 // not depend on the order.
 constexpr int kCountBit = 50;
 
+// One work-group per slice, 16 logits of a thread in registers: the slice's top first, then
+// the histogram, then its sums.
 __global__ __launch_bounds__(kBinThreads) void k_sample_bins(const SplitArgs a) {
   __shared__ unsigned long long hist[kBins];
   constexpr int kWaves = kBinThreads / 64;
@@ -216,7 +226,8 @@ __global__ __launch_bounds__(kBinThreads) void k_sample_bins(const SplitArgs a) 
   }
 }
 
-// One work-group per row, a thread per bin.
+// One work-group per row, a thread per bin: sums over the slices, 16 slices' loads in flight (with
+// a test for each slice they waited for one another: 11 us for 7).
 __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
   __shared__ double mass[kBins];
   __shared__ uint32_t count[kBins];
@@ -338,6 +349,8 @@ __global__ __launch_bounds__(kBins) void k_sample_bounds(const SplitArgs a) {
   }
 }
 
+// One work-group per slice; a token's place in the list is the number of those before it, so
+// that the list has the vocabulary's order.  (Four slices to a work-group: 22 us for 11.)
 __global__ __launch_bounds__(kBinThreads) void k_sample_gather(const SplitArgs a) {
   constexpr int kWaves = kBinThreads / 64;
   __shared__ int counts[kSlice / 64];          // [step][wave]
@@ -541,6 +554,9 @@ __device__ __forceinline__ int first_to_reach(PickShared& sh, double sum, double
   return sh.rank;
 }
 
+// One work-group per row.  The cut is put together as top_k, then top_p of the first top_k's
+// mass, then min_p; the draw goes through the slices' masses to one slice's logits, or, where all
+// kept tokens are in the list, through the list alone.
 __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a) {
   __shared__ PickShared sh;
   const int r = blockIdx.x, row = a.row0 + r, lane = lane_id(), tid = threadIdx.x;
