@@ -4,10 +4,10 @@
 //
 // What bounds it.  Every code is read once and takes part in 4 ratio operations, far below
 // what the matrix cores do, so that the bytes of the cache are the floor.  With 8 bits and more they
-// are reached (64 sequences of 8192 tokens, 8 heads of 128: 194 us for 1.13 GB, 5.8 TB/s).  With
-// 4 bits the instructions that unpack are as long: a tile of 32 tokens and 128 dims takes 286
-// vector instructions and 24 MFMAs of a wave, 36 us of the 37 us that 131071 tokens of 8 heads
-// take (the loads alone 30, 4.0 TB/s with them).
+// are reached (64 sequences of 8192 tokens, 8 heads of 128: 198 us for 1.13 GB, 5.7 TB/s).  With
+// 4 bits the unpacking is as long: a tile of 32 tokens and 128 dims takes 384 vector instructions
+// of a wave, 24 of them MFMAs (prologue and sums of the waves included): 24 us of issue in the 39 us
+// that 131071 tokens of 8 heads take (3.8 TB/s; its loads alone take 30, its arithmetic alone 36).
 //
 // Why this split.  One query head per sequence and head of the cache is no matrix product:
 // the heads that share a head of the cache (ratio, up to 16 at a time) are one MFMA operand, tokens

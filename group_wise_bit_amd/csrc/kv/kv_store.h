@@ -3,12 +3,11 @@
 // Both are copies with a change of form: their floor is the bytes of the rows and of the
 // codes.  A wave takes a part of a tile whose codes are its own whole words in the layout: half of the
 // tokens of the keys, a group of 64 dims of the values.  Whole prompts (8 of 2048 tokens, 8 heads of
-// 128, keys of 8 bits, values of 4) are written in 26 us, 6.2 TB/s of rows and codes, a quarter above a
-// large copy's rate (the rows are partly in the last cache); 16 prompts of up to 4096 tokens of 8
-// bits are read back in 37 us (4.4 TB/s), bound by the launching of waves, two to four for 8 KB,
-// and their one round of loads.  (One wave for all parts of a tile and head: slower, for the
-// same reason turned round -- its loads wait for each other.)  A few tokens take 5 us, a launch and
-// three rounds of dependent loads: offsets and lengths, the page, the rows.
+// 128, keys of 8 bits, values of 4: 94 MB) are written in 26 us (3.6 TB/s) and read back in 17.6
+// (5.3 TB/s, a large copy's rate); 16 prompts of up to 4096 tokens of 8 bits (162 MB) are read
+// back in 36 us (4.5 TB/s).  (One wave for all parts of a tile and head: slower, its loads wait
+// for each other.)  A few tokens take 5 us, a launch and three rounds of dependent loads: offsets
+// and lengths, the page, the rows.
 #pragma once
 
 #include "kv_layout.h"

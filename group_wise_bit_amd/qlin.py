@@ -1077,8 +1077,8 @@ def kv_attention(cache: KVCache, Q: torch.Tensor, table: torch.Tensor, lengths: 
 @dataclass(eq=False)
 class Sampling(_CStruct):
     """How sample() draws, one setting per row (None: off for all): temperature fp32 [m] (not above
-    0: the largest logit), top_k int32 [m] (below 1: off), top_p fp32 [m] (not below 1: off) and
-    min_p fp32 [m] (not above 0: off)."""
+    0: the first of the largest), top_k int32 [m] (below 1: off), top_p fp32 [m] (not below 1: off)
+    and min_p fp32 [m] (not above 0: off; above 1: one token)."""
     temperature: Optional[torch.Tensor] = None
     top_k: Optional[torch.Tensor] = None
     top_p: Optional[torch.Tensor] = None
