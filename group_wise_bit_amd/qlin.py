@@ -1062,6 +1062,8 @@ def kv_attention(cache: KVCache, Q: torch.Tensor, table: torch.Tensor, lengths: 
         _same_device(dev, (("Q", Q),))
     if scale is None:
         scale = d ** -0.5
+    if not 0 <= window < 1 << 31:            # (ctypes would cut it to 32 bits)
+        raise ValueError(f"window must be from 0 to 2^31 - 1, got {window}")
     lib = _lib()
     _with_workspace(
         ws, dev, lambda: lib.qlin_kv_attention_workspace_bytes(c, s, heads),

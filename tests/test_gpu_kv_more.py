@@ -223,3 +223,23 @@ def test_a_decode_step():
         torch.cuda.synchronize()
         assert ((ids >= 0) & (ids < vocab)).all() and (probs > 0).all()
         x = qlin.embed_rows(head, ids)[0]
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(1024, 256), (1024, 1), (513, 27), (256, 256)])
+@pytest.mark.parametrize("width", [2, 40])
+def test_many_heads(heads, kv_heads, width):
+    """The most heads, few and many to a head of the cache, unsplit and split."""
+    rng = np.random.default_rng(8)
+    lengths = np.array([1, 45, 64], np.int32)
+    cache, ref = new_cache(rng, 7, kv_heads, 64, 32, 4, 8)
+    table = np.full((3, width), -1, np.int32)
+    table[:, :2] = new_table(rng, 3, 2, 7)
+    # (one head's tokens in all heads, each times its own power of two: the bytes are written by the call)
+    k, v = tokens(rng, int(lengths.sum()), 1, 64)
+    size = 2.0 ** rng.integers(-2, 3, (1, kv_heads, 1))
+    k, v = (np.clip(x * size, -8, 8).astype(np.float16) for x in (k, v))
+    starts = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    qlin.kv_write(cache, dev(k), dev(v), dev(table), dev(lengths), starts=dev(starts))
+    ref.data[:] = host(cache.data).reshape(ref.data.shape)
+    q = rng.standard_normal((3, heads, 64)).astype(np.float16)
+    attend(cache, ref, q, table, lengths)

@@ -248,3 +248,12 @@ def test_binding_refuses_caches():
     good.data = good.data[..., :-16].contiguous()
     with pytest.raises(TypeError):
         good.c_struct()
+
+
+def test_binding_refuses_windows():
+    """A window that 32 bits do not hold would come to another one's result."""
+    c, _, table, lengths = binding()
+    q = torch.zeros(3, 4, 64, dtype=torch.float16)
+    for window in (-1, 1 << 31, (1 << 32) + 5):
+        with pytest.raises(ValueError, match="window"):
+            qlin.kv_attention(c, q, table, lengths, window=window)
