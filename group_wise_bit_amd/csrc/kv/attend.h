@@ -62,15 +62,19 @@ __device__ __forceinline__ int seen_tiles(const AttendArgs& a, int b) {
 // Every work-group takes `share` units of the list [sequence][head][row block][units]:
 // kStartUnits for the start of a row block's tiles, then one for each of them.  (A start costs
 // a page list, the queries, the sums of four waves and a store.  48 sequences of 1 to 4096 tokens:
-// 51 us without, 30.4 with 4 units, 29.2 with 8, 30.1 with 16.)
+// 51 us without, 30.4 with 4 units, 29.2 with 8, 30.1 with 16.)  The least share is a tile for every
+// wave: few tokens are a chain of a wave's loads, and the join has time for the parts (9 windows of
+// 1000 tokens, 256 dims of 16 bits: 10.4 us for 13.0 with 12 units, one sequence of 4000, 128
+// dims of 4 bits: 8.7 for 10.0; with their joins 15.4 for 17.1 and 14.0 for 15.9).  A range may lie
+// within a start's units: it has no tiles then, and no place among the parts.
 constexpr int kStartUnits = 8;
 __device__ __forceinline__ int seen_units(const AttendArgs& a, int b) {
   const int tiles = seen_tiles(a, b);
   return tiles > 0 ? tiles + kStartUnits : 0;
 }
 __device__ __forceinline__ int64_t unit_share(int64_t all, int groups) {
-  const int64_t s = (all + groups - 1) / groups, least = kStartUnits + kAttendWaves;
-  return s < least ? least : s;
+  const int64_t s = (all + groups - 1) / groups;
+  return s < kAttendWaves ? kAttendWaves : s;
 }
 
 // A tile in registers, as it lies in memory: a wave's loads are whole 16-byte units.  (Through
