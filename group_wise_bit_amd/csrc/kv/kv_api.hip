@@ -120,10 +120,10 @@ struct Attend {
 };
 
 // Sequences of tables up to this length are not split: a work-group has all of one, and
-// nothing is joined.  Kernel times unsplit : split with the join, in us.  One sequence, 64 dims of
-// 8 bits: 300 tokens 6.3 : 13.6, 1024 10.1 : 13.6, 2048 16.4 : 13.7; 128 dims of 4 bits: 300
-// 8.6 : 14.1, 1024 14.2 : 14.3, 2048 22.4 : 14.8.  48 ragged ones of the latter: up to 300
-// 9.1 : 16.8, 1024 16.5 : 19.4, 2048 25.6 : 23.9.
+// nothing is joined.  Kernel times unsplit : split (its join, 4.0 to 5.5 us and a launch, apart), in us.
+// One sequence, 64 dims of 8 bits: 300 tokens 6.1 : 5.4, 1024 8.8 : 5.4, 2048 13.8 : 5.5; 128
+// dims of 4 bits: 512 9.6 : 6.7, 1024 13.3 : 8.0, 2048 20.3 : 6.8; 256 dims of 16 bits: 1024 20.4 :
+// 10.0.  48 ragged ones, 128 dims of 4 bits: up to 300 9.7 : 11.3, 1024 16.7 : 14.1, 2048 25.0 : 19.9.
 constexpr int64_t kWholeTokens = 1024;
 
 struct AttendPlan {
