@@ -24,6 +24,7 @@ namespace qlin {
 constexpr int kAttendWaves = 4;
 constexpr int kAttendRows = 16;        // query heads of a work-group: a column block of an MFMA
 constexpr int kMaxParts = 1024;        // work-groups at most, and parts of a sequence
+constexpr float kNoScore = -1e30f;     // a running maximum of none: below every finite score
 
 struct AttendArgs {
   KvSeqs s;
@@ -275,6 +276,7 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const KvRegs<D, 
   float mx = x[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i]);
+  const float m0 = st.m;
   st.m = fmaxf(st.m, max16x32(mx));
   if constexpr (VB < 16) {
     // the largest scale of the tile: fp16 patterns of one sign are ordered as integers
@@ -296,7 +298,8 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const KvRegs<D, 
   }
   const float off = __builtin_fmaf(st.m, c, (float)(st.e - 15));
   if (__ballot(off != st.off) != 0) {
-    const float f = __builtin_amdgcn_exp2f(st.off - off);
+    // (0 while no score was finite: the sums are 0, and off, relative to no score, may lie above)
+    const float f = m0 > kNoScore ? __builtin_amdgcn_exp2f(st.off - off) : 0.f;
     st.l *= f;
 #pragma unroll
     for (int cg = 0; cg < G; ++cg)
@@ -464,8 +467,8 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KB, VB)) void k_attend(
 #pragma unroll
       for (int j = 0; j < 4; ++j) st.o[c][j] = f32x4{};
     st.l = 0.f;
-    st.m = -1e30f;
-    st.off = -1e30f;
+    st.m = kNoScore;
+    st.off = kNoScore;
     st.e = VB < 16 ? -14 : 0;
     // ---- this wave's tiles: first + wave, first + wave + 4, ...
     int t = first + wave;

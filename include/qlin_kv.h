@@ -114,8 +114,9 @@ qlin_status qlin_kv_read(const qlin_kv_cache* cache, const qlin_kv_seqs* seqs,
  *   lse  fp32 [seqs, heads] contiguous, 4-byte aligned, or NULL.
  * A row without tokens (or whose scores are all -inf) is zero, its lse -inf.
  * What lies in masked places (behind a sequence's end, before its window, in
- * pages that are not in the table) does not matter, NaN included; a value that is
- * not finite in a place that is seen makes its row not finite.
+ * pages that are not in the table) does not matter, NaN included.  Of the tokens that are
+ * seen, one whose score is -inf weighs nothing; a score of +inf or NaN makes its row not finite,
+ * and so does a value that is not finite, in its dims, whatever its token weighs.
  * Keys and values enter as the exact values of their codes; sums, the
  * softmax's statistics and scales are held in fp32, P with 21 bits or more, and
  * none of it below 2^-39 of the largest P * s.

@@ -1,0 +1,80 @@
+"""Attention over the cache where scores or values go to extremes: scores that are -inf."""
+import numpy as np
+import pytest
+import torch
+
+import kv_ref as kr
+from group_wise_bit_amd import qlin
+from test_gpu_kv import dev, host, new_cache, new_table
+
+pytestmark = pytest.mark.gpu
+
+
+def put(cache, ref, table, k, v, counts):
+    """Rows of k and v as the sequences' tokens; the reference is given what the library wrote."""
+    starts = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    lengths = np.asarray(counts, np.int32)
+    qlin.kv_write(cache, dev(k.astype(np.float16)), dev(v.astype(np.float16)), dev(table), dev(lengths),
+                  starts=dev(starts))
+    ref.data[:] = host(cache.data).reshape(ref.data.shape)
+    return lengths
+
+
+def widened(table, width):
+    """The same pages in a table of more places (above 1024 tokens sequences are split)."""
+    out = np.full((len(table), width), -1, np.int32)
+    out[:, :table.shape[1]] = table
+    return out
+
+
+@pytest.mark.parametrize("vb", [4, 16])
+@pytest.mark.parametrize("scale", [0.125, 0.7, 1.0, -1.0, 30.0])
+@pytest.mark.parametrize("width", [6, 40])
+def test_scores_without_end(vb, scale, width):
+    """Keys of -inf (kept with 16 bits) give scores of -inf, which weigh nothing: in a wave's first
+    tiles, in later ones, in single tokens, in all of a row's."""
+    rng = np.random.default_rng(21)
+    cache, ref = new_cache(rng, 24, 1, 64, 32, 16, vb)
+    table = new_table(rng, 4, 6, 24)
+    counts = [170, 170, 170, 170]
+    k, v = rng.uniform(-1, 1, (680, 1, 64)), rng.standard_normal((680, 1, 64))
+    pos = np.arange(680) % 170
+    seq = np.arange(680) // 170
+    gone = np.select([seq == 0, seq == 1, seq == 2], [pos < 128, (pos >= 64) & (pos < 150), pos % 7 < 5], True)
+    k[gone, 0, 5] = -np.inf * np.sign(scale)
+    lengths = put(cache, ref, table, k, v, counts)
+    q = rng.uniform(0.5, 1, (4, 3, 64)).astype(np.float16)
+    o, o16, lse = qlin.kv_attention(cache, dev(q), dev(widened(table, width)), dev(lengths), scale=scale,
+                                    want_lse=True)
+    o, o16, lse = host(o), host(o16), host(lse)
+    # the definition: over the tokens whose scores are finite
+    for b in range(3):
+        here = ~gone[seq == b]
+        sub, sub_ref = new_cache(rng, 6, 1, 64, 32, 16, vb)
+        n = put(sub, sub_ref, np.arange(6, dtype=np.int32)[None], k[seq == b][here], v[seq == b][here],
+                [int(here.sum())])
+        want, wl, eo, el = kr.attention(sub_ref, q[b:b + 1], np.arange(6)[None], n, scale, 0)
+        kr.check(o[b:b + 1], want, eo, ("O", b))
+        kr.check16(o16[b:b + 1], want, eo, ("O16", b))
+        kr.check(lse[b:b + 1], wl, el, ("lse", b))
+    assert not o[3].any() and not o16[3].any() and np.isneginf(lse[3]).all()
+
+
+@pytest.mark.parametrize("width", [6, 40])
+def test_infinite_queries(width):
+    """A query of inf on keys below 0 scores -inf everywhere: zeros, and only in its own rows."""
+    rng = np.random.default_rng(22)
+    cache, ref = new_cache(rng, 6, 1, 64, 32, 16, 8)
+    table = new_table(rng, 1, 6, 6)
+    k, v = -rng.uniform(0.5, 1, (150, 1, 64)), rng.standard_normal((150, 1, 64))
+    lengths = put(cache, ref, table, k, v, [150])
+    q = rng.uniform(-1, 1, (1, 3, 64)).astype(np.float16)
+    q[0, 1, 3] = np.inf
+    o, _, lse = qlin.kv_attention(cache, dev(q), dev(widened(table, width)), dev(lengths), scale=1.0,
+                                  want_lse=True)
+    o, lse = host(o), host(lse)
+    assert not o[0, 1].any() and np.isneginf(lse[0, 1])
+    rest = [0, 2]
+    want, wl, eo, el = kr.attention(ref, q[:, rest], table, lengths, 1.0, 0)
+    kr.check(o[:, rest], want, eo, "O")
+    kr.check(lse[:, rest], wl, el, "lse")
