@@ -37,7 +37,7 @@ struct AttendArgs {
   int64_t ldo;
   float* lse;
   float* part;               // [2 work-groups][rows][D]: sums of cut sequences
-  float* stat;               // [2 work-groups][rows][2]: their offset and weight
+  float* stat;               // [2 work-groups][rows][2]: their largest score and weight
   int heads, kv_heads, ratio;
   int rows;                  // query heads per work-group, min(ratio, 16)
   int rts;                   // work-groups' row blocks per head of the cache
@@ -159,12 +159,12 @@ __device__ __forceinline__ float sum16x32(float v) {
 
 // The running state of a wave for 16 query heads: lane (g, n) = (l / 16, l % 16) has the
 // sums of head n for dims 64 c + 16 g + 4 i + j in o[c][j][i], and the weight l of its
-// own tokens.  All are relative to 2^off.
+// own tokens.  All are relative to 2^(m c + e - 15).
 template <int D>
 struct AttendState {
   static constexpr int G = D / 64;
   f32x4 o[G][4];
-  float l, m, off;
+  float l, m;                // m: the largest q . k so far
   int e;                     // exponent of the largest scale of values so far (uniform)
 };
 
@@ -174,8 +174,9 @@ struct AttendState {
 // no data crosses lanes but the maximum.  Scales of keys multiply the sums of a
 // group; scales of values multiply P, which enters as two fp16 halves (hi rounded
 // towards zero, lo the rest: 21 bits).  So that P * s has these bits whatever the
-// size of s, P is taken relative to 2^off, off = max + e - 15, s < 2^e for every scale
-// so far: P s < 2^15.
+// size of s, P is taken relative to 2^(max + e - 15), s < 2^e for every scale so far:
+// P s < 2^15.  Exponents are formed from differences to the maximum, which fp32 holds
+// whatever the size of the scores (from 2^24 on a rounding of max c alone would be 1 or more).
 template <int D, int KB, int VB>
 __device__ __forceinline__ void attend_tile(AttendState<D>& st, const KvRegs<D, KB, VB>& t,
                                             const f16x8 (&q)[D / 32], float c, bool edge, int first,
@@ -277,6 +278,7 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const KvRegs<D, 
 #pragma unroll
   for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i]);
   const float m0 = st.m;
+  const int e0 = st.e;
   st.m = fmaxf(st.m, max16x32(mx));
   if constexpr (VB < 16) {
     // the largest scale of the tile: fp16 patterns of one sign are ordered as integers
@@ -296,21 +298,19 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const KvRegs<D, 
     all = max(all, __builtin_amdgcn_readlane(one, 48));
     st.e = max(st.e, (all >> 10) - 14);
   }
-  const float off = __builtin_fmaf(st.m, c, (float)(st.e - 15));
-  if (__ballot(off != st.off) != 0) {
-    // (0 while no score was finite: the sums are 0, and off, relative to no score, may lie above)
-    const float f = m0 > kNoScore ? __builtin_amdgcn_exp2f(st.off - off) : 0.f;
+  if (__ballot(st.m != m0 || st.e != e0) != 0) {
+    const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(m0 - st.m, c, (float)(e0 - st.e)));
     st.l *= f;
 #pragma unroll
     for (int cg = 0; cg < G; ++cg)
 #pragma unroll
       for (int j = 0; j < 4; ++j) st.o[cg][j] *= f;
-    st.off = off;
   }
+  const float unit = (float)(15 - st.e);
   float p[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -off));
+    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i] - st.m, c, unit));
     st.l += p[i];
   }
   union { f16x8 v; f16x2 p[4]; } ph, pl;
@@ -468,7 +468,6 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KB, VB)) void k_attend(
       for (int j = 0; j < 4; ++j) st.o[c][j] = f32x4{};
     st.l = 0.f;
     st.m = kNoScore;
-    st.off = kNoScore;
     st.e = VB < 16 ? -14 : 0;
     // ---- this wave's tiles: first + wave, first + wave + 4, ...
     int t = first + wave;
@@ -524,21 +523,22 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KB, VB)) void k_attend(
         }
       }
     }
-    st.l = sum16x32(st.l);
-    // ---- the waves' sums together: 2 and 3 to 0 and 1, 1 to 0
+    // ---- the waves' sums together, relative to 2^(m c): 2 and 3 to 0 and 1, 1 to 0
+    const float unit = (float)(st.e - 15);
+    st.l = sum16x32(st.l) * __builtin_amdgcn_exp2f(unit);
     if (g == 0) {
-      rst[wave][n][0] = st.off;
+      rst[wave][n][0] = st.m;
       rst[wave][n][1] = st.l;
     }
     lds_barrier();
-    float off = rst[0][n][0];
+    float m = rst[0][n][0];
 #pragma unroll
-    for (int w = 1; w < kAttendWaves; ++w) off = fmaxf(off, rst[w][n][0]);
+    for (int w = 1; w < kAttendWaves; ++w) m = fmaxf(m, rst[w][n][0]);
     float l = 0.f;
 #pragma unroll
     for (int w = 0; w < kAttendWaves; ++w)
-      l += rst[w][n][1] * __builtin_amdgcn_exp2f(rst[w][n][0] - off);
-    const float f = __builtin_amdgcn_exp2f(st.off - off);
+      l += rst[w][n][1] * __builtin_amdgcn_exp2f((rst[w][n][0] - m) * a.c);
+    const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(st.m - m, a.c, unit));
     // a lane's 16 dims of a group: 4 i + j
     auto put = [&](float* to) {
 #pragma unroll
@@ -583,7 +583,7 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KB, VB)) void k_attend(
               *(f32x4*)(a.part + slot * D + c * 64 + g * 16 + 4 * i) =
                   f32x4{st.o[c][0][i], st.o[c][1][i], st.o[c][2][i], st.o[c][3][i]};
           if (g == 0) {
-            a.stat[slot * 2] = off;
+            a.stat[slot * 2] = m;
             a.stat[slot * 2 + 1] = l;
           }
         } else {
@@ -604,7 +604,8 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KB, VB)) void k_attend(
             }
           if (a.lse != nullptr && g == 0)
             a.lse[(int64_t)b * a.heads + h] =
-                l == 0.f ? -__builtin_inff() : (off + __builtin_log2f(l)) * 0.69314718055994531f;
+                l == 0.f ? -__builtin_inff()
+                         : __builtin_fmaf(m, a.c, __builtin_log2f(l)) * 0.69314718055994531f;
         }
       }
     }
@@ -620,7 +621,7 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KB, VB)) void k_attend(
 }
 
 // The parts of the sequences that more than one work-group dealt with, and rows without
-// tokens: O = sum of 2^(off_i - max) O_i over the same of l_i.  One work-group per (sequence, query
+// tokens: O = sum of 2^((m_i - max) c) O_i over the same of l_i.  One work-group per (sequence, query
 // head): a thread per part for its weight, then D / 4 threads per part, 1024 / D of them at
 // a time, eight loads of a thread in flight.  Bound by two rounds of loads, one behind the other:
 // 4.0 to 5.5 us, of 1 to 1024 parts.
@@ -647,7 +648,7 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a) {
     all += __builtin_amdgcn_readlane(sum, 63);
   }
   f32x4 o{};
-  float l = 0.f, top = -1e30f;
+  float l = 0.f, top = kNoScore;
   const int sub = tid / kLanes, d = tid % kLanes;
   if (units > 0) {
     const int64_t share = unit_share(all * hgs, a.groups);
@@ -661,7 +662,7 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a) {
 #pragma unroll
     for (int j = 0; j < kMaxParts / 256; ++j) {
       const int i = j * 256 + tid;
-      pm[j] = i < parts ? a.stat[place(i) * 2] : -1e30f;
+      pm[j] = i < parts ? a.stat[place(i) * 2] : kNoScore;
       pl[j] = i < parts ? a.stat[place(i) * 2 + 1] : 0.f;
       top = fmaxf(top, pm[j]);
     }
@@ -672,7 +673,7 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a) {
 #pragma unroll
     for (int j = 0; j < kMaxParts / 256; ++j) {
       const int i = j * 256 + tid;
-      const float f = __builtin_amdgcn_exp2f(pm[j] - top);
+      const float f = __builtin_amdgcn_exp2f((pm[j] - top) * a.c);
       if (i < parts) weight[i] = f;
       l += pl[j] * f;
     }
@@ -704,7 +705,8 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttendArgs a) {
   }
   if (a.lse != nullptr && d == 0)
     a.lse[(int64_t)b * a.heads + h] =
-        l == 0.f ? -__builtin_inff() : (top + __builtin_log2f(l)) * 0.69314718055994531f;
+        l == 0.f ? -__builtin_inff()
+                 : __builtin_fmaf(top, a.c, __builtin_log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace qlin

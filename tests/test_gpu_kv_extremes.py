@@ -1,4 +1,4 @@
-"""Attention over the cache where scores or values go to extremes: scores that are -inf."""
+"""Attention over the cache where scores go to extremes: -inf, and far beyond those of models."""
 import numpy as np
 import pytest
 import torch
@@ -78,3 +78,52 @@ def test_infinite_queries(width):
     want, wl, eo, el = kr.attention(ref, q[:, rest], table, lengths, 1.0, 0)
     kr.check(o[:, rest], want, eo, "O")
     kr.check(lse[:, rest], wl, el, "lse")
+
+
+@pytest.mark.parametrize("kb,vb", [(4, 4), (8, 8), (16, 16)])
+@pytest.mark.parametrize("scale", [2.0 ** 20, -2.0 ** 20, 2.0 ** 12, 16.0, 1.0])
+@pytest.mark.parametrize("width", [6, 40])
+def test_far_scores(kb, vb, scale, width):
+    """Scores of any size the arguments allow.  Keys and queries are whole numbers that the cache
+    holds exactly (a group's range is 15 or 255 steps of 1), so that fp32 holds every score
+    q . k < 2^24 and their differences, and a weight is wrong by the rounding of its own
+    exponent only: 4 U relative to |S - max S|, which is 40 at most where it counts."""
+    rng = np.random.default_rng(23)
+    seqs, n = 3, 170
+    cache, ref = new_cache(rng, 6 * seqs, 1, 128, 32, kb, vb)
+    table = new_table(rng, seqs, 6, 6 * seqs)
+    low, high = (-7, 8) if kb == 4 else (-127, 128)
+    k = rng.integers(low, high + 1, (seqs * n, 1, 128)).astype(float)
+    k[:, :, ::64], k[:, :, 1::64] = low, high
+    # tokens that score the same as another, by 1 less, and by 2 less
+    for b in range(seqs):
+        for i, at in enumerate((40, 41, 90, 169)):
+            k[b * n + at] = k[b * n + 11]
+            k[b * n + at, 0, 2] += (i % 3) * (-1 if k[b * n + 11, 0, 2] > 0 else 1)
+    v = rng.uniform(-2, 2, (seqs * n, 1, 128))
+    lengths = put(cache, ref, table, k, v, [n] * seqs)
+    q = np.round(rng.integers(-200, 201, (seqs, 3, 128)))
+    q[:, :, 2] = 1
+    for b in range(seqs):                        # one query that token 11 scores highest on
+        q[b, 2] = np.sign(scale) * np.clip(k[b * n + 11, 0] * 3, -300, 300)
+        q[b, 2, 2] = 1
+    q = q.astype(np.float16)
+    o, o16, lse = qlin.kv_attention(cache, dev(q), dev(widened(table, width)), dev(lengths), scale=scale,
+                                    want_lse=True)
+    o, o16, lse = host(o), host(o16), host(lse)
+    for b in range(seqs):
+        kk, vv = ref.sequence(table, b, 0, n)
+        assert np.array_equal(kk[:, 0], k[b * n:(b + 1) * n, 0])
+        for h in range(3):
+            x = kk[:, 0] @ q[b, h].astype(float)
+            assert (np.abs(kk[:, 0]) @ np.abs(q[b, h].astype(float))).max() < 2 ** 24
+            s = scale * x
+            p = np.exp(s - s.max())
+            total = p.sum()
+            want = (p / total) @ vv[:, 0]
+            err = (p / total) @ np.abs(vv[:, 0]) * (2 * kr.U * (4 * 40 + n + 64) + 2.0 ** -20) + \
+                n * 2.0 ** -38 * np.abs(vv).max()
+            kr.check(o[b, h], want, err, ("O", b, h))
+            kr.check16(o16[b, h], want, err, ("O16", b, h))
+            wl = s.max() + np.log(total)
+            kr.check(lse[b, h], wl, (n + 64) * kr.U + 8 * kr.U * (abs(wl) + 1), ("lse", b, h))
