@@ -1,6 +1,6 @@
 // Attention of one new token per sequence over the cache (gfx950, wave64):
 //     S[p] = scale q . k_p,   P = exp(S - max),   O = sum P v_p / sum P,
-// in one pass over the cached tokens with a running maximum and sum; k = s (code - z).
+// in one pass over the cached tokens with running sums and a unit of them; k = s (code - z).
 //
 // What bounds it.  Every code is read once and takes part in 4 ratio operations, far below
 // what the matrix cores do, so that the bytes of the cache are the floor.  With 8 bits and more they
@@ -37,7 +37,7 @@ struct AttendArgs {
   int64_t ldo;
   float* lse;
   float* part;               // [2 work-groups][rows][D]: sums of cut sequences
-  float* stat;               // [2 work-groups][rows][2]: their largest score and weight
+  float* stat;               // [2 work-groups][rows][2]: the score they are relative to, their weight
   int heads, kv_heads, ratio;
   int rows;                  // query heads per work-group, min(ratio, 16)
   int rts;                   // work-groups' row blocks per head of the cache
@@ -159,13 +159,12 @@ __device__ __forceinline__ float sum16x32(float v) {
 
 // The running state of a wave for 16 query heads: lane (g, n) = (l / 16, l % 16) has the
 // sums of head n for dims 64 c + 16 g + 4 i + j in o[c][j][i], and the weight l of its
-// own tokens.  All are relative to 2^(m c + e - 15).
+// own tokens.  A token of score x weighs p = 2^((x - r) c + k).
 template <int D>
 struct AttendState {
   static constexpr int G = D / 64;
   f32x4 o[G][4];
-  float l, m;                // m: the largest q . k so far
-  int e;                     // exponent of the largest scale of values so far (uniform)
+  float l, r, k;
 };
 
 // A tile of 32 tokens.  Keys are the rows of the first products' A operand and query
@@ -173,10 +172,17 @@ struct AttendState {
 // of each half -- the order in which the second products' B operand wants P, with values as the rows of A:
 // no data crosses lanes but the maximum.  Scales of keys multiply the sums of a
 // group; scales of values multiply P, which enters as two fp16 halves (hi rounded
-// towards zero, lo the rest: 21 bits).  So that P * s has these bits whatever the
-// size of s, P is taken relative to 2^(max + e - 15), s < 2^e for every scale so far:
-// P s < 2^15.  Exponents are formed from differences to the maximum, which fp32 holds
-// whatever the size of the scores (from 2^24 on a rounding of max c alone would be 1 or more).
+// towards zero, lo the rest: 21 bits).  So that P * s has these bits whatever the sizes of s
+// and of P where s is large, p is taken in units in which the largest p s so far is 2^15 to
+// 2^16 (an s below 2^-24, fp16's least number, counts as that, so that weights stay below
+// 2^40): where a p s reaches 2^16, k falls, and where it does by far (with the first tile of a
+// wave, say), r rises to the largest score.  As long as none does, no lane needs to know of
+// another's scores.  Exponents are formed from differences of scores, which fp32 holds whatever
+// their size (from 2^24 on a rounding of r c alone would be 1 or more).
+constexpr float kRoom = 0x1p16f;
+constexpr float kFar = 0x1p64f;        // p s from here on, and k below kLeast: r is taken anew, too
+constexpr float kLeast = -32.f;
+constexpr float kUnset = 1000.f;       // k of no token: the first weight is beyond any room
 template <int D, int KB, int VB>
 __device__ __forceinline__ void attend_tile(AttendState<D>& st, const KvRegs<D, KB, VB>& t,
                                             const f16x8 (&q)[D / 32], float c, bool edge, int first,
@@ -274,45 +280,56 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const KvRegs<D, 
       }
     }
   }
-  float mx = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i]);
-  const float m0 = st.m;
-  const int e0 = st.e;
-  st.m = fmaxf(st.m, max16x32(mx));
+  // the largest scale of a token's groups (a NaN is passed over)
+  uint32_t top[4];
   if constexpr (VB < 16) {
-    // the largest scale of the tile: fp16 patterns of one sign are ordered as integers
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    u16x2 top{};
 #pragma unroll
-    for (int cg = 0; cg < G; ++cg)
+    for (int i = 0; i < 4; ++i) {
+      top[i] = 0x00010001u;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t pair = vs[cg][i];
-        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, pair));
-      }
-    const int one = max((int)top[0], (int)top[1]);
-    int all = __builtin_amdgcn_readlane(one, 0);
-    all = max(all, __builtin_amdgcn_readlane(one, 16));
-    all = max(all, __builtin_amdgcn_readlane(one, 32));
-    all = max(all, __builtin_amdgcn_readlane(one, 48));
-    st.e = max(st.e, (all >> 10) - 14);
+      for (int cg = 0; cg < G; ++cg) top[i] = pk_max(top[i], vs[cg][i]);
+    }
   }
-  if (__ballot(st.m != m0 || st.e != e0) != 0) {
-    const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(m0 - st.m, c, (float)(e0 - st.e)));
+  float p[8];
+  // the weights, and the largest p s of the lane's tokens
+  auto weigh = [&](float r, float k) {
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i] - r, c, k));
+      most = fmaxf(most, VB < 16 ? __builtin_fmaf((float)as_h2(top[i / 2])[i % 2], p[i], mix.zero) : p[i]);
+    }
+    return most;
+  };
+  float most = weigh(st.r, st.k);
+  if (__ballot(most >= kRoom) != 0) {
+    most = max16x32(most);
+    float r = st.r, k = fminf(st.k, st.k + (float)(16 - __builtin_amdgcn_frexp_expf(most)));
+    if (__ballot(most >= kFar || k < kLeast) != 0) {
+      r = x[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) r = fmaxf(r, x[i]);
+      r = fmaxf(st.r, max16x32(r));
+      // (a tile whose weights are all 0 leaves k as it is)
+      most = fmaxf(max16x32(weigh(r, 0.f)), 0x1p-126f);
+      k = fminf(__builtin_fmaf(r - st.r, c, st.k), (float)(16 - __builtin_amdgcn_frexp_expf(most)));
+      weigh(r, k);
+    } else {
+      const float f = __builtin_amdgcn_exp2f(k - st.k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] *= f;
+    }
+    const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(st.r - r, c, k - st.k));
     st.l *= f;
 #pragma unroll
     for (int cg = 0; cg < G; ++cg)
 #pragma unroll
       for (int j = 0; j < 4; ++j) st.o[cg][j] *= f;
+    st.r = r;
+    st.k = k;
   }
-  const float unit = (float)(15 - st.e);
-  float p[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i] - st.m, c, unit));
-    st.l += p[i];
-  }
+  for (int i = 0; i < 8; ++i) st.l += p[i];
   union { f16x8 v; f16x2 p[4]; } ph, pl;
 #pragma unroll
   for (int cg = 0; cg < G; ++cg) {
@@ -467,8 +484,8 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KB, VB)) void k_attend(
 #pragma unroll
       for (int j = 0; j < 4; ++j) st.o[c][j] = f32x4{};
     st.l = 0.f;
-    st.m = kNoScore;
-    st.e = VB < 16 ? -14 : 0;
+    st.r = kNoScore;
+    st.k = kUnset;
     // ---- this wave's tiles: first + wave, first + wave + 4, ...
     int t = first + wave;
     if (t < last) {
@@ -523,22 +540,21 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KB, VB)) void k_attend(
         }
       }
     }
-    // ---- the waves' sums together, relative to 2^(m c): 2 and 3 to 0 and 1, 1 to 0
-    const float unit = (float)(st.e - 15);
-    st.l = sum16x32(st.l) * __builtin_amdgcn_exp2f(unit);
+    // ---- the waves' sums together, relative to 2^(r c): 2 and 3 to 0 and 1, 1 to 0
+    st.l = sum16x32(st.l) * __builtin_amdgcn_exp2f(-st.k);
     if (g == 0) {
-      rst[wave][n][0] = st.m;
+      rst[wave][n][0] = st.r;
       rst[wave][n][1] = st.l;
     }
     lds_barrier();
-    float m = rst[0][n][0];
+    float r = rst[0][n][0];
 #pragma unroll
-    for (int w = 1; w < kAttendWaves; ++w) m = fmaxf(m, rst[w][n][0]);
+    for (int w = 1; w < kAttendWaves; ++w) r = fmaxf(r, rst[w][n][0]);
     float l = 0.f;
 #pragma unroll
     for (int w = 0; w < kAttendWaves; ++w)
-      l += rst[w][n][1] * __builtin_amdgcn_exp2f((rst[w][n][0] - m) * a.c);
-    const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(st.m - m, a.c, unit));
+      l += rst[w][n][1] * __builtin_amdgcn_exp2f((rst[w][n][0] - r) * a.c);
+    const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(st.r - r, a.c, -st.k));
     // a lane's 16 dims of a group: 4 i + j
     auto put = [&](float* to) {
 #pragma unroll
@@ -583,7 +599,7 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KB, VB)) void k_attend(
               *(f32x4*)(a.part + slot * D + c * 64 + g * 16 + 4 * i) =
                   f32x4{st.o[c][0][i], st.o[c][1][i], st.o[c][2][i], st.o[c][3][i]};
           if (g == 0) {
-            a.stat[slot * 2] = m;
+            a.stat[slot * 2] = r;
             a.stat[slot * 2 + 1] = l;
           }
         } else {
@@ -605,7 +621,7 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KB, VB)) void k_attend(
           if (a.lse != nullptr && g == 0)
             a.lse[(int64_t)b * a.heads + h] =
                 l == 0.f ? -__builtin_inff()
-                         : __builtin_fmaf(m, a.c, __builtin_log2f(l)) * 0.69314718055994531f;
+                         : __builtin_fmaf(r, a.c, __builtin_log2f(l)) * 0.69314718055994531f;
         }
       }
     }
@@ -621,7 +637,7 @@ __global__ __launch_bounds__(256, attend_occupancy(D, KB, VB)) void k_attend(
 }
 
 // The parts of the sequences that more than one work-group dealt with, and rows without
-// tokens: O = sum of 2^((m_i - max) c) O_i over the same of l_i.  One work-group per (sequence, query
+// tokens: O = sum of 2^((r_i - max) c) O_i over the same of l_i.  One work-group per (sequence, query
 // head): a thread per part for its weight, then D / 4 threads per part, 1024 / D of them at
 // a time, eight loads of a thread in flight.  Bound by two rounds of loads, one behind the other:
 // 4.0 to 5.5 us, of 1 to 1024 parts.

@@ -37,6 +37,13 @@ struct KvSeqs {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
+// The larger ones of two pairs of fp16 numbers (of a NaN and another the other one).
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("v_pk_max_f16 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+
 // Inclusive sum over the wave's lanes (within rows of 16, then row 0's into row 1
 // and 2's into 3, then the lower half's into the upper).
 template <int CTRL, int ROWS>

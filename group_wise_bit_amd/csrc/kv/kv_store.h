@@ -116,11 +116,6 @@ __device__ __forceinline__ uint32_t pk_min(uint32_t a, uint32_t b) {
   asm("v_pk_min_f16 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("v_pk_max_f16 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
-  return r;
-}
 template <int N>
 __device__ __forceinline__ uint32_t range_of(const uint32_t (&w)[N]) {
   typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));

@@ -1,4 +1,5 @@
-"""Attention over the cache where scores go to extremes: -inf, and far beyond those of models."""
+"""Attention over the cache where scores or values go to extremes: scores of -inf and far beyond those of
+models, values whose sizes and weights lie far apart."""
 import numpy as np
 import pytest
 import torch
@@ -127,3 +128,106 @@ def test_far_scores(kb, vb, scale, width):
             kr.check16(o16[b, h], want, err, ("O16", b, h))
             wl = s.max() + np.log(total)
             kr.check(lse[b, h], wl, (n + 64) * kr.U + 8 * kr.U * (abs(wl) + 1), ("lse", b, h))
+
+
+def from_dim_0(cache, ref, q, table, lengths):
+    """(O, lse, their bounds) of queries that are 0 but in dim 0, with a scale of 1: a score is one
+    exact product.  A weight's exponent is rounded relative to S - max S, and once more for every
+    rise of the running maximum, 18 U of it in all.  A wave has tiles / 4 + 1 tiles at most; each adds
+    64 roundings of its products' sums, 8 of the weights', 8 of factors; exp, the waves' sums, parts
+    of other work-groups and the division add 100 + 2 tiles.  P s (P alone with 16 bits) is held to 21 bits and a step of 2^-39 of the row's
+    largest, P * 2^-24 at least, |q - z| <= qmax.  The codes of a group reach from 0 or 1 to qmax or
+    qmax - 1, so that its largest value is 7 s (127 s) at least and s qmax below 2.5 times that, s's
+    rounding to fp16 included."""
+    eo, el = np.zeros(q.shape), np.zeros(q.shape[:2])
+    o, lse = np.zeros(q.shape), np.zeros(q.shape[:2])
+    for b in range(len(q)):
+        k, v = (x[:, 0] for x in ref.sequence(table, b, 0, int(lengths[b])))
+        n, sizes = len(k), np.abs(v).max(-1)
+        for h in range(q.shape[1]):
+            s = k[:, 0] * float(q[b, h, 0])
+            p = np.exp(s - s.max())
+            tiles = -(-n // 32)
+            e = kr.U * (18 * (s.max() - s) + 80 * (tiles / 4 + 1) + 100 + 2 * tiles)
+            lse[b, h] = s.max() + np.log(p.sum())
+            p /= p.sum()
+            o[b, h] = p @ v
+            el[b, h] = p @ e + 8 * kr.U * (abs(lse[b, h]) + 1)
+            step = 2.0 ** -38 * p.max() * sizes.max() if ref.bits[1] == 16 else \
+                2.0 ** -39 * max((p * 2.5 * sizes).max(), p.max() * 2.0 ** -24 * 255)
+            eo[b, h] = (p * (e + p @ e + 2.0 ** -20)) @ np.abs(v) + n * step
+    return o, lse, eo, el
+
+
+@pytest.mark.parametrize("vb", [4, 8])
+@pytest.mark.parametrize("far", [12.0, 25.0, 40.0, 70.0])
+@pytest.mark.parametrize("width", [6, 40])
+def test_large_values_of_little_weight(vb, far, width):
+    """Tokens of large values whose scores lie far below, first, last, between others and alone in
+    a wave's tiles, do not cost the others their bits."""
+    rng = np.random.default_rng(24)
+    places = [[0], [31], [169], [3, 40, 100, 130], list(range(32, 64)), list(range(128, 170))]
+    seqs, n = len(places), 170
+    cache, ref = new_cache(rng, 6 * seqs, 1, 128, 32, 16, vb)
+    table = new_table(rng, seqs, 6, 6 * seqs)
+    k = rng.standard_normal((seqs * n, 1, 128))
+    v = 1.2e-4 * rng.uniform(-1, 1, (seqs * n, 1, 128))
+    k[:, :, 0] *= 0.1
+    for b, at in enumerate(places):
+        for i in at:
+            k[b * n + i, 0, 0] = -far
+            v[b * n + i] = rng.choice([-6e4, 5e4, 6e4], (1, 128))
+    lengths = put(cache, ref, table, k, v, [n] * seqs)
+    q = np.zeros((seqs, 3, 128), np.float16)
+    q[:, :, 0] = 1, 0.5, 0.25
+    o, _, lse = qlin.kv_attention(cache, dev(q), dev(widened(table, width)), dev(lengths), scale=1.0,
+                                  want_lse=True)
+    want, wl, eo, el = from_dim_0(cache, ref, q, table, lengths)
+    kr.check(host(o), want, eo, "O")
+    kr.check(host(lse), wl, el, "lse")
+
+
+@pytest.mark.parametrize("vb", [4, 8])
+@pytest.mark.parametrize("far", [5.0, 30.0, 60.0])
+def test_weight_on_tokens_without_values(vb, far):
+    """Where the highest scores are those of tokens whose values are zeros, or are small, the
+    output comes from the others."""
+    rng = np.random.default_rng(25)
+    n = 170
+    for small in (0.0, 1e-4):
+        for at in ([0], [169], [5, 77], list(range(96, 128))):
+            cache, ref = new_cache(rng, 6, 1, 64, 32, 16, vb)
+            table = new_table(rng, 1, 6, 6)
+            k, v = rng.standard_normal((n, 1, 64)), rng.uniform(-2, 2, (n, 1, 64))
+            k[:, :, 0] *= 0.1
+            k[at, 0, 0] = far
+            v[at] *= small
+            lengths = put(cache, ref, table, k, v, [n])
+            q = np.zeros((1, 4, 64), np.float16)
+            q[:, :, 0] = 1, 0.5, 0.25, 0
+            for width in (6, 40):
+                o, _, lse = qlin.kv_attention(cache, dev(q), dev(widened(table, width)), dev(lengths),
+                                              scale=1.0, want_lse=True)
+                want, wl, eo, el = from_dim_0(cache, ref, q, table, lengths)
+                kr.check(host(o), want, eo, ("O", small, at[0], width))
+                kr.check(host(lse), wl, el, ("lse", small, at[0], width))
+
+
+@pytest.mark.parametrize("vb", [4, 8, 16])
+@pytest.mark.parametrize("step", [0.3, -0.3, 2.0, -2.0])
+def test_scores_that_climb(vb, step):
+    """Scores that rise or fall from token to token, and values that do the reverse."""
+    rng = np.random.default_rng(26)
+    n = 1300
+    cache, ref = new_cache(rng, 41, 1, 64, 32, 16, vb)
+    table = new_table(rng, 1, 41, 41)
+    k, v = rng.standard_normal((n, 1, 64)), rng.uniform(-1, 1, (n, 1, 64))
+    k[:, 0, 0] = (step * np.arange(n)) % 700.0
+    v *= np.exp(-np.minimum((abs(step) * np.arange(n)) % 20.0, 9.0))[:, None, None]
+    lengths = put(cache, ref, table, k, v, [n])
+    q = np.zeros((1, 2, 64), np.float16)
+    q[:, :, 0] = 1, -0.5
+    o, _, lse = qlin.kv_attention(cache, dev(q), dev(table), dev(lengths), scale=1.0, want_lse=True)
+    want, wl, eo, el = from_dim_0(cache, ref, q, table, lengths)
+    kr.check(host(o), want, eo, "O")
+    kr.check(host(lse), wl, el, "lse")
