@@ -21,6 +21,8 @@
 
 namespace qlin {
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kAttendWaves = 4;
 constexpr int kAttendRows = 16;        // query heads of a work-group: a column block of an MFMA
 constexpr int kMaxParts = 1024;        // work-groups at most, and parts of a sequence
@@ -172,9 +174,9 @@ struct AttendState {
 // of each half -- the order in which the second products' B operand wants P, with values as the rows of A:
 // no data crosses lanes but the maximum.  Scales of keys multiply the sums of a
 // group; scales of values multiply P, which enters as two fp16 halves (hi rounded
-// towards zero, lo the rest: 21 bits).  So that P * s has these bits whatever the sizes of s
-// and of P where s is large, p is taken in units in which the largest p s so far is 2^15 to
-// 2^16 (an s below 2^-24, fp16's least number, counts as that, so that weights stay below
+// towards zero, lo the rest to nearest: 22 bits, and no side that all roundings go to).  So that
+// P * s has these bits whatever the sizes of s and of P where s is large, p is taken in units in
+// which the largest p s so far is 2^14 to 2^16 (an s below 2^-24, fp16's least number, counts as that, so that weights stay below
 // 2^40): where a p s reaches 2^16, k falls, and where it does by far (with the first tile of a
 // wave, say), r rises to the largest score.  As long as none does, no lane needs to know of
 // another's scores.  Exponents are formed from differences of scores, which fp32 holds whatever
@@ -304,7 +306,7 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const KvRegs<D, 
   float most = weigh(st.r, st.k);
   if (__ballot(most >= kRoom) != 0) {
     most = max16x32(most);
-    float r = st.r, k = fminf(st.k, st.k + (float)(16 - __builtin_amdgcn_frexp_expf(most)));
+    float r = st.r, k = fminf(st.k, st.k + (float)(15 - __builtin_amdgcn_frexp_expf(most)));
     if (__ballot(most >= kFar || k < kLeast) != 0) {
       r = x[0];
 #pragma unroll
@@ -312,7 +314,7 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const KvRegs<D, 
       r = fmaxf(st.r, max16x32(r));
       // (a tile whose weights are all 0 leaves k as it is)
       most = fmaxf(max16x32(weigh(r, 0.f)), 0x1p-126f);
-      k = fminf(__builtin_fmaf(r - st.r, c, st.k), (float)(16 - __builtin_amdgcn_frexp_expf(most)));
+      k = fminf(__builtin_fmaf(r - st.r, c, st.k), (float)(15 - __builtin_amdgcn_frexp_expf(most)));
       weigh(r, k);
     } else {
       const float f = __builtin_amdgcn_exp2f(k - st.k);
@@ -343,9 +345,9 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const KvRegs<D, 
           w1 = __builtin_fmaf((float)as_h2(pair)[1], w1, mix.zero);
         }
         ph.p[i] = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(w0, w1));
-        pl.p[i] = __builtin_bit_cast(
-            f16x2, __builtin_amdgcn_cvt_pkrtz(__builtin_fmaf((float)ph.p[i][0], mix.minus, w0),
-                                              __builtin_fmaf((float)ph.p[i][1], mix.minus, w1)));
+        pl.p[i] = __builtin_convertvector(
+            (f32x2{__builtin_fmaf((float)ph.p[i][0], mix.minus, w0),
+                   __builtin_fmaf((float)ph.p[i][1], mix.minus, w1)}), f16x2);
       }
     }
     f16x2 c1[4], c2[4];

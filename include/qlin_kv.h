@@ -119,8 +119,8 @@ qlin_status qlin_kv_read(const qlin_kv_cache* cache, const qlin_kv_seqs* seqs,
  * and so does a value that is not finite, in its dims, whatever its token weighs.
  * Keys and values enter as the exact values of their codes; sums, the
  * softmax's statistics and scales are held in fp32, P * s (s the scale of the value's
- * group, 1 with 16 bits; what is below counts as 2^-24) with 21 bits or more, and none of it
- * below 2^-39 of the row's largest.
+ * group, 1 with 16 bits; what is below counts as 2^-24) to 2^-22 of it, rounded to
+ * nearest, or to 2^-39 of the row's largest where that is more.
  * Deterministic: the result depends on the inputs and, to the order of fp32 sums,
  * on the lengths of all the call's sequences.
  * The cache is read once: the tokens of all sequences are dealt out evenly over

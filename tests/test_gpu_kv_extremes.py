@@ -231,3 +231,19 @@ def test_scores_that_climb(vb, step):
     want, wl, eo, el = from_dim_0(cache, ref, q, table, lengths)
     kr.check(host(o), want, eo, "O")
     kr.check(host(lse), wl, el, "lse")
+
+
+def test_weights_are_rounded_to_either_side():
+    """Values that are 1 in a dim of their token's own add up to 1 over the dims, but for the rounding
+    of P to its two halves and that of the sums: 4 U at most, to either side, so that the mean of 512
+    rows is off by 16 U / sqrt(512) < U at four standard errors."""
+    rng = np.random.default_rng(27)
+    seqs, heads, n = 16, 32, 61
+    cache, ref = new_cache(rng, 2 * seqs, 1, 64, 32, 16, 16)
+    table = new_table(rng, seqs, 2, 2 * seqs)
+    k = rng.standard_normal((seqs * n, 1, 64))
+    v = np.tile(np.eye(64)[:n, None], (seqs, 1, 1))
+    lengths = put(cache, ref, table, k, v, [n] * seqs)
+    q = rng.standard_normal((seqs, heads, 64)).astype(np.float16)
+    o = host(qlin.kv_attention(cache, dev(q), dev(table), dev(lengths), scale=0.1)[0]).astype(np.float64)
+    assert abs((o.sum(-1) - 1).mean()) <= kr.U
