@@ -306,7 +306,7 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const KvRegs<D, 
   float most = weigh(st.r, st.k);
   if (__ballot(most >= kRoom) != 0) {
     most = max16x32(most);
-    float r = st.r, k = fminf(st.k, st.k + (float)(15 - __builtin_amdgcn_frexp_expf(most)));
+    float r = st.r, k = fminf(st.k, st.k + (float)(15 - __builtin_amdgcn_frexp_expf(most))), to = k - st.k;
     if (__ballot(most >= kFar || k < kLeast) != 0) {
       r = x[0];
 #pragma unroll
@@ -315,13 +315,13 @@ __device__ __forceinline__ void attend_tile(AttendState<D>& st, const KvRegs<D, 
       // (a tile whose weights are all 0 leaves k as it is)
       most = fmaxf(max16x32(weigh(r, 0.f)), 0x1p-126f);
       k = fminf(__builtin_fmaf(r - st.r, c, st.k), (float)(15 - __builtin_amdgcn_frexp_expf(most)));
-      weigh(r, k);
-    } else {
-      const float f = __builtin_amdgcn_exp2f(k - st.k);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] *= f;
+      // (above 40 only for a head without scores so far, whose p are 0)
+      to = fminf(k, 41.f);
     }
     const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(st.r - r, c, k - st.k));
+    to = __builtin_amdgcn_exp2f(to);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] *= to;
     st.l *= f;
 #pragma unroll
     for (int cg = 0; cg < G; ++cg)
