@@ -53,9 +53,10 @@ __device__ __forceinline__ SampleRow sample_row(const SampleArgs& a, int row) {
 __device__ __forceinline__ float logit_of(float l) {
   return l > -__builtin_inff() ? fminf(l, FLT_MAX) : -__builtin_inff();
 }
-// An integer of the same order, 0 for no token (the key of -inf is 0x007FFFFF).
+// An integer of the same order, 0 for no token (the key of -inf is 0x007FFFFF).  -0 is
+// equal to +0: the sum of both signs' zeros with +0 is +0.
 __device__ __forceinline__ uint32_t logit_key(float l) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, l);
+  const uint32_t b = __builtin_bit_cast(uint32_t, l + 0.f);
   return l == -__builtin_inff() ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
