@@ -437,23 +437,28 @@ __device__ __forceinline__ void sort_keys(uint64_t* keys, int size) {
 }
 
 // The gathered tokens are sorted into 1024 parts of their range, by t: bins a .. z share kMainParts
-// of them, the bin e has the rest.  Counts and masses of the parts (in steps of 2^-34
-// of bin a's / e's unit, the count from bit 50 on) tell where a cut lies; only the tokens of that part
-// are put in order.
+// of them, the bin e has the rest.  Counts and masses of the parts tell where a cut lies; only the
+// tokens of that part are put in order.  Masses are whole numbers of 2^-50 of bin a's (or e's)
+// unit, so that a sum does not depend on its order: 8192 tokens, exp(1 / 24) at most each, stay below
+// 2^64, and a token far below bin a's is off by 2^-51 of the unit (the sum over all kept ones,
+// the largest logit's among them, is 0.95 units at least).
 constexpr int kParts = 1024;
 constexpr int kMainParts = 896;
-constexpr int kPartCount = 50;
+constexpr int kPartStep = 50;
+static_assert(kListMax <= 1 << (63 - kPartStep), "sums of parts");
 
 struct PickShared {
   float l[kListMax];                         // the gathered tokens
   uint32_t index[kListMax];
   uint16_t part_of[kListMax];
   uint64_t keys[kListMax];                   // a part's tokens in order
-  unsigned long long part[kParts];           // sums up to a part
+  unsigned long long part[kParts];           // masses up to a part
+  uint32_t part_count[kParts];               // tokens up to a part
   double factor[kBins];
   unsigned long long slice_mass[kSlices];
   double wave[kSampleWaves];
   uint64_t scan[kSampleWaves];
+  uint32_t scan_count[kSampleWaves];
   double before, target, total;
   uint64_t cut;
   int slice, count[3], size, at, rank;
@@ -511,7 +516,7 @@ __device__ __forceinline__ int first_part(PickShared& sh, int from, int to, F re
   __syncthreads();
 #pragma unroll 1
   for (int i = from + threadIdx.x; i < to; i += kPickThreads)
-    if (reaches(sh.part[i]) && (i == from || !reaches(sh.part[i - 1]))) sh.at = i;
+    if (reaches(i) && (i == from || !reaches(i - 1))) sh.at = i;
   __syncthreads();
   return sh.at;
 }
@@ -595,8 +600,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
   const int n = p.n, main = p.main;
   const uint2* list = a.list + (int64_t)r * kListMax;
   uint64_t cut = 0;                            // keys up to it are kept
-  constexpr uint64_t kMassMask = (1ull << kPartCount) - 1;
-  constexpr double kStep = 1. / (double)(1ull << kMassStep);
+  constexpr double kStep = 1. / (double)(1ull << kPartStep);
   const double top_hi = (double)p.top * c.hi, top_lo = t_low((double)p.top, top_hi, c);
   // p of a token relative to the largest one's
   auto relative = [&](float l) {
@@ -670,7 +674,10 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
   __syncthreads();
   const double to_mass = p.a < kBins ? sh.factor[p.a] * kStep : 0.;   // bin a's
   if (n > kRankMax) {
-    for (int i = tid; i < kParts; i += kPickThreads) sh.part[i] = 0;
+    for (int i = tid; i < kParts; i += kPickThreads) {
+      sh.part[i] = 0;
+      sh.part_count[i] = 0;
+    }
     __syncthreads();
     const double scale = (double)kMainParts / (double)(p.z + 1 - p.a);
     // part and steps of a token
@@ -682,7 +689,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
       const double y = __builtin_fmin(__builtin_fmax(0.5 - x, 0.), 1.);
       double rel = bin_mass(x, poly) - (kMassOne - 1.);
       if (!extra) rel *= sh.factor[k - p.a];
-      steps = (uint64_t)__builtin_rint(rel * (double)(1ull << kMassStep));
+      steps = (uint64_t)__builtin_rint(rel * (double)(1ull << kPartStep));
       return extra ? kMainParts + min((int)(y * (kParts - kMainParts)), kParts - kMainParts - 1)
                    : min((int)(((double)(k - p.a) + y) * scale), kMainParts - 1);
     };
@@ -697,7 +704,8 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
       sh.l[i] = l;
       sh.index[i] = w0.x;
       sh.part_of[i] = (uint16_t)part;
-      atomicAdd(&sh.part[part], (unsigned long long)(steps | 1ull << kPartCount));
+      atomicAdd(&sh.part[part], (unsigned long long)steps);
+      atomicAdd(&sh.part_count[part], 1u);
       w0 = w1;
       w1 = w2;
     }
@@ -706,26 +714,34 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
     static_assert(kParts == 2 * kPickThreads && kMainParts % 128 == 0, "two parts a thread");
     {
       const uint64_t v0 = sh.part[2 * tid], v1 = sh.part[2 * tid + 1];
+      const uint32_t c0 = sh.part_count[2 * tid], c1 = sh.part_count[2 * tid + 1];
       uint64_t v = v0 + v1;
+      uint32_t q = c0 + c1;
       for (int d = 1; d < 64; d *= 2) {
-        const uint64_t o = shfl_up64(v, d);
-        if (lane >= d) v += o;
+        const uint64_t ov = shfl_up64(v, d);
+        const uint32_t oq = __shfl_up(q, d);
+        if (lane >= d) { v += ov; q += oq; }
       }
-      if (lane == 63) sh.scan[wave_id()] = v;
+      if (lane == 63) { sh.scan[wave_id()] = v; sh.scan_count[wave_id()] = q; }
       __syncthreads();
-      for (int w = 2 * tid >= kMainParts ? kMainParts / 128 : 0; w < wave_id(); ++w) v += sh.scan[w];
+      for (int w = 2 * tid >= kMainParts ? kMainParts / 128 : 0; w < wave_id(); ++w) {
+        v += sh.scan[w];
+        q += sh.scan_count[w];
+      }
       sh.part[2 * tid] = v - v1;
       sh.part[2 * tid + 1] = v;
+      sh.part_count[2 * tid] = q - c1;
+      sh.part_count[2 * tid + 1] = q;
       __syncthreads();
     }
-    auto count_to = [&](int part, int from) { return part > from ? (int)(sh.part[part - 1] >> kPartCount) : 0; };
-    auto mass_to = [&](int part, int from) { return part > from ? (double)(sh.part[part - 1] & kMassMask) : 0.; };
+    auto count_to = [&](int part, int from) { return part > from ? (int)sh.part_count[part - 1] : 0; };
+    auto mass_to = [&](int part, int from) { return part > from ? (double)sh.part[part - 1] : 0.; };
     // tokens of a .. z that are kept: the first `kept` of them in order
     int kept = p.k_main;
     int held = -1;                             // part of a .. z that sh.keys holds
     auto rank_of = [&](int want) {             // the want-th token is sh.keys[rank_of(want) - 1]
       if (held < 0 || want <= count_to(held, 0) || want > count_to(held, 0) + sh.size) {
-        held = first_part(sh, 0, kMainParts, [&](uint64_t v) { return (int)(v >> kPartCount) >= want; });
+        held = first_part(sh, 0, kMainParts, [&](int i) { return (int)sh.part_count[i] >= want; });
         order_part(sh, n, held);
       }
       return want - count_to(held, 0);
@@ -734,7 +750,7 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
       double mass_k = p.mass_k;
       if (p.e >= 0) {
         const int pe = first_part(sh, kMainParts, kParts,
-                                  [&](uint64_t v) { return (int)(v >> kPartCount) >= p.k_extra; });
+                                  [&](int i) { return (int)sh.part_count[i] >= p.k_extra; });
         order_part(sh, n, pe);
         mass_k += mass_to(pe, kMainParts) * sh.factor[p.e] * kStep +
                   mass_of_first(sh, p.k_extra - count_to(pe, kMainParts), f, c, poly);
@@ -744,8 +760,8 @@ __global__ __launch_bounds__(kPickThreads) void k_sample_pick(const SplitArgs a)
       }
       // the token with which the sum reaches the target (by rounding there may be none: all)
       const double target = (double)set.p * mass_k;
-      const int pp = first_part(sh, 0, kMainParts, [&](uint64_t v) {
-        return p.mass_a + (double)(v & kMassMask) * to_mass >= target; });
+      const int pp = first_part(sh, 0, kMainParts, [&](int i) {
+        return p.mass_a + (double)sh.part[i] * to_mass >= target; });
       if (pp < kParts && count_to(pp, 0) < kept) {
         if (held != pp) order_part(sh, n, pp);
         held = pp;
