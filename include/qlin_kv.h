@@ -61,7 +61,11 @@ typedef struct qlin_kv_cache {
 
 /* The sequences of a batch.  Sequence b has lengths[b] tokens; token p lies in
  * page table[b * ld + p / cache.page].  A length below 1 is an empty sequence. A
- * token beyond the table, or in a page that is not 0 .. pages - 1, is not there. */
+ * token beyond the table, or in a page that is not 0 .. pages - 1, is not there.
+ * Work-groups find their sequence by the lengths of all (rows with starts; attention with
+ * tables above 1024 tokens), so that such a call's time grows with the square of seqs from some
+ * thousands on: with one token and one head of 64 each, 1024 sequences take 13 us to write and
+ * 25 to attend to, 4096 102 and 104, 16384 1360 and 860. */
 typedef struct qlin_kv_seqs {
   int32_t seqs;             /* 0 .. 65536                                        */
   int32_t width;            /* pages per table row, width * cache.page <= 2^27   */
@@ -83,7 +87,9 @@ int64_t qlin_kv_page_bytes(int32_t head_dim, int32_t page, int32_t k_bits, int32
  * A token whose position is negative, or that is not there, is left out.  Nothing
  * but the written tokens changes in a page.  Two rows of a call must not go to the same place (a page
  * that is written belongs to one sequence): what such a place then holds is undefined.
- * m <= 2^20; seqs = 0 or m = 0 is a no-op.
+ * m <= 2^20; seqs = 0 or m = 0 is a no-op.  A call whose grid would have 2^32 threads is
+ * refused with QLIN_ERR_SHAPE: (m / 32 + 2 min(m, seqs)) * ceil(kv_heads * (2 + head_dim / 64) / 4),
+ * without starts seqs times the second factor, is below 2^24.
  */
 qlin_status qlin_kv_write(const qlin_kv_cache* cache, const uint16_t* K, int64_t ld_k,
                           const uint16_t* V, int64_t ld_v, int32_t m, const qlin_kv_seqs* seqs,
@@ -95,7 +101,7 @@ qlin_status qlin_kv_write(const qlin_kv_cache* cache, const uint16_t* K, int64_t
  * each value s * (q - z).  K and V are both fp16 (wide = 0: rounded to nearest even, +-65504 at
  * most unless the value is kept with 16 bits) or both fp32 (wide = 1: exact), [m, ld_k] and [m, ld_v],
  * pitches multiples of 8 (K and V may be columns of one matrix).  Rows of tokens that
- * are not there are zero; rows from starts[seqs] on are not written.
+ * are not there are zero; rows from starts[seqs] on are not written.  Limits as for qlin_kv_write.
  */
 qlin_status qlin_kv_read(const qlin_kv_cache* cache, const qlin_kv_seqs* seqs,
                          const int32_t* starts, int32_t m, void* K, int64_t ld_k, void* V,
@@ -123,12 +129,13 @@ qlin_status qlin_kv_read(const qlin_kv_cache* cache, const qlin_kv_seqs* seqs,
  * nearest, or to 2^-39 of the row's largest where that is more.
  * Deterministic: the result depends on the inputs and, to the order of fp32 sums,
  * on the lengths of all the call's sequences.
- * The cache is read once: the tokens of all sequences are dealt out evenly over
- * the work-groups, and the parts of a sequence joined in a second kernel.
+ * The cache is read once for every 16 query heads of a head of the cache: the tokens of all
+ * sequences are dealt out evenly over the work-groups, and the parts of a sequence joined in a
+ * second kernel (tables of up to 1024 tokens: neither).
  * workspace: scratch of qlin_kv_attention_workspace_bytes (or QLIN_ERR_WORKSPACE; 0
  * is returned there for invalid arguments); its first 65536 bytes are left as they
  * are, so that it may be the buffer of the other calls.  Calls that can run at the same time need
- * workspaces of their own.  heads <= 1024; |scale| <= 2^20.
+ * workspaces of their own.  heads <= 1024; |scale| <= 2^20; seqs * heads < 2^24.
  */
 int64_t qlin_kv_attention_workspace_bytes(const qlin_kv_cache* cache, const qlin_kv_seqs* seqs,
                                           int32_t heads);
