@@ -780,9 +780,9 @@ def main():
         out["achieved_peaks"] = peaks
     if "c1_gemv_latency" in res:
         out["c1_us_per_call"] = round(res["c1_gemv_latency"]["ms_median"] * 1e3 / C1_CALLS, 3)
-    # the per-stage detail last, after every summary key
-    out["phases"] = res
-    out["rooflines"] = rooflines
+    # the per-stage detail (18 KB) goes to stderr, so that the result's line stays short
+    print("[bench] detail " + json.dumps({"phases": res, "rooflines": rooflines}), file=sys.stderr,
+          flush=True)
     print(json.dumps(out), flush=True)
 
 
