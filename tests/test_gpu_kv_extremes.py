@@ -247,3 +247,33 @@ def test_weights_are_rounded_to_either_side():
     q = rng.standard_normal((seqs, heads, 64)).astype(np.float16)
     o = host(qlin.kv_attention(cache, dev(q), dev(table), dev(lengths), scale=0.1)[0]).astype(np.float64)
     assert abs((o.sum(-1) - 1).mean()) <= kr.U
+
+
+@pytest.mark.parametrize("vb", [4, 8, 16])
+@pytest.mark.parametrize("width", [6, 40])
+def test_values_and_scores_that_are_not_finite(vb, width):
+    """An infinite value shows in its own dims (its group's where it is quantized) and a score of
+    +inf in its own row; what is beside them keeps its bits, large values of the same token too."""
+    rng = np.random.default_rng(28)
+    n = 170
+    cache, ref = new_cache(rng, 6, 1, 128, 32, 16, vb)
+    table = new_table(rng, 1, 6, 6)
+    k, v = rng.uniform(0.5, 1, (n, 1, 128)), rng.uniform(-1, 1, (n, 1, 128))
+    v[20, 0, :64] *= 3e4
+    v[20, 0, 70] = np.inf
+    lengths = put(cache, ref, table, k, v, [n])
+    q = rng.uniform(-0.2, 0.2, (1, 4, 128)).astype(np.float16)
+    q[0, 2, 3] = np.inf
+    o, _, lse = qlin.kv_attention(cache, dev(q), dev(widened(table, width)), dev(lengths), scale=1.0,
+                                  want_lse=True)
+    o, lse = host(o), host(lse)
+    rows, bad = [0, 1, 3], np.arange(128) >= 64 if vb < 16 else np.arange(128) == 70
+    assert not np.isfinite(o[0, 2]).any() and not np.isfinite(o[0, rows][:, bad]).any()
+    # (the reference without the group that is not finite: its values as zeros)
+    clean = v.copy()
+    clean[20, 0, 64:] = 0
+    sub, sub_ref = new_cache(rng, 6, 1, 128, 32, 16, vb)
+    put(sub, sub_ref, table, k, clean, [n])
+    want, wl, eo, el = kr.attention(sub_ref, q[:, rows], table, lengths, 1.0, 0)
+    kr.check(o[:, rows][:, :, :64], want[:, :, :64], eo[:, :, :64], "O")
+    kr.check(lse[:, rows], wl, el, "lse")
