@@ -2,12 +2,16 @@
 //     S[p] = scale q . k_p,   P = exp(S - max),   O = sum P v_p / sum P,
 // in one pass over the cached tokens with running sums and a unit of them; k = s (code - z).
 //
-// What bounds it.  Every code is read once and takes part in 4 ratio operations, far below
-// what the matrix cores do, so that the bytes of the cache are the floor.  With 8 bits and more they
-// are reached (64 sequences of 8192 tokens, 8 heads of 128: 198 us for 1.13 GB, 5.7 TB/s).  With
-// 4 bits the unpacking is as long: a tile of 32 tokens and 128 dims takes 384 vector instructions
-// of a wave, 24 of them MFMAs (prologue and sums of the waves included): 24 us of issue in the 39 us
-// that 131071 tokens of 8 heads take (3.8 TB/s; its loads alone take 30, its arithmetic alone 36).
+// What bounds it.  Every code is read once for up to 16 query heads and takes part in 4 ratio
+// operations, far below what the matrix cores do, so that the bytes of the cache are the floor.  With 8
+// bits and more they are reached (64 sequences of 8192 tokens, 8 heads of 128: 196 us for 1.13 GB, 5.7
+// TB/s).  With 4 bits a tile of 32 tokens and 128 dims takes 383 vector instructions of a wave, 24 of
+// them MFMAs (prologue and sums of the waves included): 131071 tokens of 8 heads take 39 us (3.8
+// TB/s), 20 of them issue (at 2.4 GHz), 28 their bytes; a wave waits for its loads and results a third
+// of its cycles and for an issue slot another third, at three waves a SIMD.  A ragged batch (48
+// sequences of 1 to 4096 tokens, 28.8 us, 12 of issue, 15 of bytes) is bound by the starts of its 384
+// row blocks: about five tiles a wave, each start a page list, queries, a first tile and three
+// barriers with nothing in flight.
 //
 // Why this split.  One query head per sequence and head of the cache is no matrix product:
 // the heads that share a head of the cache (ratio, up to 16 at a time) are one MFMA operand, tokens
@@ -401,10 +405,13 @@ struct PageList {
 // two gain nothing: 128 dims of 16 bits 47.8 us : 48.2 with one, 256 dims of 8 bits 43.3 : 40.1, of
 // 16 bits 50.1 : 48.2 (48 sequences of 1 to 4096 tokens; the other waves' loads are enough there).
 constexpr bool attend_two(int d, int kb, int vb) { return d <= 128 && (kb + vb) * (d / 64) <= 32; }
-// Work-groups per CU that registers allow (four waves each, one per SIMD).  Small tiles three: 168
-// registers; two take 30.3 us for 27.8 (48 sequences, 128 dims, 4 bits), four with one tile 29.2;
-// 64 dims 12.2 (three) : 13.0 (four).  256 dims with up to 16 bits together two: 4 bits 28.8
-// for 37.3 with one, 8 bits 36.0 for 40.1 (more bits do not fit).
+// Work-groups per CU that the grid and the registers are sized for (four waves each, one per SIMD).
+// Small tiles three: 168 registers, 3 of them spilled (16 bytes of scratch a lane) with 128 dims of 4
+// bits; two take 30.3 us for 27.8 (48 sequences, 128 dims, 4 bits), four with one tile 29.2; 64 dims
+// 12.2 (three) : 13.0 (four).  256 dims with up to 16 bits together two: 4 bits 28.8 for 37.3 with one,
+// 8 bits 36.0 for 40.1 (13 registers spilled; more bits do not fit).  The others two, or one: 64
+// and 128 dims with a side of 16 bits have registers for one more, which is not measured.  Every
+// instance spills 17 to 35 scalar registers to lanes of vector ones.
 constexpr int attend_occupancy(int d, int kb, int vb) {
   return d == 256 ? (kb + vb <= 16 ? 2 : 1) : (kb + vb) * (d / 64) <= 16 ? 3 : 2;
 }

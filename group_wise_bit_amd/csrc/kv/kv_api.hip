@@ -124,6 +124,9 @@ struct Attend {
 // One sequence, 64 dims of 8 bits: 300 tokens 6.1 : 5.4, 1024 8.8 : 5.4, 2048 13.8 : 5.5; 128
 // dims of 4 bits: 512 9.6 : 6.7, 1024 13.3 : 8.0, 2048 20.3 : 6.8; 256 dims of 16 bits: 1024 20.4 :
 // 10.0.  48 ragged ones, 128 dims of 4 bits: up to 300 9.7 : 11.3, 1024 16.7 : 14.1, 2048 25.0 : 19.9.
+// So the limit is where 64 and 128 dims of up to 8 bits come out even, join and launch counted; wider
+// tiles do so at fewer tokens (256 dims of 16 bits at 1024 lose 5 us by it), and a short
+// sequence under a long table is split.
 constexpr int64_t kWholeTokens = 1024;
 
 struct AttendPlan {

@@ -6,8 +6,8 @@
 
 namespace qlin {
 
-// Work-groups of the attention: as many as the chip's 256 CUs hold at once, so that none
-// waits for another's end.
+// Work-groups of the attention: as many as the launch bounds let 256 CUs hold at once (or fewer),
+// so that none waits for another's end.
 inline int attend_groups(int d, int kb, int vb) {
   return 256 * attend_occupancy(d, kb, vb);
 }

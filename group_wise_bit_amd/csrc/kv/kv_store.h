@@ -3,7 +3,7 @@
 // Both are copies with a change of form: their floor is the bytes of the rows and of the
 // codes.  A wave takes a part of a tile whose codes are its own whole words in the layout: half of the
 // tokens of the keys, a group of 64 dims of the values.  Whole prompts (8 of 2048 tokens, 8 heads of
-// 128, keys of 8 bits, values of 4: 94 MB) are written in 26 us (3.6 TB/s) and read back in 17.6
+// 128, keys of 8 bits, values of 4: 94 MB) are written in 26 us (3.6 TB/s) and read back in 17.5
 // (5.3 TB/s, a large copy's rate); 16 prompts of up to 4096 tokens of 8 bits (162 MB) are read
 // back in 36 us (4.5 TB/s).  (One wave for all parts of a tile and head: slower, its loads wait
 // for each other.)  A few tokens take 5 us, a launch and three rounds of dependent loads: offsets
@@ -104,7 +104,9 @@ __device__ __forceinline__ int kv_page(const KvSeqs& s, const KvSpan& sp) {
   return page >= 0 && page < s.pages ? page : -1;
 }
 
-// Rounding is bound by vector instructions (prompts: 36 us before these forms, 26 with them):
+// Rounding takes most of its time in vector instructions (prompts: 36 us before these forms, 26 with
+// them, 16 of those issue at 2.4 GHz; the rest is that a wave loads, rounds and stores once, one
+// after the other: it waits half of its cycles):
 // ranges are taken on packed fp16 pairs, ties looked for in pairs, codes packed by the conversion
 // itself, and for values one lane forms the rounding of a token for the 16 that share it.
 //
